@@ -9,7 +9,9 @@
  *   f_i(x) = W_down^(i) ( SiLU(W_gate^(i) x) * W_up^(i) x )
  *
  * in three calls, in stream order:
- *   moe_route     router projection, top-k selection and normalised gates;
+ *   moe_route     router projection, top-k selection and normalised gates
+ *                 (or moe_route_scored: sigmoid or softmax scores, a bias for
+ *                 the choice, groups, scaled gates);
  *   moe_schedule  the dispatch schedule of Algorithm 1 (per-expert counts,
  *                 prefix sums, the position -> source-route table and its
  *                 inverse);
@@ -54,7 +56,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 8
+#define MOE_ABI_VERSION 9
 
 typedef enum {
   MOE_OK = 0,
@@ -180,6 +182,60 @@ moe_status moe_workspace_init(const moe_shape* shape, void* ws, size_t ws_bytes,
  */
 moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router, float* logits,
                      int32_t* topk_idx, float* topk_gate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Routing from scores.  With l the logits of a token (as in moe_route: from x,
+ * or given), s its scores and b the per-expert bias:
+ *   s_e = 1 / (1 + exp(-l_e))            MOE_SCORE_SIGMOID
+ *   s_e = exp(l_e) / sum_e' exp(l_e')    MOE_SCORE_SOFTMAX (over all experts)
+ *   c_e = s_e + b_e                      what the experts are chosen by
+ * The experts form `groups` groups of E_total / groups consecutive ones.  A
+ * group ranks by its largest c (MOE_GROUP_MAX) or by the sum of its two
+ * largest (MOE_GROUP_TOP2; a group of one expert by that one), and the
+ * kept_groups best stay, ties to the lower group.  Of their experts the k
+ * largest c are chosen, in falling order.  The gates are
+ *   g_s = scale * s_s / sum_s' s_s'      renorm = 1 (0 where the sum is 0)
+ *   g_s = scale * s_s                    renorm = 0
+ * The bias only chooses; it never enters a gate.  Scores are formed in 64
+ * bits, and two c are told apart down to 2^-42 of their value: closer ones tie,
+ * to the lower expert id.  A logit of -inf or NaN scores 0, and an expert whose
+ * c is -inf or NaN ranks below every other; a non-finite logit or bias sets
+ * MOE_DEVERR_NONFINITE.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+typedef struct {
+  int32_t score;       /* moe_score */
+  int32_t groups;      /* divides E_total; 1 .. 64 */
+  int32_t kept_groups; /* 1 .. groups; kept_groups * (E_total / groups) >= k */
+  int32_t group_score; /* moe_group_score */
+  int32_t renorm;      /* 0 or 1 */
+  float scale;         /* finite */
+} moe_router;
+
+/*   x, w_router, logits, topk_idx, topk_gate, ws: as in moe_route
+ *   bias  [E_total] fp32, or NULL for none */
+moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, const void* x, const void* w_router,
+                            const float* bias, float* logits, int32_t* topk_idx, float* topk_gate, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * The gradient of moe_route_scored's gates with respect to the logits, the
+ * choice of experts held fixed (the bias, which only chooses, has none).
+ *   logits    [T, E_total] fp32, as moe_route_scored left them
+ *   topk_idx  [T, k] int32: the chosen experts, different ones for one token
+ *   dgate     [T, k] fp32: the gradient of the gates
+ *   dlogits   [T, E_total] fp32 out, every entry written
+ * With W = sum_s s_s over the chosen:
+ *   dw_s = scale (dg_s - sum_s' dg_s' s_s' / W) / W    renorm = 1 (0 where W is 0)
+ *   dw_s = scale dg_s                                  renorm = 0
+ *   dl_e = s_e (1 - s_e) dw_e                          sigmoid (0 unless chosen)
+ *   dl_e = s_e (dw_e - sum_s s_s dw_s)                 softmax (dw_e = 0 unless chosen)
+ * A chosen id outside [0, E_total) sets MOE_DEVERR_EXPERT_RANGE and adds nothing.
+ */
+moe_status moe_route_backward(const moe_shape* shape, const moe_router* router, const float* logits,
+                              const int32_t* topk_idx, const float* dgate, float* dlogits, void* ws,
+                              size_t ws_bytes, void* stream);
 
 /*
  * Dispatch schedule (MoK paper §3.1, "Scheduling", and its Algorithm 1).
@@ -334,6 +390,18 @@ moe_status moe_backward(const moe_shape* shape, const moe_bwd_weights* bw, const
                         const float* topk_gate, const int32_t* expert_offsets, const int32_t* sched_src,
                         const int32_t* route_dst, const void* y_routes, const void* dout, const moe_grads* grads,
                         int32_t* dev_error, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_backward for a forward whose gates came from moe_route_scored: the
+ * logits' gradient follows `router` and the fp32 `logits` [T, E_total] of that
+ * call (dl is stored bf16 for the router's two products, as in moe_backward).
+ * Everything else is moe_backward's.
+ */
+moe_status moe_backward_scored(const moe_shape* shape, const moe_router* router, const moe_bwd_weights* bw,
+                               const void* x, const float* logits, const int32_t* topk_idx, const float* topk_gate,
+                               const int32_t* expert_offsets, const int32_t* sched_src, const int32_t* route_dst,
+                               const void* y_routes, const void* dout, const moe_grads* grads, int32_t* dev_error,
+                               void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Where moe_forward leaves the routed output rows inside the workspace (bf16,

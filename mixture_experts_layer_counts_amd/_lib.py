@@ -18,6 +18,8 @@ MOE_OK = 0
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_WORKSPACE",
           -4: "MOE_ERR_HIP"}
 MOE_BF16, MOE_MXFP8 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 DEVERR_EXPERT_RANGE, DEVERR_ROW_OVERFLOW, DEVERR_NONFINITE, DEVERR_PIPELINE = 0x1, 0x2, 0x4, 0x8
 KERNELS = {"router_gemm": 0, "topk": 1, "schedule": 2, "tiles": 3, "shared_up": 4, "shared_down": 5, "gather": 6,
            "up_gate": 7, "down": 8, "combine": 9, "pipeline": 10, "bwd_replay": 11, "bwd_dgrad": 12,
@@ -30,6 +32,11 @@ class MoeShape(ctypes.Structure):
         "tokens_per_src_rank", "max_rows", "minibatch_rows", "ring_rows")] + [
         ("precision", ctypes.c_int32), ("shared_precision", ctypes.c_int32), ("pipeline", ctypes.c_int32),
         ("mem_workgroups", ctypes.c_int32), ("weights_tiled", ctypes.c_int32)]
+
+
+class MoeRouter(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "kept_groups", "group_score", "renorm")] + [
+        ("scale", ctypes.c_float)]
 
 
 class MoeWeights(ctypes.Structure):
@@ -67,6 +74,10 @@ _SIGS = {
     "moe_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
     "moe_workspace_init": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.c_size_t, _P]),
     "moe_route": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_route_scored": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeRouter), _P, _P, _P, _P, _P, _P,
+                                        _P, ctypes.c_size_t, _P]),
+    "moe_route_backward": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeRouter), _P, _P, _P, _P, _P,
+                                          ctypes.c_size_t, _P]),
     "moe_schedule": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_schedule_static": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, _P]),
     "moe_forward": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights), _P, _P, _P, _P, _P, _P,
@@ -83,6 +94,9 @@ _SIGS = {
     "moe_backward_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
     "moe_backward": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeBwdWeights), _P, _P, _P, _P, _P, _P,
                                     _P, _P, ctypes.POINTER(MoeGrads), _P, _P, ctypes.c_size_t, _P]),
+    "moe_backward_scored": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeRouter),
+                                           ctypes.POINTER(MoeBwdWeights), _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                           ctypes.POINTER(MoeGrads), _P, _P, ctypes.c_size_t, _P]),
     "moe_probe_begin": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32]),
     "moe_probe_end": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32)]),
     "moe_stream_probe": (ctypes.c_int, [ctypes.POINTER(MoeStreamProbeArgs), _P]),

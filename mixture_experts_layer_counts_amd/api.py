@@ -62,6 +62,23 @@ def shape_for(T: int, D: int, I: int, E: int, k: int, I_shared: Optional[int] = 
     return s
 
 
+def router_for(score: str = "sigmoid", groups: int = 1, kept_groups: int = 1, group_score: str = "top2",
+               renorm: bool = True, scale: float = 1.0) -> _lib.MoeRouter:
+    """A moe_router: how ``route`` scores and chooses experts (moe_route_scored).
+    ``score`` is "sigmoid" or "softmax"; of ``groups`` groups of consecutive
+    experts the ``kept_groups`` best stay, ranked by their largest value
+    (``group_score`` "max") or the sum of their two largest ("top2");
+    ``renorm`` divides the gates by their sum, ``scale`` multiplies them."""
+    if score not in _lib.SCORES:
+        raise ValueError(f"score must be one of {sorted(_lib.SCORES)}, got {score!r}")
+    if group_score not in _lib.GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(_lib.GROUP_SCORES)}, got {group_score!r}")
+    r = _lib.MoeRouter()
+    r.score, r.groups, r.kept_groups = _lib.SCORES[score], groups, kept_groups
+    r.group_score, r.renorm, r.scale = _lib.GROUP_SCORES[group_score], int(bool(renorm)), scale
+    return r
+
+
 class MoELayer:
     """One layer's shape plus its device workspace, on ``device``."""
 
@@ -90,8 +107,17 @@ class MoELayer:
 
     # -- moe_route ---------------------------------------------------------
     def route(self, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor],
-              logits: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+              logits: Optional[torch.Tensor] = None, router: Optional[_lib.MoeRouter] = None,
+              bias: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """(logits, idx, gate).  Without ``router``: top-k of the logits with
+        renormalised softmax gates (moe_route).  With one (``router_for``):
+        moe_route_scored, with ``bias`` [E] fp32 added to the scores for the
+        choice alone."""
         s, dev = self.shape, self.device
+        if bias is not None:
+            if router is None:
+                raise ValueError("a bias needs a router")
+            _need(bias, "bias", torch.float32, (s.E_total,), dev)
         if x is None:
             if logits is None:
                 raise ValueError("given-logits mode needs logits")
@@ -102,9 +128,29 @@ class MoELayer:
             logits = torch.empty((s.T, s.E_total), dtype=torch.float32, device=dev)
         idx = torch.empty((s.T, s.k), dtype=torch.int32, device=dev)
         gate = torch.empty((s.T, s.k), dtype=torch.float32, device=dev)
-        _lib.check("moe_route", self.lib.moe_route(ctypes.byref(s), _ptr(x), _ptr(w_router), _ptr(logits),
-                                                   _ptr(idx), _ptr(gate), _ptr(self.ws), self.ws_bytes, _stream()))
+        if router is None:
+            _lib.check("moe_route", self.lib.moe_route(ctypes.byref(s), _ptr(x), _ptr(w_router), _ptr(logits),
+                                                       _ptr(idx), _ptr(gate), _ptr(self.ws), self.ws_bytes,
+                                                       _stream()))
+        else:
+            _lib.check("moe_route_scored", self.lib.moe_route_scored(
+                ctypes.byref(s), ctypes.byref(router), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(logits), _ptr(idx),
+                _ptr(gate), _ptr(self.ws), self.ws_bytes, _stream()))
         return logits, idx, gate
+
+    def route_backward(self, logits: torch.Tensor, idx: torch.Tensor, dgate: torch.Tensor,
+                       router: _lib.MoeRouter) -> torch.Tensor:
+        """The gradient [T, E] fp32 of the logits for a gradient ``dgate`` of
+        the gates that ``route`` returned with ``router`` (moe_route_backward)."""
+        s, dev = self.shape, self.device
+        _need(logits, "logits", torch.float32, (s.T, s.E_total), dev)
+        _need(idx, "idx", torch.int32, (s.T, s.k), dev)
+        _need(dgate, "dgate", torch.float32, (s.T, s.k), dev)
+        dlogits = torch.empty((s.T, s.E_total), dtype=torch.float32, device=dev)
+        _lib.check("moe_route_backward", self.lib.moe_route_backward(
+            ctypes.byref(s), ctypes.byref(router), _ptr(logits), _ptr(idx), _ptr(dgate), _ptr(dlogits),
+            _ptr(self.ws), self.ws_bytes, _stream()))
+        return dlogits
 
     # -- moe_schedule ------------------------------------------------------
     def schedule(self, routes: torch.Tensor) -> Dict[str, torch.Tensor]:
@@ -174,9 +220,10 @@ class MoELayer:
 
     # -- whole layer -------------------------------------------------------
     def __call__(self, x: torch.Tensor, w_router: Optional[torch.Tensor], weights: Dict[str, torch.Tensor],
-                 logits: Optional[torch.Tensor] = None):
+                 logits: Optional[torch.Tensor] = None, router: Optional[_lib.MoeRouter] = None,
+                 bias: Optional[torch.Tensor] = None):
         """route + schedule + forward for R = 1 (from x, or from given logits)."""
-        lg, idx, gate = self.route(None if logits is not None else x, w_router, logits)
+        lg, idx, gate = self.route(None if logits is not None else x, w_router, logits, router, bias)
         sched = self.schedule(idx)
         out, out32 = self.forward(weights, x, x, gate, sched)
         return {"logits": lg, "idx": idx, "gate": gate, "out": out, "out32": out32, **sched}
@@ -267,8 +314,15 @@ class MoEBackward:
 
     def __call__(self, bw: Dict[str, torch.Tensor], x: torch.Tensor, idx: torch.Tensor, gate: torch.Tensor,
                  sched: Dict[str, torch.Tensor], y_routes: torch.Tensor, dout: torch.Tensor,
-                 grads: Optional[Dict[str, torch.Tensor]] = None) -> Dict[str, torch.Tensor]:
+                 grads: Optional[Dict[str, torch.Tensor]] = None, router: Optional[_lib.MoeRouter] = None,
+                 logits: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+        """The gradients of one forward.  ``router`` and ``logits``: those of
+        its ``route`` call, when that had a router (moe_backward_scored)."""
         s, dev = self.shape, self.device
+        if (router is None) != (logits is None):
+            raise ValueError("router and logits come together")
+        if logits is not None:
+            _need(logits, "logits", torch.float32, (s.T, s.E_total), dev)
         T, D, I, Is, E, k, L = s.T, s.D, s.I, s.I_shared, s.E_total, s.k, s.experts_per_rank
         _need(x, "x", torch.bfloat16, (T, D), dev)
         _need(dout, "dout", torch.bfloat16, (T, D), dev)
@@ -285,10 +339,13 @@ class MoEBackward:
             _need(grads[n], n, dt, shp, dev)
         g = _lib.MoeGrads(*[_ptr(grads[n]) for n, _ in _lib.MoeGrads._fields_])
         b = _lib.MoeBwdWeights(*[_ptr(bw[n]) for n, _ in _lib.MoeBwdWeights._fields_])
-        _lib.check("moe_backward", self.lib.moe_backward(
-            ctypes.byref(s), ctypes.byref(b), _ptr(x), _ptr(idx), _ptr(gate), _ptr(sched["offsets"]),
-            _ptr(sched["sched"]), _ptr(sched["route_dst"]), _ptr(y_routes), _ptr(dout), ctypes.byref(g),
-            _ptr(self.err), _ptr(self.ws), self.ws_bytes, _stream()))
+        rest = (_ptr(idx), _ptr(gate), _ptr(sched["offsets"]), _ptr(sched["sched"]), _ptr(sched["route_dst"]),
+                _ptr(y_routes), _ptr(dout), ctypes.byref(g), _ptr(self.err), _ptr(self.ws), self.ws_bytes, _stream())
+        if router is None:
+            _lib.check("moe_backward", self.lib.moe_backward(ctypes.byref(s), ctypes.byref(b), _ptr(x), *rest))
+        else:
+            _lib.check("moe_backward_scored", self.lib.moe_backward_scored(
+                ctypes.byref(s), ctypes.byref(router), ctypes.byref(b), _ptr(x), _ptr(logits), *rest))
         return grads
 
     def device_error(self) -> int:

@@ -22,6 +22,24 @@ constexpr int kMaxRouterParts = 4;
 hipError_t launch_topk_gate(const float* planes, int parts, int64_t part_stride, float* logits, int T, int E, int k,
                             int32_t* idx, float* gate, int* err, hipStream_t stream);
 
+// Routing from scores (moe_router in include/moe.h).
+struct RouterArgs {
+  bool sigmoid;  // else softmax
+  int groups, kept_groups;
+  bool top2;  // groups rank by their two largest, else by their largest
+  bool renorm;
+  float scale;
+};
+constexpr int kMaxGroups = 64;
+// planes, parts, part_stride, logits, idx, gate, err: as launch_topk_gate
+hipError_t launch_route_scored(const RouterArgs& r, const float* planes, int parts, int64_t part_stride,
+                               const float* bias, float* logits, int T, int E, int k, int32_t* idx, float* gate,
+                               int* err, hipStream_t stream);
+// dlogits into out32 [T][E] (ld == E), or as bf16 into out16 [T][ld] with zeros past E (out32 NULL)
+hipError_t launch_route_backward(const RouterArgs& r, const float* logits, const int32_t* idx, const float* dgate,
+                                 int T, int E, int k, float* out32, uint16_t* out16, int ld, int* err,
+                                 hipStream_t stream);
+
 hipError_t launch_schedule(const int32_t* routes, int R, int NK, int c, int L, int E_total, int64_t max_rows,
                            int32_t* counts, int32_t* offsets, int32_t* sched_src, int32_t* route_dst,
                            const SchedScratch& s, int* err, hipStream_t stream);

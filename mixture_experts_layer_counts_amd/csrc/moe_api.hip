@@ -2,6 +2,7 @@
 // launch sequence of the MoE-layer forward.  See include/moe.h for the contract.
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -316,6 +317,52 @@ hipError_t shared_expert_mx(const moe_shape* shape, const moe_weights* w, const 
   return moe::launch_gemm_mx(d, moe::kEpiF32, s);
 }
 
+// logits = x W_r^T, or with several K ranges its partial planes in the workspace.
+hipError_t router_gemm(const moe_shape* shape, const void* x, const void* w_router, float* logits, const Layout& L,
+                       void* ws, hipStream_t s) {
+  const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total);
+  moe::GemmArgs g{};
+  g.k_splits = 1;
+  g.A = static_cast<const uint16_t*>(x);
+  g.a_bytes = shape->T * shape->D * 2;
+  g.lda = shape->D;
+  g.a_sub = 0;
+  g.a_mod = INT64_MAX;
+  g.B0 = static_cast<const uint16_t*>(w_router);
+  g.B1 = nullptr;
+  g.b_expert_stride = 0;
+  g.N = E;
+  g.K = static_cast<int>(shape->D);
+  g.C = L.router_splits > 1 ? static_cast<void*>(at<float>(ws, L.router_parts)) : static_cast<void*>(logits);
+  g.ldc = E;
+  g.k_splits = L.router_splits;
+  g.c_split_stride = static_cast<int64_t>(T) * E;
+  g.c_idx = nullptr;
+  g.c_sub = 0;
+  g.tiles = nullptr;
+  g.tile_count = nullptr;
+  g.dense_rows = T;
+  ProbeScope probe(MOE_K_ROUTER_GEMM, s);
+  return moe::launch_gemm(g, moe::kEpiF32, s);
+}
+
+// A router that valid_shape's bounds on E_total and k allow.
+bool valid_router(const moe_shape* s, const moe_router* r) {
+  if (!r) return false;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return false;
+  if (r->group_score != MOE_GROUP_MAX && r->group_score != MOE_GROUP_TOP2) return false;
+  if (r->renorm != 0 && r->renorm != 1) return false;
+  if (r->groups < 1 || r->groups > moe::kMaxGroups || s->E_total % r->groups) return false;
+  if (r->kept_groups < 1 || r->kept_groups > r->groups) return false;
+  if (r->kept_groups * (s->E_total / r->groups) < s->k) return false;
+  return std::isfinite(r->scale);
+}
+
+moe::RouterArgs router_args(const moe_router* r) {
+  return moe::RouterArgs{r->score == MOE_SCORE_SIGMOID, r->groups, r->kept_groups, r->group_score == MOE_GROUP_TOP2,
+                         r->renorm != 0, r->scale};
+}
+
 // One minibatch of the routed experts in MXFP8 (MoK paper §3.4 "MXFP8
 // Support"): the gather quantises x along D into the ring, the up/gate GEMM
 // quantises h along I in its epilogue, the down GEMM writes bf16 rows.
@@ -440,36 +487,45 @@ moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
   if (T == 0) return MOE_OK;
-  if (x) {
-    moe::GemmArgs g{};
-    g.k_splits = 1;
-    g.A = static_cast<const uint16_t*>(x);
-    g.a_bytes = shape->T * shape->D * 2;
-    g.lda = shape->D;
-    g.a_sub = 0;
-    g.a_mod = INT64_MAX;
-    g.B0 = static_cast<const uint16_t*>(w_router);
-    g.B1 = nullptr;
-    g.b_expert_stride = 0;
-    g.N = E;
-    g.K = static_cast<int>(shape->D);
-    g.C = L.router_splits > 1 ? static_cast<void*>(at<float>(ws, L.router_parts)) : static_cast<void*>(logits);
-    g.ldc = E;
-    g.k_splits = L.router_splits;
-    g.c_split_stride = static_cast<int64_t>(T) * E;
-    g.c_idx = nullptr;
-    g.c_sub = 0;
-    g.tiles = nullptr;
-    g.tile_count = nullptr;
-    g.dense_rows = T;
-    ProbeScope probe(MOE_K_ROUTER_GEMM, s);
-    MOE_TRY_HIP(moe::launch_gemm(g, moe::kEpiF32, s));
-  }
+  if (x) MOE_TRY_HIP(router_gemm(shape, x, w_router, logits, L, ws, s));
   ProbeScope probe(MOE_K_TOPK, s);
   const bool parts = x && L.router_splits > 1;
   return hip_status(moe::launch_topk_gate(parts ? at<float>(ws, L.router_parts) : logits,
                                           parts ? L.router_splits : 1, static_cast<int64_t>(T) * E, logits, T, E, k,
                                           topk_idx, topk_gate, at<int>(ws, L.err), s));
+}
+
+moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, const void* x, const void* w_router,
+                            const float* bias, float* logits, int32_t* topk_idx, float* topk_gate, void* ws,
+                            size_t ws_bytes, void* stream) {
+  Layout L;
+  const moe_status st = check_ws(shape, ws, ws_bytes, &L);
+  if (st != MOE_OK) return st;
+  if (!valid_router(shape, router)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !topk_gate || (x && !w_router)) return MOE_ERR_INVALID_ARG;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
+  if (T == 0) return MOE_OK;
+  if (x) MOE_TRY_HIP(router_gemm(shape, x, w_router, logits, L, ws, s));
+  ProbeScope probe(MOE_K_TOPK, s);
+  const bool parts = x && L.router_splits > 1;
+  return hip_status(moe::launch_route_scored(router_args(router), parts ? at<float>(ws, L.router_parts) : logits,
+                                             parts ? L.router_splits : 1, static_cast<int64_t>(T) * E, bias, logits, T,
+                                             E, k, topk_idx, topk_gate, at<int>(ws, L.err), s));
+}
+
+moe_status moe_route_backward(const moe_shape* shape, const moe_router* router, const float* logits,
+                              const int32_t* topk_idx, const float* dgate, float* dlogits, void* ws,
+                              size_t ws_bytes, void* stream) {
+  Layout L;
+  const moe_status st = check_ws(shape, ws, ws_bytes, &L);
+  if (st != MOE_OK) return st;
+  if (!valid_router(shape, router)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !dgate || !dlogits) return MOE_ERR_INVALID_ARG;
+  const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
+  if (T == 0) return MOE_OK;
+  return hip_status(moe::launch_route_backward(router_args(router), logits, topk_idx, dgate, T, E, k, dlogits, nullptr,
+                                               E, at<int>(ws, L.err), static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_schedule(const moe_shape* shape, const int32_t* routes, int32_t* expert_counts,
@@ -988,10 +1044,12 @@ moe_status moe_backward_prepare(const moe_shape* shape, const moe_weights* w, co
   return MOE_OK;
 }
 
-moe_status moe_backward(const moe_shape* shape, const moe_bwd_weights* bw, const void* x, const int32_t* topk_idx,
-                        const float* topk_gate, const int32_t* expert_offsets, const int32_t* sched_src,
-                        const int32_t* route_dst, const void* y_routes, const void* dout, const moe_grads* g,
-                        int32_t* dev_error, void* ws, size_t ws_bytes, void* stream) {
+// `router` NULL: the gates are moe_route's (renormalised softmax; `logits` unused).
+static moe_status backward_impl(const moe_shape* shape, const moe_router* router, const moe_bwd_weights* bw,
+                                const void* x, const float* logits, const int32_t* topk_idx, const float* topk_gate,
+                                const int32_t* expert_offsets, const int32_t* sched_src, const int32_t* route_dst,
+                                const void* y_routes, const void* dout, const moe_grads* g, int32_t* dev_error,
+                                void* ws, size_t ws_bytes, void* stream) {
   moe_status why;
   if (!valid_bwd_shape(shape, &why)) return why;
   const BwdLayout L = bwd_layout_of(shape);
@@ -1142,7 +1200,11 @@ moe_status moe_backward(const moe_shape* shape, const moe_bwd_weights* bw, const
   uint16_t* dlT = at<uint16_t>(ws, L.dlT);
   float* dx_r = at<float>(ws, L.dx_r);
   MOE_TRY_HIP(moe::launch_route_grad(dob, static_cast<const uint16_t*>(y_routes), P, D, k, dg, s));
-  MOE_TRY_HIP(moe::launch_gate_grad(topk_gate, dg, topk_idx, T, E, static_cast<int>(Ep), k, dl, s));
+  if (router)
+    MOE_TRY_HIP(moe::launch_route_backward(router_args(router), logits, topk_idx, dg, T, E, k, nullptr, dl,
+                                           static_cast<int>(Ep), dev_error, s));
+  else
+    MOE_TRY_HIP(moe::launch_gate_grad(topk_gate, dg, topk_idx, T, E, static_cast<int>(Ep), k, dl, s));
   MOE_TRY_HIP(moe::launch_gemm(dense_args(dl, Ep, T, bw->w_router_t, 0, D, static_cast<int>(Ep), dx_r, D),
                                moe::kEpiF32, s));
   MOE_TRY_HIP(moe::launch_seg_transpose(dl, Ep, static_cast<int>(Ep), seg_off, seg_pad, 1, Tpad, dlT, Tpad, s, true));
@@ -1150,6 +1212,26 @@ moe_status moe_backward(const moe_shape* shape, const moe_bwd_weights* bw, const
 
   // ---- dx, in a fixed order ----
   return hip_status(moe::launch_dx_assemble(dx_s, dx_r, dx_ring, route_dst, T, D, k, P, g->dx, dev_error, s));
+}
+
+moe_status moe_backward(const moe_shape* shape, const moe_bwd_weights* bw, const void* x, const int32_t* topk_idx,
+                        const float* topk_gate, const int32_t* expert_offsets, const int32_t* sched_src,
+                        const int32_t* route_dst, const void* y_routes, const void* dout, const moe_grads* g,
+                        int32_t* dev_error, void* ws, size_t ws_bytes, void* stream) {
+  return backward_impl(shape, nullptr, bw, x, nullptr, topk_idx, topk_gate, expert_offsets, sched_src, route_dst,
+                       y_routes, dout, g, dev_error, ws, ws_bytes, stream);
+}
+
+moe_status moe_backward_scored(const moe_shape* shape, const moe_router* router, const moe_bwd_weights* bw,
+                               const void* x, const float* logits, const int32_t* topk_idx, const float* topk_gate,
+                               const int32_t* expert_offsets, const int32_t* sched_src, const int32_t* route_dst,
+                               const void* y_routes, const void* dout, const moe_grads* g, int32_t* dev_error,
+                               void* ws, size_t ws_bytes, void* stream) {
+  moe_status why;
+  if (!valid_bwd_shape(shape, &why)) return why;
+  if (!valid_router(shape, router) || !logits) return MOE_ERR_INVALID_ARG;
+  return backward_impl(shape, router, bw, x, logits, topk_idx, topk_gate, expert_offsets, sched_src, route_dst,
+                       y_routes, dout, g, dev_error, ws, ws_bytes, stream);
 }
 
 }  // extern "C"
