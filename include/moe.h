@@ -35,7 +35,7 @@
  *     launch; violations return MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED.
  *     Every GEMM operand must stay below 2^31 bytes (x: T*D*2; the ring:
  *     C*D*e; h: b*I*e; the shared h: T*I_shared*e; one routed or the shared
- *     weight matrix: I*D*e, I_shared*D*e; e = 2 in bf16, 1 in MXFP8);
+ *     weight matrix: I*D*e, I_shared*D*e; e = 2 in bf16, 1 in MXFP8 and int8);
  *     larger shapes return MOE_ERR_UNSUPPORTED.
  *   - Data errors found on the device (an expert id out of range, more routed
  *     rows than `max_rows`, a non-finite router logit) set bits of a sticky
@@ -66,9 +66,11 @@ typedef enum {
   MOE_ERR_HIP = -4          /* a HIP launch or runtime call failed */
 } moe_status;
 
-/* Arithmetic of the routed experts (MoK paper §3.4, "MXFP8 Support": the shared
- * expert always stays bf16). */
-typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1 } moe_precision;
+/* Arithmetic of the experts.  MOE_MXFP8: MoK paper §3.4, "MXFP8 Support" (there
+ * the shared expert always stays bf16).  MOE_INT8: 8-bit integers with one
+ * fp32 scale per token (activation row) and one per output channel (weight
+ * row), exact int32 sums; see moe_quantize_int8. */
+typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_INT8 = 2 } moe_precision;
 
 /* Device error bits, OR-ed into the workspace's sticky error word. */
 #define MOE_DEVERR_EXPERT_RANGE 0x1 /* a route names an expert outside [0, E_total) */
@@ -102,8 +104,8 @@ typedef struct {
   int32_t precision;           /* moe_precision of the routed experts */
   int32_t shared_precision;    /* moe_precision of the shared expert: MOE_BF16, as
                                   the MoK paper keeps it (§3.4, "MXFP8 Support"),
-                                  or MOE_MXFP8 as an option (D and I_shared then
-                                  multiples of 128) */
+                                  or MOE_MXFP8 or MOE_INT8 as an option (D and
+                                  I_shared then multiples of 128) */
   int32_t pipeline;            /* 0: the routed minibatch loop as stream-ordered
                                   launches (gather, up/gate, down per minibatch);
                                   1: as one persistent kernel whose workgroups
@@ -129,7 +131,8 @@ typedef struct {
                                   holding all N rows), or its E4M3 bytes as
                                   [K/128, N, 128] in MXFP8 (moe_tile_bf16 on
                                   the bytes taken as 2-byte units; the scales
-                                  stay as described under moe_weights), so
+                                  stay as described under moe_weights), int8
+                                  bytes in MOE_INT8 the same, so
                                   that one K stage of the expert GEMMs reads
                                   one contiguous plane.  Values and results
                                   are the same either way */
@@ -148,7 +151,13 @@ typedef struct {
  *           (E8M0, shared_precision MOE_MXFP8 only, else NULL): stage-major
  *           scales, as moe_mxfp8_pack_scales writes them with groups = 1
  * In MXFP8 the activations follow the weights: x (routed: in the gather;
- * shared: in its own pass) and h are quantised along their K axis. */
+ * shared: in its own pass) and h are quantised along their K axis.
+ * In MOE_INT8 (routed: D and I multiples of 128) the weights are int8 in the
+ * e4m3 layouts (plain bytes, or K-tiled), and the s_* (ss_*) pointers hold fp32
+ * scales, one per weight row: s_gate, s_up [L, I], s_down [L, D]; ss_gate,
+ * ss_up [I_shared], ss_down [D].  x is quantised per token, and h = SiLU(gate) *
+ * up, held in fp32 until its whole row is known, per routed row (shared: per
+ * token).  Weight pointers are 16-byte aligned. */
 typedef struct {
   const void *w_gate, *w_up, *w_down;
   const uint8_t *s_gate, *s_up, *s_down;
@@ -449,6 +458,30 @@ moe_status moe_quantize_mxfp8(const void* src, int64_t rows, int64_t K, uint8_t*
  */
 moe_status moe_mxfp8_pack_scales(const uint8_t* scale, int64_t groups, int64_t rows, int64_t K, uint8_t* packed,
                                  void* stream);
+
+/*
+ * 8-bit integer rows (MOE_INT8's form of activations and weights).  src
+ * [rows, K] bf16 or fp32 -> q [rows, Kp] int8 with Kp = K rounded up to 128
+ * (zeros past K), and scale [rows] fp32: with m = max |v| of the row,
+ *   scale = m / 127,  q = round(127 v / m), ties to even, in [-127, 127].
+ * A row of zeros has scale 0; a row that holds an infinity or a NaN has q = 0
+ * and scale NaN (its products are NaN).  q 16-byte aligned; src aligned to its
+ * element.  One launch on `stream`.
+ */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 } moe_dtype;
+moe_status moe_quantize_int8(const void* src, int32_t src_dtype, int64_t rows, int64_t K, int8_t* q, float* scale,
+                             void* stream);
+
+/*
+ * out [M, N] (bf16 or fp32) = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k], with
+ * exact int32 sums: a [M, K] and b [N, K] int8 as moe_quantize_int8 writes them
+ * (K its Kp: a multiple of 128, at most 65536), scales fp32.  Each value is the
+ * sum rounded to fp32, times a_scale, times b_scale, and for bf16 rounded once
+ * more.  a, b and out 16-byte aligned (MOE_ERR_INVALID_ARG); M*K and N*K below
+ * 2^31 (MOE_ERR_UNSUPPORTED).  Launches on `stream` only.
+ */
+moe_status moe_matmul_int8(const int8_t* a, const float* a_scale, int64_t M, const int8_t* b, const float* b_scale,
+                           int64_t N, int64_t K, void* out, int32_t out_dtype, void* stream);
 
 /* Read the sticky device error word (MOE_DEVERR_* bits).  SYNCHRONISES the
  * stream: diagnostics only, never on the hot path. */

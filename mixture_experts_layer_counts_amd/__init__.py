@@ -5,5 +5,5 @@ into the C calls moe_route, moe_schedule and moe_forward; every step of the
 layer runs in the library's kernels.
 """
 
-from .api import (MoEBackward, MoELayer, pack_mxfp8_scales, prepare_backward, quantize_mxfp8, router_for,  # noqa: F401
-                  shape_for, tile_bf16, tile_mxfp8)
+from .api import (MoEBackward, MoELayer, linear_int8, matmul_int8, pack_mxfp8_scales, prepare_backward,  # noqa: F401
+                  quantize_int8, quantize_mxfp8, router_for, shape_for, tile_bf16, tile_int8, tile_mxfp8)

@@ -43,10 +43,11 @@ def shape_for(T: int, D: int, I: int, E: int, k: int, I_shared: Optional[int] = 
               weights_tiled: bool = False) -> _lib.MoeShape:
     """A moe_shape for one GPU (R = 1) or for rank ``rank`` of R source ranks.
     ``precision`` is that of the routed experts, ``shared_precision`` that of
-    the shared expert (bf16 unless MXFP8 is asked for).  ``pipeline`` runs the
+    the shared expert (bf16 unless MXFP8 or int8 is asked for).  ``pipeline`` runs the
     routed minibatch loop as one persistent kernel, ``mem_workgroups`` of
     whose workgroups gather the minibatches the ring does not hold at once.
-    ``weights_tiled``: the routed bf16 weights come K-tiled (``tile_bf16``)."""
+    ``weights_tiled``: the routed weights come K-tiled (``tile_bf16``,
+    ``tile_mxfp8``, ``tile_int8``)."""
     L = E // R
     max_rows = T * k if max_rows is None else max_rows
     b = minibatch_rows or max(max_rows, 1)
@@ -55,8 +56,8 @@ def shape_for(T: int, D: int, I: int, E: int, k: int, I_shared: Optional[int] = 
     s.T, s.D, s.I, s.I_shared, s.E_total, s.k = T, D, I, I if I_shared is None else I_shared, E, k
     s.num_src_ranks, s.rank, s.experts_per_rank, s.tokens_per_src_rank = R, rank, L, T
     s.max_rows, s.minibatch_rows, s.ring_rows = max_rows, b, C
-    s.precision = {"bf16": _lib.MOE_BF16, "mxfp8": _lib.MOE_MXFP8}[precision]
-    s.shared_precision = {"bf16": _lib.MOE_BF16, "mxfp8": _lib.MOE_MXFP8}[shared_precision]
+    s.precision = _lib.PRECISIONS[precision]
+    s.shared_precision = _lib.PRECISIONS[shared_precision]
     s.pipeline, s.mem_workgroups = int(bool(pipeline)), mem_workgroups
     s.weights_tiled = int(bool(weights_tiled))
     return s
@@ -185,6 +186,15 @@ class MoELayer:
                 # row-major [L, N, K], or K-tiled [L, K/64, N, 64] (tile_bf16)
                 _need(weights[n], n, torch.bfloat16, (L, K // 64, N, 64) if s.weights_tiled else (L, N, K), dev)
                 setattr(w, n, _ptr(weights[n]))
+        elif s.precision == _lib.MOE_INT8:
+            for n, qn, sn, shp in (("w_gate", "q_gate", "s_gate", (L, I, D)), ("w_up", "q_up", "s_up", (L, I, D)),
+                                   ("w_down", "q_down", "s_down", (L, D, I))):
+                # row-major [L, N, K], or K-tiled [L, K/128, N, 128] (tile_int8); scales [L, N]
+                _need(weights[qn], qn, torch.int8,
+                      (L, shp[2] // 128, shp[1], 128) if s.weights_tiled else shp, dev)
+                _need(weights[sn], sn, torch.float32, shp[:2], dev)
+                setattr(w, n, _ptr(weights[qn]))
+                setattr(w, sn, _ptr(weights[sn]))
         else:
             for n, qn, sn, shp in (("w_gate", "q_gate", "s_gate", (L, I, D)), ("w_up", "q_up", "s_up", (L, I, D)),
                                    ("w_down", "q_down", "s_down", (L, D, I))):
@@ -198,6 +208,13 @@ class MoELayer:
             for n, shp in (("ws_gate", (Is, D)), ("ws_up", (Is, D)), ("ws_down", (D, Is))):
                 _need(weights[n], n, torch.bfloat16, shp, dev)
                 setattr(w, n, _ptr(weights[n]))
+        elif s.shared_precision == _lib.MOE_INT8:  # int8 "qs_*" and row scales "ss_*" (quantize_int8)
+            for n, qn, sn, shp in (("ws_gate", "qs_gate", "ss_gate", (Is, D)), ("ws_up", "qs_up", "ss_up", (Is, D)),
+                                   ("ws_down", "qs_down", "ss_down", (D, Is))):
+                _need(weights[qn], qn, torch.int8, shp, dev)
+                _need(weights[sn], sn, torch.float32, shp[:1], dev)
+                setattr(w, n, _ptr(weights[qn]))
+                setattr(w, sn, _ptr(weights[sn]))
         else:  # E4M3 bytes "qs_*" and packed scales "ss_*" (quantize_mxfp8, pack_mxfp8_scales)
             for n, qn, sn, shp in (("ws_gate", "qs_gate", "ss_gate", (Is, D)), ("ws_up", "qs_up", "ss_up", (Is, D)),
                                    ("ws_down", "qs_down", "ss_down", (D, Is))):
@@ -403,3 +420,78 @@ def pack_mxfp8_scales(scale: torch.Tensor) -> torch.Tensor:
     _lib.check("moe_mxfp8_pack_scales", lib.moe_mxfp8_pack_scales(_ptr(scale), G, N, KS * 32, _ptr(packed),
                                                                   _stream()))
     return packed
+
+
+_INT8_DTYPES = {torch.bfloat16: _lib.DT_BF16, torch.float32: _lib.DT_F32}
+
+
+def _need_int8_source(t: torch.Tensor, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in _INT8_DTYPES or not t.is_contiguous() or t.device.type != "cuda" or t.dim() < 1:
+        raise ValueError(f"{name} must be a contiguous bf16 or fp32 device tensor")
+    if t.shape[-1] < 1:
+        raise ValueError(f"{name} must have at least one column")
+
+
+def quantize_int8(src: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of a bf16 or fp32 tensor [..., K] -> (q [..., Kp] int8, scale [...]
+    fp32), Kp = K rounded up to 128 (zeros past K): moe_quantize_int8."""
+    lib = _lib.load()
+    _need_int8_source(src, "src")
+    K = src.shape[-1]
+    rows = src.numel() // K
+    with torch.cuda.device(src.device):
+        q = torch.empty(src.shape[:-1] + ((K + 127) // 128 * 128,), dtype=torch.int8, device=src.device)
+        scale = torch.empty(src.shape[:-1], dtype=torch.float32, device=src.device)
+        _lib.check("moe_quantize_int8", lib.moe_quantize_int8(_ptr(src), _INT8_DTYPES[src.dtype], rows, K, _ptr(q),
+                                                              _ptr(scale), _stream()))
+    return q, scale
+
+
+def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """[M, N] = (a b^T) * a_scale[:, None] * b_scale[None, :] of int8 rows a
+    [M, Kp], b [N, Kp] as ``quantize_int8`` returns them (moe_matmul_int8)."""
+    lib = _lib.load()
+    for t, n in ((a, "a"), (b, "b")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a tensor")
+        if t.dim() != 2 or t.device.type != "cuda":
+            raise ValueError(f"{n} must be a 2-d device tensor")
+    (M, K), dev = a.shape, a.device
+    _need(a, "a", torch.int8, (M, K), dev)
+    _need(a_scale, "a_scale", torch.float32, (M,), dev)
+    _need(b, "b", torch.int8, (b.shape[0], K), dev)
+    _need(b_scale, "b_scale", torch.float32, (b.shape[0],), dev)
+    if out_dtype not in _INT8_DTYPES:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    with torch.cuda.device(dev):
+        out = torch.empty((M, b.shape[0]), dtype=out_dtype, device=dev)
+        _lib.check("moe_matmul_int8", lib.moe_matmul_int8(
+            _ptr(a), _ptr(a_scale), M, _ptr(b), _ptr(b_scale), b.shape[0], K, _ptr(out), _INT8_DTYPES[out_dtype],
+            _stream()))
+    return out
+
+
+def linear_int8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """x [..., K] (bf16 or fp32) -> [..., N]: x's rows quantised (quantize_int8),
+    then the product with int8 weights w [N, Kp] and their scales [N], as
+    ``quantize_int8`` made them from [N, K].  ``out_dtype``: x's unless given."""
+    _need_int8_source(x, "x")
+    K = x.shape[-1]
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != (K + 127) // 128 * 128:
+        raise ValueError(f"w must be int8 [N, {(K + 127) // 128 * 128}] for {K} columns of x")
+    q, scale = quantize_int8(x.view(-1, K))
+    out = matmul_int8(q, scale, w, w_scale, x.dtype if out_dtype is None else out_dtype)
+    return out.view(x.shape[:-1] + (w.shape[0],))
+
+
+def tile_int8(q: torch.Tensor) -> torch.Tensor:
+    """Row-major int8 matrices [G, N, K] -> the K-tiled [G, K/128, N, 128] that
+    ``forward`` reads with ``weights_tiled`` (moe_tile_bf16 on the bytes taken
+    as 2-byte units)."""
+    if q.dtype != torch.int8:
+        raise ValueError("q must be int8")
+    return tile_mxfp8(q.view(torch.uint8)).view(torch.int8)

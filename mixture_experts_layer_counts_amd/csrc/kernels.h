@@ -158,6 +158,66 @@ hipError_t launch_gemm_mx(const MxGemmArgs& args, int epilogue, hipStream_t stre
 // Tile rows of the routed MXFP8 GEMM kernels (their tile lists are built with it).
 int gemm_mx_routed_bm();
 
+// ---------------------------------------------------------------------------
+// Products in 8-bit integers, int32 accumulation:
+// C[r][n] = As[r] Bs[n] sum_k A[r][k] B[n][k]
+// ---------------------------------------------------------------------------
+// Over a tile list (routed experts) or dense (tiles NULL: rows 0 ..
+// dense_rows - 1 of expert 0).  Epilogues: kEpiSwiGLU writes SiLU(gate) * up in
+// fp32, kEpiBF16 and kEpiF32 the product.
+struct I8GemmArgs {
+  const int8_t* A;  // [a_rows][K]
+  const float* As;  // [a_rows]
+  int64_t a_rows;
+  // tile position p reads row a_idx[p] / a_div, or (p - a_sub) mod a_mod when a_idx is NULL
+  const int32_t* a_idx;
+  int a_div;
+  int64_t a_sub, a_mod;
+  const int8_t *B0, *B1;    // per expert [N][K], or K-tiled [K/128][N][128] (b_plane == N); B1: SwiGLU's up
+  const float *Bs0, *Bs1;   // per expert [N]
+  int64_t b_plane;
+  int N, K;
+  void* C;  // output row = c_idx ? c_idx[p] : p - c_sub, of c_rows rows
+  int64_t ldc, c_rows;
+  const int32_t* c_idx;
+  int64_t c_sub;
+  const int4* tiles;
+  const int32_t* tile_count;
+  const int32_t* tile_runs;
+  int max_tiles;
+  int dense_rows;
+};
+// Rows outside the operand (a table not built by the schedule kernels) read
+// row 0 and write nothing.
+__device__ __forceinline__ int64_t i8_a_row(const I8GemmArgs& a, int64_t p) {
+  const int64_t r = a.a_idx ? a.a_idx[p] / a.a_div : (p - a.a_sub) % a.a_mod;
+  return r >= 0 && r < a.a_rows ? r : 0;
+}
+__device__ __forceinline__ int64_t i8_c_row(const I8GemmArgs& a, int64_t p) {
+  const int64_t r = a.c_idx ? a.c_idx[p] : p - a.c_sub;
+  return r >= 0 && r < a.c_rows ? r : -1;
+}
+constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel
+hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
+
+// Rows of bf16 or fp32 [.][K] -> int8 [.][Kp] (zeros past K) and one scale per
+// row.  Row i of the launch goes to row i, or with `sched` schedule position p
+// = p_begin + i reads row sched[p] / k and goes to row p mod ring_rows.  With
+// `limit` (device), positions p_begin + i at or past it are left alone.
+struct QuantI8Args {
+  const void* src;
+  int64_t K, Kp;
+  int8_t* q;
+  float* scale;
+  const int32_t* limit;
+  int64_t p_begin;
+  const int32_t* sched;
+  int k;
+  int64_t src_rows, ring_rows;
+  int* err;
+};
+hipError_t launch_quantize_rows_i8(const QuantI8Args& args, bool src_f32, int64_t rows, hipStream_t stream);
+
 // Tiling of the routed bf16 GEMMs for minibatches of mb_rows rows, max_rows
 // routed rows in all over `experts` local experts, intermediate width I and
 // hidden width D: the tile height bm (the tile lists are built with it) and

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -27,7 +28,7 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
   size_t err, ord_local, chunk_cnt, M, tiles, tile_count, tile_runs, ring, ring_s, h, h_s, Y, h_shared, shared_out, router_parts,
-      xs_q, xs_s, hs_s, shared_tiles, shared_tile_count, total;
+      xs_q, xs_s, hs_s, h32, hs32, shared_tiles, shared_tile_count, total;
   int router_splits;
   int64_t n_minibatches;
   int max_tiles;
@@ -43,14 +44,14 @@ struct Layout {
 //   x (router, shared expert)  T*D*2     ring      C*D*e      routed h  b*I*e
 //   shared h                   T*I_s*e_s one routed weight matrix I*D*e
 //   shared weight matrix       I_s*D*e_s
-// with e (e_s) = 2 bytes per element in bf16 and 1 in MXFP8.  T, D, I and
+// with e (e_s) = 2 bytes per element in bf16 and 1 in MXFP8 and int8.  T, D, I and
 // I_s are already bounded when this runs; the router weights, E_total*D*2,
 // stay below 2^28 under the bounds E_total <= 1024 and D <= 65536.
 bool operands_addressable(const moe_shape* s) {
   constexpr int64_t kLimit = int64_t(1) << 31;
   if (s->ring_rows >= kLimit || s->minibatch_rows >= kLimit) return false;
-  const int64_t e = s->precision == MOE_MXFP8 ? 1 : 2;
-  const int64_t es = s->shared_precision == MOE_MXFP8 ? 1 : 2;
+  const int64_t e = s->precision == MOE_BF16 ? 2 : 1;
+  const int64_t es = s->shared_precision == MOE_BF16 ? 2 : 1;
   // every factor is now below 2^31 and every multiplier below 2^17: no int64 overflow
   const int64_t bytes[] = {s->T * s->D * 2,         s->ring_rows * s->D * e, s->minibatch_rows * s->I * e,
                            s->T * s->I_shared * es, s->I * s->D * e,         s->I_shared * s->D * es};
@@ -62,7 +63,8 @@ bool operands_addressable(const moe_shape* s) {
 bool valid_shape(const moe_shape* s, moe_status* why) {
   *why = MOE_ERR_INVALID_ARG;
   if (!s) return false;
-  if (s->shared_precision != MOE_BF16 && s->shared_precision != MOE_MXFP8) return false;
+  const auto known = [](int32_t p) { return p == MOE_BF16 || p == MOE_MXFP8 || p == MOE_INT8; };
+  if (!known(s->shared_precision)) return false;
   if (s->T < 0 || s->D <= 0 || s->I <= 0 || s->I_shared <= 0 || s->E_total <= 0 || s->k <= 0) return false;
   if (s->k > s->E_total) return false;
   if (s->num_src_ranks < 1 || s->rank < 0 || s->rank >= s->num_src_ranks) return false;
@@ -73,7 +75,7 @@ bool valid_shape(const moe_shape* s, moe_status* why) {
   if (s->max_rows < 0) return false;
   if (s->num_src_ranks == 1 && s->max_rows != s->T * s->k) return false;
   if (s->max_rows > s->num_src_ranks * s->T * s->k) return false;
-  if (s->precision != MOE_BF16 && s->precision != MOE_MXFP8) return false;
+  if (!known(s->precision)) return false;
   if (s->pipeline != 0 && s->pipeline != 1) return false;
   if (s->pipeline && (s->mem_workgroups < 0 || s->mem_workgroups % 8)) return false;
   if (s->weights_tiled != 0 && s->weights_tiled != 1) return false;
@@ -84,9 +86,9 @@ bool valid_shape(const moe_shape* s, moe_status* why) {
   if (s->num_src_ranks * s->T * s->k >= (int64_t(1) << 31)) return false;
   if (s->max_rows >= (int64_t(1) << 31) || s->T >= (int64_t(1) << 31)) return false;
   if (s->D > 65536 || s->I > 65536 || s->I_shared > 65536) return false;
-  // MXFP8 GEMM stages are 128 elements of K wide (D for up/gate, I for down)
-  if (s->precision == MOE_MXFP8 && (s->D % 128 || s->I % 128)) return false;
-  if (s->shared_precision == MOE_MXFP8 && (s->D % 128 || s->I_shared % 128)) return false;
+  // MXFP8 and int8 GEMM stages are 128 elements of K wide (D for up/gate, I for down)
+  if (s->precision != MOE_BF16 && (s->D % 128 || s->I % 128)) return false;
+  if (s->shared_precision != MOE_BF16 && (s->D % 128 || s->I_shared % 128)) return false;
   if (!operands_addressable(s)) return false;
   *why = MOE_OK;
   return true;
@@ -113,6 +115,8 @@ Layout layout_of(const moe_shape* s) {
   const int64_t mb_rows = std::min<int64_t>(s->minibatch_rows, std::max<int64_t>(s->max_rows, 1));
   const moe::RoutedTiling tiling = s->precision == MOE_MXFP8
                                        ? moe::RoutedTiling{moe::gemm_mx_routed_bm(), 0, 0}
+                                   : s->precision == MOE_INT8
+                                       ? moe::RoutedTiling{moe::kI8RowsBM, 0, 0}
                                        : moe::gemm_routed_tiling(mb_rows, s->max_rows, Lx, s->I, s->D,
                                                                  s->pipeline != 0);
   const int bm = tiling.bm;
@@ -140,6 +144,15 @@ Layout layout_of(const moe_shape* s) {
     L.ring_s = take(s->ring_rows * (s->D / 32));
     L.h = take(s->minibatch_rows * s->I);
     L.h_s = take(s->minibatch_rows * (s->I / 32));
+  } else if (s->precision == MOE_INT8) {
+    // R == 1: every token quantised once, and the GEMM reads rows through the
+    // schedule table; R > 1: the routed rows in ring slots
+    const int64_t rows = R == 1 ? s->T : s->ring_rows;
+    L.ring = take(rows * s->D);
+    L.ring_s = take(sizeof(float) * rows);
+    L.h = take(mb_rows * s->I);
+    L.h_s = take(sizeof(float) * mb_rows);
+    L.h32 = take(sizeof(float) * mb_rows * s->I);
   } else {
     L.ring = take(sizeof(uint16_t) * s->ring_rows * s->D);
     // the persistent kernel runs up/gate up to H - 1 minibatches ahead of
@@ -159,6 +172,12 @@ Layout layout_of(const moe_shape* s) {
     L.hs_s = take(s->T * (s->I_shared / 32));
     L.shared_tiles = take(sizeof(int4) * moe::dense_tiles_bound(s->T, moe::gemm_mx_routed_bm()));
     L.shared_tile_count = take(sizeof(int32_t));
+  } else if (s->shared_precision == MOE_INT8) {
+    L.xs_q = take(s->T * s->D);
+    L.xs_s = take(sizeof(float) * s->T);
+    L.h_shared = take(s->T * s->I_shared);
+    L.hs_s = take(sizeof(float) * s->T);
+    L.hs32 = take(sizeof(float) * s->T * s->I_shared);
   } else {
     L.h_shared = take(sizeof(uint16_t) * s->T * s->I_shared);
   }
@@ -441,6 +460,153 @@ hipError_t routed_minibatch_mx(const moe_shape* shape, const moe_weights* w, con
   return moe::launch_gemm_mx(d, moe::kEpiBF16, s);
 }
 
+// The K-quantised rows of a [rows, K] matrix, in place order.
+hipError_t quantize_i8(const void* src, bool src_f32, int64_t rows, int64_t K, int8_t* q, float* scale, hipStream_t s,
+                       const int32_t* limit = nullptr, int64_t p_begin = 0) {
+  moe::QuantI8Args a{};
+  a.src = src;
+  a.K = a.Kp = K;
+  a.q = q;
+  a.scale = scale;
+  a.limit = limit;
+  a.p_begin = p_begin;
+  return moe::launch_quantize_rows_i8(a, src_f32, rows, s);
+}
+
+// C = A B^T of quantised rows, dense.
+moe::I8GemmArgs dense_i8(const int8_t* A, const float* As, int64_t M, const void* B, const void* Bs, int64_t N,
+                         int64_t K, void* C) {
+  moe::I8GemmArgs g{};
+  g.A = A;
+  g.As = As;
+  g.a_rows = M;
+  g.a_mod = INT64_MAX;
+  g.B0 = static_cast<const int8_t*>(B);
+  g.Bs0 = static_cast<const float*>(Bs);
+  g.N = static_cast<int>(N);
+  g.K = static_cast<int>(K);
+  g.C = C;
+  g.ldc = N;
+  g.c_rows = M;
+  g.dense_rows = static_cast<int>(M);
+  return g;
+}
+
+// The shared expert in int8: x quantised per token, up/gate with SwiGLU into
+// fp32 h, h quantised per token, down into fp32 rows for the combine.
+hipError_t shared_expert_i8(const moe_shape* shape, const moe_weights* w, const void* x_local, const Layout& L,
+                            void* ws, hipStream_t s) {
+  const int64_t T = shape->T, D = shape->D, Is = shape->I_shared;
+  int8_t* xq = at<int8_t>(ws, L.xs_q);
+  float* xs = at<float>(ws, L.xs_s);
+  int8_t* hq = at<int8_t>(ws, L.h_shared);
+  float* hs = at<float>(ws, L.hs_s);
+  float* h32 = at<float>(ws, L.hs32);
+  {
+    ProbeScope probe(MOE_K_SHARED_UP, s);
+    hipError_t e = quantize_i8(x_local, false, T, D, xq, xs, s);
+    if (e != hipSuccess) return e;
+    moe::I8GemmArgs u = dense_i8(xq, xs, T, w->ws_gate, w->ss_gate, Is, D, h32);
+    u.B1 = static_cast<const int8_t*>(w->ws_up);
+    u.Bs1 = reinterpret_cast<const float*>(w->ss_up);
+    e = moe::launch_gemm_i8(u, moe::kEpiSwiGLU, s);
+    if (e != hipSuccess) return e;
+  }
+  ProbeScope probe(MOE_K_SHARED_DOWN, s);
+  hipError_t e = quantize_i8(h32, true, T, Is, hq, hs, s);
+  if (e != hipSuccess) return e;
+  return moe::launch_gemm_i8(dense_i8(hq, hs, T, w->ws_down, w->ss_down, D, Is, at<float>(ws, L.shared_out)),
+                             moe::kEpiF32, s);
+}
+
+// One minibatch of the routed experts in int8.  With one source rank every
+// token was quantised once (first minibatch) and the up/gate GEMM reads its
+// rows through the schedule table; with several the routed rows are quantised
+// into ring slots.
+hipError_t routed_minibatch_i8(const moe_shape* shape, const moe_weights* w, const void* x_src,
+                               const int32_t* sched_src, const int32_t* expert_offsets, const Layout& L, void* ws,
+                               int64_t m, int64_t p_begin, int64_t rows, hipStream_t s) {
+  const int64_t D = shape->D, I = shape->I, C = shape->ring_rows, R = shape->num_src_ranks;
+  const int32_t* limit = expert_offsets + shape->experts_per_rank;
+  int8_t* xq = at<int8_t>(ws, L.ring);
+  float* xs = at<float>(ws, L.ring_s);
+  int8_t* hq = at<int8_t>(ws, L.h);
+  float* hs = at<float>(ws, L.h_s);
+  float* h32 = at<float>(ws, L.h32);
+  if (R > 1 || m == 0) {
+    ProbeScope probe(MOE_K_GATHER, s);
+    hipError_t e;
+    if (R == 1) {
+      e = quantize_i8(x_src, false, shape->T, D, xq, xs, s);
+    } else {
+      moe::QuantI8Args a{};
+      a.src = x_src;
+      a.K = a.Kp = D;
+      a.q = xq;
+      a.scale = xs;
+      a.limit = limit;
+      a.p_begin = p_begin;
+      a.sched = sched_src;
+      a.k = static_cast<int>(shape->k);
+      a.src_rows = R * shape->T;
+      a.ring_rows = C;
+      a.err = at<int>(ws, L.err);
+      e = moe::launch_quantize_rows_i8(a, false, rows, s);
+    }
+    if (e != hipSuccess) return e;
+  }
+  moe::I8GemmArgs u{};
+  u.A = xq;
+  u.As = xs;
+  u.a_rows = R == 1 ? shape->T : C;
+  u.a_idx = R == 1 ? sched_src : nullptr;
+  u.a_div = static_cast<int>(shape->k);
+  u.a_mod = C;
+  u.B0 = static_cast<const int8_t*>(w->w_gate);
+  u.B1 = static_cast<const int8_t*>(w->w_up);
+  u.Bs0 = reinterpret_cast<const float*>(w->s_gate);
+  u.Bs1 = reinterpret_cast<const float*>(w->s_up);
+  u.b_plane = shape->weights_tiled ? I : 0;
+  u.N = static_cast<int>(I);
+  u.K = static_cast<int>(D);
+  u.C = h32;
+  u.ldc = I;
+  u.c_rows = rows;
+  u.c_sub = p_begin;
+  u.tiles = at<int4>(ws, L.tiles) + m * L.max_tiles;
+  u.tile_count = at<int32_t>(ws, L.tile_count) + m;
+  u.tile_runs = at<int32_t>(ws, L.tile_runs) + m * moe::kTileRunBounds;
+  u.max_tiles = L.max_tiles;
+  {
+    ProbeScope probe(MOE_K_UP_GATE, s);
+    const hipError_t e = moe::launch_gemm_i8(u, moe::kEpiSwiGLU, s);
+    if (e != hipSuccess) return e;
+  }
+  ProbeScope probe(MOE_K_DOWN, s);
+  const hipError_t e = quantize_i8(h32, true, rows, I, hq, hs, s, limit, p_begin);
+  if (e != hipSuccess) return e;
+  moe::I8GemmArgs d = u;
+  d.A = hq;
+  d.As = hs;
+  d.a_rows = rows;
+  d.a_idx = nullptr;
+  d.a_sub = p_begin;
+  d.a_mod = INT64_MAX;
+  d.B0 = static_cast<const int8_t*>(w->w_down);
+  d.B1 = nullptr;
+  d.Bs0 = reinterpret_cast<const float*>(w->s_down);
+  d.Bs1 = nullptr;
+  d.b_plane = shape->weights_tiled ? D : 0;
+  d.N = static_cast<int>(D);
+  d.K = static_cast<int>(I);
+  d.C = at<uint16_t>(ws, L.Y);
+  d.ldc = D;
+  d.c_rows = L.y_rows;
+  d.c_idx = R == 1 ? sched_src : nullptr;
+  d.c_sub = 0;
+  return moe::launch_gemm_i8(d, moe::kEpiBF16, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -483,10 +649,10 @@ moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router
   Layout L;
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
   if (!logits || !topk_idx || !topk_gate || (x && !w_router)) return MOE_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
-  if (T == 0) return MOE_OK;
   if (x) MOE_TRY_HIP(router_gemm(shape, x, w_router, logits, L, ws, s));
   ProbeScope probe(MOE_K_TOPK, s);
   const bool parts = x && L.router_splits > 1;
@@ -502,10 +668,10 @@ moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, co
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
   if (!valid_router(shape, router)) return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
   if (!logits || !topk_idx || !topk_gate || (x && !w_router)) return MOE_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
-  if (T == 0) return MOE_OK;
   if (x) MOE_TRY_HIP(router_gemm(shape, x, w_router, logits, L, ws, s));
   ProbeScope probe(MOE_K_TOPK, s);
   const bool parts = x && L.router_splits > 1;
@@ -521,9 +687,9 @@ moe_status moe_route_backward(const moe_shape* shape, const moe_router* router, 
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
   if (!valid_router(shape, router)) return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0) return MOE_OK;
   if (!logits || !topk_idx || !dgate || !dlogits) return MOE_ERR_INVALID_ARG;
   const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
-  if (T == 0) return MOE_OK;
   return hip_status(moe::launch_route_backward(router_args(router), logits, topk_idx, dgate, T, E, k, dlogits, nullptr,
                                                E, at<int>(ws, L.err), static_cast<hipStream_t>(stream)));
 }
@@ -535,7 +701,7 @@ moe_status moe_schedule(const moe_shape* shape, const int32_t* routes, int32_t* 
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
   const int64_t NK = shape->T * shape->k;
-  if (!expert_counts || !expert_offsets || !route_dst || (NK > 0 && !routes) || (shape->max_rows > 0 && !sched_src))
+  if (!expert_counts || !expert_offsets || (NK > 0 && (!routes || !route_dst)) || (shape->max_rows > 0 && !sched_src))
     return MOE_ERR_INVALID_ARG;
   moe::SchedScratch sc{at<int32_t>(ws, L.ord_local), at<int32_t>(ws, L.chunk_cnt), at<int32_t>(ws, L.M)};
   ProbeScope probe(MOE_K_SCHEDULE, static_cast<hipStream_t>(stream));
@@ -577,10 +743,17 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
   const bool mx = shape->precision == MOE_MXFP8;
+  if (shape->T == 0 && shape->max_rows == 0) return MOE_OK;  // no rows: their pointers may be NULL
   if (!w || !w->w_gate || !w->w_up || !w->w_down || !w->ws_gate || !w->ws_up || !w->ws_down) return MOE_ERR_INVALID_ARG;
-  if (mx && (!w->s_gate || !w->s_up || !w->s_down)) return MOE_ERR_INVALID_ARG;
-  const bool shared_mx = shape->shared_precision == MOE_MXFP8;
-  if (shared_mx && (!w->ss_gate || !w->ss_up || !w->ss_down)) return MOE_ERR_INVALID_ARG;
+  const bool i8 = shape->precision == MOE_INT8;
+  if ((mx || i8) && (!w->s_gate || !w->s_up || !w->s_down)) return MOE_ERR_INVALID_ARG;
+  const bool shared_mx = shape->shared_precision == MOE_MXFP8, shared_i8 = shape->shared_precision == MOE_INT8;
+  if ((shared_mx || shared_i8) && (!w->ss_gate || !w->ss_up || !w->ss_down)) return MOE_ERR_INVALID_ARG;
+  auto aligned16 = [](std::initializer_list<const void*> ps) {
+    return std::all_of(ps.begin(), ps.end(), [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; });
+  };
+  if (i8 && !aligned16({w->w_gate, w->w_up, w->w_down})) return MOE_ERR_INVALID_ARG;
+  if (shared_i8 && !aligned16({w->ws_gate, w->ws_up, w->ws_down})) return MOE_ERR_INVALID_ARG;
   if (!expert_offsets || !route_dst || !topk_gate || !out) return MOE_ERR_INVALID_ARG;
   if (shape->T > 0 && !x_local) return MOE_ERR_INVALID_ARG;
   if (shape->max_rows > 0 && (!x_src || !sched_src)) return MOE_ERR_INVALID_ARG;
@@ -589,7 +762,6 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   const int Is = static_cast<int>(shape->I_shared), k = static_cast<int>(shape->k);
   const int Lx = static_cast<int>(shape->experts_per_rank);
   const int64_t b = shape->minibatch_rows, C = shape->ring_rows, R = shape->num_src_ranks;
-  if (T == 0 && shape->max_rows == 0) return MOE_OK;
   if (shape->pipeline) {
     // the persistent kernel's grid is every workgroup the chip holds at once
     // (a host query): at least 8 of them must be left for the GEMMs, and some
@@ -623,6 +795,8 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   //    it needs no dispatch, so it goes first)
   if (T > 0 && shared_mx) {
     MOE_TRY_HIP(shared_expert_mx(shape, w, x_local, L, ws, s));
+  } else if (T > 0 && shared_i8) {
+    MOE_TRY_HIP(shared_expert_i8(shape, w, x_local, L, ws, s));
   } else if (T > 0) {
     moe::GemmArgs g{};
     g.k_splits = 1;
@@ -772,6 +946,10 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
             routed_minibatch_mx(shape, w, x_src, sched_src, expert_offsets, route_dst, L, ws, m, p_begin, rows, s));
         continue;
       }
+      if (i8) {
+        MOE_TRY_HIP(routed_minibatch_i8(shape, w, x_src, sched_src, expert_offsets, L, ws, m, p_begin, rows, s));
+        continue;
+      }
       MOE_TRY_HIP(gather(m));
       {
         ProbeScope probe(MOE_K_UP_GATE, s);
@@ -823,6 +1001,43 @@ moe_status moe_mxfp8_pack_scales(const uint8_t* scale, int64_t groups, int64_t r
   if (!scale || !packed || scale == packed) return MOE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(scale) % 4 || reinterpret_cast<uintptr_t>(packed) % 4) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_pack_mx_scales(scale, groups, rows, K, packed, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_quantize_int8(const void* src, int32_t src_dtype, int64_t rows, int64_t K, int8_t* q, float* scale,
+                             void* stream) {
+  if (src_dtype != MOE_DT_BF16 && src_dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const bool f32 = src_dtype == MOE_DT_F32;
+  if (!src || !q || !scale || src == q) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(src) % (f32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(scale) % 4)
+    return MOE_ERR_INVALID_ARG;
+  if (rows >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  moe::QuantI8Args a{};
+  a.src = src;
+  a.K = K;
+  a.Kp = (K + 127) / 128 * 128;
+  a.q = q;
+  a.scale = scale;
+  return hip_status(moe::launch_quantize_rows_i8(a, f32, rows, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_matmul_int8(const int8_t* a, const float* a_scale, int64_t M, const int8_t* b, const float* b_scale,
+                           int64_t N, int64_t K, void* out, int32_t out_dtype, void* stream) {
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || K <= 0 || K % 128) return MOE_ERR_INVALID_ARG;
+  constexpr int64_t kLimit = int64_t(1) << 31;
+  if (K > 65536 || M >= kLimit || N >= kLimit || M * K >= kLimit || N * K >= kLimit) return MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return MOE_OK;
+  if (!a || !a_scale || !b || !b_scale || !out) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(a), static_cast<const void*>(b), static_cast<const void*>(out)})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return MOE_ERR_INVALID_ARG;
+  for (const float* p : {a_scale, b_scale})
+    if (reinterpret_cast<uintptr_t>(p) % 4) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_gemm_i8(dense_i8(a, a_scale, M, b, b_scale, N, K, out),
+                                        out_dtype == MOE_DT_F32 ? moe::kEpiF32 : moe::kEpiBF16,
+                                        static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_probe_begin(int32_t kernel_id, int32_t max_launches) {

@@ -20,4 +20,4 @@ Every function is pinned by ``tests/test_oracle_*.py`` to something other than
 itself (brute force, closed forms, library routines, invariants).
 """
 
-from . import backward, bf16, mx, moe, scored  # noqa: F401
+from . import backward, bf16, int8, mx, moe, scored  # noqa: F401

@@ -1,0 +1,331 @@
+"""GPU parity of the 8-bit integer operators: moe_quantize_int8 and
+moe_matmul_int8 bit for bit, and the int8 experts of moe_forward.
+
+Quotients, sums and the two scalings are defined to the bit, so the first two
+are compared for equality.  A layer's output is not: SiLU is approximated (to
+about 2^-20) before h is quantised, so a value of h within 127 2^-20 of a
+border between two integers may fall on its other side.  That is below 2.5e-4
+of the values, half a value a row at I = 2048; 8 such steps a row are allowed,
+each of m_h / 127 times the largest weight of the channel.  The routed rows are
+stored bf16, half a step 2^-8 of the value, and the rest is fp32: 2^-20.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from mixture_experts_layer_counts_amd import (MoELayer, linear_int8, matmul_int8, quantize_int8, router_for, shape_for,
+                                              tile_int8)
+from oracle import int8
+from tests._gpu import need_gpu, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_with_ties(rows, K, dtype, seed):
+    """Normal rows; some with entries whose quotient 127 v / m is half an integer."""
+    v = torch.randn((rows, K), generator=torch.Generator().manual_seed(seed)).to(dtype)
+    for r in range(0, rows, 3):
+        v[r] = torch.where(v[r].abs() > 2.0, v[r], (v[r] * 16).round() / 16).clamp(-4, 4)
+        v[r, -1] = 4.0 if r % 2 else 127.0 / 32
+    return v
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (5, 128), (7, 130), (9, 1001), (4, 2048), (2, 7168), (3, 8200),
+                                    (2, 40001), (300, 256)])
+def test_quantize_int8(rows, K, dtype):
+    dev = need_gpu()
+    say("quantize_int8", rows, K, dtype)
+    v = rows_with_ties(rows, K, dtype, K)
+    q, s = quantize_int8(v.to(dev))
+    wq, _ = int8.quantize(v.double().numpy())
+    Kp = (K + 127) // 128 * 128
+    assert q.shape == (rows, Kp)
+    got = q.cpu().numpy()
+    assert np.array_equal(got[:, :K], wq) and np.all(got[:, K:] == 0)
+    m = np.abs(v.float().numpy()).max(axis=1)
+    assert np.array_equal(s.cpu().numpy(), m / np.float32(127))
+
+
+def test_quantize_int8_special_rows():
+    dev = need_gpu()
+    say("quantize_int8 special")
+    v = torch.zeros((8, 200))
+    v[1, 3], v[2, 5], v[3, 199] = float("inf"), float("nan"), -float("inf")
+    v[4, 0], v[4, 1] = torch.finfo(torch.float32).max, torch.finfo(torch.float32).min / 2
+    v[5, 0], v[5, 1] = 1e-45, -1e-45  # the smallest numbers
+    v[6, 0], v[6, 1] = 1.0, 2.0 ** -120
+    v[7, ::2] = -0.0
+    q, s = (t.cpu() for t in quantize_int8(v.to(dev)))
+    assert torch.isnan(s[1:4]).all() and (q[1:4] == 0).all()
+    assert (q[0] == 0).all() and s[0] == 0 and (q[7] == 0).all() and s[7] == 0
+    assert q[4, :2].tolist() == [127, -64] and q[5, :2].tolist() == [127, -127] and q[6, :2].tolist() == [127, 0]
+    # a row that is not finite gives NaN, and only in its own row
+    w = torch.ones((16, 256), dtype=torch.int8, device=dev)
+    out = matmul_int8(q.to(dev), s.to(dev), w, torch.ones(16, device=dev)).cpu()
+    assert torch.isnan(out[1:4]).all() and torch.isfinite(out[[0, 5, 6, 7]]).all()
+
+
+def reference(q, s, wq, ws, dtype):
+    acc = (q.double() @ wq.double().T).float()  # exact integers, rounded to fp32 once
+    return ((acc * s[:, None]) * ws[None, :]).to(dtype)
+
+
+MATS = [(1, 1, 128), (1, 2048, 7168), (2, 17, 256), (15, 33, 384), (16, 64, 128), (17, 1001, 1536), (32, 130, 2048),
+        (33, 257, 640), (64, 512, 1024), (100, 96, 128), (255, 300, 256), (257, 511, 384), (777, 1001, 1536),
+        (1024, 768, 2048), (513, 8, 65536)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", MATS, ids=lambda v: str(v))
+def test_matmul_int8(M, N, K, dtype):
+    dev = need_gpu()
+    say("matmul_int8", M, N, K, dtype)
+    gen = torch.Generator().manual_seed(M + N)
+    q = torch.randint(-127, 128, (M, K), generator=gen, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=gen, dtype=torch.int8)
+    if M > 1:
+        q[1], w[0] = 127, 127  # the largest sum there is
+    s, ws = torch.rand(M, generator=gen), torch.rand(N, generator=gen) - 0.5
+    got = matmul_int8(q.to(dev), s.to(dev), w.to(dev), ws.to(dev), out_dtype=dtype).cpu()
+    assert torch.equal(got, reference(q, s, w, ws, dtype))
+
+
+def test_matmul_int8_writes_only_its_rows():
+    # a result inside a larger buffer of the allocator stays inside it: rows past M keep their bytes
+    dev = need_gpu()
+    from mixture_experts_layer_counts_amd import _lib
+    lib = _lib.load()
+    for M, N in ((5, 37), (40, 129), (300, 257)):
+        q = torch.ones((M, 128), dtype=torch.int8, device=dev)
+        w = torch.ones((N, 128), dtype=torch.int8, device=dev)
+        one_m, one_n = torch.ones(M, device=dev), torch.ones(N, device=dev)
+        buf = torch.full((M * N + 512,), -7.0, device=dev)
+        assert lib.moe_matmul_int8(q.data_ptr(), one_m.data_ptr(), M, w.data_ptr(), one_n.data_ptr(), N, 128,
+                                   buf.data_ptr(), 1, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert (buf[:M * N] == 128).all() and (buf[M * N:] == -7).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lead,K,N", [((1,), 100, 7), ((2, 9), 1500, 301), ((130,), 7168, 256)])
+def test_linear_int8(lead, K, N, dtype):
+    dev = need_gpu()
+    say("linear_int8", lead, K, N)
+    gen = torch.Generator().manual_seed(N)
+    x = torch.randn(lead + (K,), generator=gen).to(dtype)
+    wq, ws = quantize_int8((torch.randn((N, K), generator=gen) / K ** 0.5).to(dev))
+    for out_dtype in (None, torch.float32):
+        got = linear_int8(x.to(dev), wq, ws, out_dtype)
+        q, _ = int8.quantize(x.double().numpy().reshape(-1, K))
+        s = x.float().abs().amax(dim=-1).reshape(-1) / 127.0
+        want = reference(torch.from_numpy(q), s, wq.cpu()[:, :K], ws.cpu(), dtype if out_dtype is None else out_dtype)
+        assert got.shape == lead + (N,) and torch.equal(got.cpu().reshape(-1, N), want)
+    empty = linear_int8(torch.empty((0, K), dtype=dtype, device=dev), wq, ws)
+    assert empty.shape == (0, N)
+
+
+# ---------------------------------------------------------------------------
+# the layer
+# ---------------------------------------------------------------------------
+def quantised(inp, dev, routed=True, shared=True, tiled=False):
+    w = {}
+    for n in ("gate", "up", "down"):
+        if routed:
+            w["q_" + n], w["s_" + n] = quantize_int8(inp["w_" + n].to(dev))
+            if tiled:
+                w["q_" + n] = tile_int8(w["q_" + n])
+        else:
+            w["w_" + n] = inp["w_" + n].to(dev)
+        if shared:
+            w["qs_" + n], w["ss_" + n] = quantize_int8(inp["ws_" + n].to(dev))
+        else:
+            w["ws_" + n] = inp["ws_" + n].to(dev)
+    return w
+
+
+def oracle(w, inp, idx, gate, routed=True, shared=True):
+    """(out, bound) in fp64 for the layer with int8 routed and shared experts."""
+    x = inp["x"].double().numpy()
+    wq = {}
+    for n in ("gate", "up", "down"):
+        wq["q_" + n], wq["s_" + n] = int8.quantize(inp["w_" + n].double().numpy())
+        wq["qs_" + n], wq["ss_" + n] = int8.quantize(inp["ws_" + n].double().numpy())
+    out, tol = np.zeros((w.T, w.D)), np.zeros((w.T, w.D))
+
+    def add(rows, xr, g, prefix, e, step):
+        y, m = int8.ffn(xr, wq, prefix, e)
+        q, s = wq[f"q{prefix}_down"], wq[f"s{prefix}_down"]
+        big = np.abs(q if e is None else q[e]).max(axis=1) * (s if e is None else s[e])
+        out[rows] += g[:, None] * y
+        tol[rows] += np.abs(g)[:, None] * (step * np.abs(y) + 8 * (m / 127)[:, None] * big[None, :])
+    for e in range(w.E):
+        t, slot = np.nonzero(idx == e)
+        if len(t):
+            add(t, x[t], gate[t, slot].astype(np.float64), "", e, 2.0 ** -8 + 2.0 ** -20)
+    add(np.arange(w.T), x, np.ones(w.T), "s", None, 2.0 ** -20)
+    return out, tol + 2.0 ** -20 * np.abs(out)
+
+
+LAYERS = [  # workload, minibatch, ring
+    (synth.Workload("one", T=1, D=256, I=128, E=8, k=2, I_shared=128, seed=1, routing="gaussian"), None, None),
+    (synth.Workload("few", T=5, D=512, I=256, E=64, k=8, I_shared=384, seed=2, routing="gaussian"), None, None),
+    (synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian"), None, None),
+    (synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian"), 256, 512),
+    (synth.Workload("skewed", T=1100, D=384, I=128, E=24, k=6, I_shared=256, seed=8, routing="zipf"), None, None),
+    (synth.Workload("single", T=700, D=128, I=128, E=1, k=1, I_shared=128, seed=9, routing="gaussian"), None, None),
+]
+
+
+def make(w, dev, b=None, C=None, tiled=False, precision="int8", shared="int8"):
+    return MoELayer(shape_for(w.T, w.D, w.I, w.E, w.k, I_shared=w.I_shared, minibatch_rows=b, ring_rows=C,
+                              precision=precision, shared_precision=shared, weights_tiled=tiled), device=dev)
+
+
+@pytest.mark.parametrize("w,b,C", LAYERS, ids=[f"{c[0].name}-{c[1]}" for c in LAYERS])
+def test_int8_layer_parity(w, b, C):
+    dev = need_gpu()
+    say("int8 layer", w, b, C)
+    inp = synth.make_inputs(w)
+    x, lg = inp["x"].to(dev), inp["logits"].to(dev)
+    outs = []
+    for tiled in (False, True):
+        m = make(w, dev, b, C, tiled)
+        r = m(x, None, quantised(inp, dev, tiled=tiled), logits=lg)
+        torch.cuda.synchronize()
+        assert m.device_error() == 0
+        outs.append(r["out32"])
+    assert torch.equal(outs[0], outs[1])  # the layout of the weights changes no bit
+    want, tol = oracle(w, inp, r["idx"].cpu().numpy(), r["gate"].cpu().numpy())
+    err = np.abs(r["out32"].cpu().numpy() - want)
+    say("   max err / bound", (err / tol).max())
+    assert np.all(err <= tol)
+    assert torch.equal(r["out"], r["out32"].to(torch.bfloat16))
+
+
+def test_int8_layer_is_the_same_for_every_minibatch():
+    dev = need_gpu()
+    w = synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian")
+    inp = synth.make_inputs(w)
+    x, lg = inp["x"].to(dev), inp["logits"].to(dev)
+    wd = quantised(inp, dev)
+    want = make(w, dev)(x, None, wd, logits=lg)["out32"]
+    for b, C in ((1, 1), (7, 7), (64, 128), (1000, 2000)):
+        got = make(w, dev, b, C)(x, None, wd, logits=lg)["out32"]
+        assert torch.equal(got, want), (b, C)
+
+
+@pytest.mark.parametrize("routed,shared", [(True, False), (False, True)])
+def test_int8_for_one_kind_of_expert(routed, shared):
+    # bf16 experts beside int8 ones: the int8 part of the result is the same bits as in the all-int8 layer
+    dev = need_gpu()
+    w = synth.Workload("mixed", T=130, D=256, I=128, E=8, k=2, I_shared=128, seed=4, routing="gaussian")
+    say("int8 mixed", routed, shared)
+    inp = synth.make_inputs(w)
+    x, lg = inp["x"].to(dev), inp["logits"].to(dev)
+    both = make(w, dev)
+    rb = both(x, None, quantised(inp, dev), logits=lg)
+    yb = both.routed_rows().clone()
+    m = make(w, dev, precision="int8" if routed else "bf16", shared="int8" if shared else "bf16")
+    r = m(x, None, quantised(inp, dev, routed, shared), logits=lg)
+    y = m.routed_rows().clone()
+    plain = make(w, dev, precision="bf16", shared="bf16")
+    rp = plain(x, None, to_dev(inp, dev), logits=lg)
+    if routed:
+        assert torch.equal(y, yb)
+    else:
+        assert torch.equal(y, plain.routed_rows())
+    # out32 = (sum of routed, in order) + shared: what is left of one is the other's
+    g = r["gate"].double()
+    def shared_part(res, rows):
+        return res["out32"].double() - (g[:, :, None] * rows.double().view(w.T, w.k, w.D)).sum(1)
+    other = shared_part(rb if shared else rp, yb if shared else plain.routed_rows())
+    scale = r["out32"].abs().max().double()
+    assert (shared_part(r, y) - other).abs().max() <= 2.0 ** -20 * scale
+
+
+def test_int8_expert_parallel_share():
+    # R source ranks: this rank's routed rows equal those of the one-GPU layer on the same tokens
+    dev = need_gpu()
+    w = synth.Workload("ep", T=96, D=256, I=128, E=8, k=2, I_shared=128, seed=14, routing="gaussian")
+    R, L = 2, 4
+    say("int8 ep", w)
+    inp = synth.make_inputs(w)
+    wd = quantised(inp, dev)
+    x = inp["x"].to(dev)
+    half = w.T // R
+    one = make(w, dev)
+    res = one(x, None, wd, logits=inp["logits"].to(dev))
+    y = one.routed_rows().clone().view(w.T, w.k, w.D)
+    A = res["idx"].view(R, half * w.k)
+    for rank in range(R):
+        for b, C in ((None, None), (40, 80)):
+            m = MoELayer(shape_for(half, w.D, w.I, w.E, w.k, I_shared=w.I_shared, R=R, rank=rank,
+                                   max_rows=w.T * w.k, minibatch_rows=b, ring_rows=C,
+                                   precision="int8", shared_precision="int8"), device=dev)
+            sched = m.schedule(A.contiguous())
+            mine = {n: (v[rank * L:(rank + 1) * L].contiguous() if n.startswith(("q_", "s_")) else v)
+                    for n, v in wd.items()}
+            m.routed_rows().fill_(-3.0)  # rows behind the last routed one stay as they were
+            m.forward(mine, x, x[rank * half:(rank + 1) * half].contiguous(),
+                      res["gate"][rank * half:(rank + 1) * half].contiguous(), sched)
+            torch.cuda.synchronize()
+            assert m.device_error() == 0
+            P = int(sched["offsets"][-1])
+            rows = m.routed_rows()
+            src = sched["sched"][:P].long()
+            assert torch.equal(rows[:P], y.view(-1, w.D)[src]), (rank, b)
+            assert (rows[P:] == -3).all()
+
+
+def test_int8_layer_with_a_scored_router_in_a_graph():
+    """Router, schedule and int8 experts as a serving step runs them: captured,
+    replayed on new tokens between eager work, each replay equal to the eager step."""
+    dev = need_gpu()
+    w = synth.Workload("serve", T=12, D=512, I=256, E=32, k=4, I_shared=256, seed=21)
+    say("int8 serving step", w)
+    inp = synth.make_inputs(w)
+    wd = quantised(inp, dev, tiled=True)
+    wr = inp["w_router"].to(dev)
+    bias = 0.1 * torch.randn(w.E, generator=torch.Generator().manual_seed(1)).to(dev)
+    r = router_for(score="sigmoid", groups=8, kept_groups=4, scale=2.5)
+    x = inp["x"].to(dev)
+    m, eager = make(w, dev, tiled=True), make(w, dev, tiled=True)
+
+    def step(layer):
+        return layer(x, wr, wd, router=r, bias=bias)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(m)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(m)
+    gen = torch.Generator().manual_seed(3)
+    for rep in range(3):
+        x.copy_(torch.randn((w.T, w.D), generator=gen).to(torch.bfloat16))
+        want = step(eager)
+        for n in ("out", "out32", "idx"):
+            got[n].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for n in ("logits", "idx", "gate", "out", "out32"):
+            assert torch.equal(got[n], want[n]), (rep, n)
+    assert m.device_error() == 0
+    # and the eager step is the oracle's
+    want, tol = oracle(w, {**inp, "x": x.cpu()}, got["idx"].cpu().numpy(), got["gate"].cpu().numpy())
+    assert np.all(np.abs(got["out32"].cpu().numpy() - want) <= tol)
+
+
+def test_int8_layer_without_tokens():
+    dev = need_gpu()
+    w = synth.Workload("none", T=4, D=128, I=128, E=4, k=2, I_shared=128, seed=3, routing="gaussian")
+    inp = synth.make_inputs(w)
+    m = MoELayer(shape_for(0, 128, 128, 4, 2, precision="int8", shared_precision="int8"), device=dev)
+    r = m(torch.empty((0, 128), dtype=torch.bfloat16, device=dev), None, quantised(inp, dev),
+          logits=torch.empty((0, 4), device=dev))
+    assert r["out"].shape == (0, 128) and m.device_error() == 0
