@@ -59,7 +59,6 @@ __device__ __forceinline__ void rows_item(const I8GemmArgs& a, int e, int64_t p0
       for (int rb = 0; rb < RB; ++rb) acc[h][b][rb] = i32x4_t{};
 
   const int nk = a.K / kStage;
-#pragma unroll 2
   for (int st = wave; st < nk; st += kWaves) {
     i32x4_t av[RB][2], bv[NB][NBL][2];
 #pragma unroll
@@ -180,6 +179,7 @@ hipError_t launch_gemm_i8(const I8GemmArgs& a, int epilogue, hipStream_t stream)
   for (const void* p : {static_cast<const void*>(a.A), static_cast<const void*>(a.B0),
                         static_cast<const void*>(epilogue == kEpiSwiGLU ? a.B1 : a.B0), static_cast<const void*>(a.C)})
     if (!p || reinterpret_cast<uintptr_t>(p) % 16) return hipErrorInvalidValue;
+  if (a.tile_rows == kI8BM) return launch_gemm_i8_tiles(a, epilogue, stream);
   switch (epilogue) {
     case kEpiSwiGLU:
       return run_rows<2, kEpiSwiGLU>(a, stream);

@@ -185,6 +185,7 @@ struct I8GemmArgs {
   const int32_t* tile_count;
   const int32_t* tile_runs;
   int max_tiles;
+  int tile_rows;  // height of the tile lists, which picks the kernel: kI8RowsBM or kI8BM
   int dense_rows;
 };
 // Rows outside the operand (a table not built by the schedule kernels) read
@@ -197,7 +198,11 @@ __device__ __forceinline__ int64_t i8_c_row(const I8GemmArgs& a, int64_t p) {
   const int64_t r = a.c_idx ? a.c_idx[p] : p - a.c_sub;
   return r >= 0 && r < a.c_rows ? r : -1;
 }
-constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel
+constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel (gemm_i8_rows.hip)
+constexpr int kI8BM = 256;     // tile rows of the LDS-staged kernel (gemm_i8.hip)
+// Tile height for `rows` rows spread over `groups` weight matrices.
+inline int i8_tile_rows(int64_t rows, int64_t groups) { return rows > 32 * groups ? kI8BM : kI8RowsBM; }
+hipError_t launch_gemm_i8_tiles(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 
 // Rows of bf16 or fp32 [.][K] -> int8 [.][Kp] (zeros past K) and one scale per

@@ -116,7 +116,7 @@ Layout layout_of(const moe_shape* s) {
   const moe::RoutedTiling tiling = s->precision == MOE_MXFP8
                                        ? moe::RoutedTiling{moe::gemm_mx_routed_bm(), 0, 0}
                                    : s->precision == MOE_INT8
-                                       ? moe::RoutedTiling{moe::kI8RowsBM, 0, 0}
+                                       ? moe::RoutedTiling{moe::i8_tile_rows(mb_rows, Lx), 0, 0}
                                        : moe::gemm_routed_tiling(mb_rows, s->max_rows, Lx, s->I, s->D,
                                                                  s->pipeline != 0);
   const int bm = tiling.bm;
@@ -488,6 +488,7 @@ moe::I8GemmArgs dense_i8(const int8_t* A, const float* As, int64_t M, const void
   g.C = C;
   g.ldc = N;
   g.c_rows = M;
+  g.tile_rows = moe::i8_tile_rows(M, 1);
   g.dense_rows = static_cast<int>(M);
   return g;
 }
@@ -577,6 +578,7 @@ hipError_t routed_minibatch_i8(const moe_shape* shape, const moe_weights* w, con
   u.tile_count = at<int32_t>(ws, L.tile_count) + m;
   u.tile_runs = at<int32_t>(ws, L.tile_runs) + m * moe::kTileRunBounds;
   u.max_tiles = L.max_tiles;
+  u.tile_rows = L.routed_bm;
   {
     ProbeScope probe(MOE_K_UP_GATE, s);
     const hipError_t e = moe::launch_gemm_i8(u, moe::kEpiSwiGLU, s);
