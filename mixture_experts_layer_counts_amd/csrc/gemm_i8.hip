@@ -1,8 +1,15 @@
 // Products in 8-bit integers on gfx950, for many rows: C[r, n] = sa[r] sb[n]
 // sum_k A[r, k] B[n, k], over the experts' tile lists or dense, in the pipeline
-// of the MXFP8 kernels: 256 x BN tiles, 8 waves, K stages of 128 bytes per row
-// in two LDS rings fed by direct buffer->LDS loads (activation rows one stage
-// ahead, weight rows two), one barrier per stage.
+// of the bf16 kernels: K stages of 128 bytes per row in two LDS rings fed by
+// direct buffer->LDS loads (activation rows one stage ahead, weight rows two
+// where LDS holds a third slot), one barrier per stage.  The bytes per stage and
+// the matrix instructions' cycles are those of the bf16 kernels, at twice the
+// products.
+//
+// What bounds them is the load path: a CU streams rows into LDS at about 42
+// GB/s however deep its rings are (five stages ahead measured no faster than
+// two), so few rows want many small tiles on many CUs and many rows want the
+// fewest bytes per product, the 256- and 320-row tiles.
 //
 // v_mfma_i32_32x32x32_i8 multiplies a 32x32 block of A by one of B in int32;
 // lane l supplies row l % 32, 16 bytes of K chosen by l / 32.  Which bytes does
@@ -29,157 +36,172 @@ namespace {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-constexpr int kBM = kI8BM;
-constexpr int kRB = 128;           // bytes (K elements) of one stage row
-constexpr int kNSA = 2, kNSB = 3;  // ring slots: activation rows, weight rows
-constexpr int kWM = 4, kWN = 2;    // waves along rows and columns, two per SIMD
-constexpr int kNW = kWM * kWN;
+constexpr int kRB = 128;  // bytes (K elements) of one stage row
+
+// LDS ring slots: activation rows and weight rows.  A ring of n slots loads its
+// rows n - 1 stages ahead.
+constexpr int ring_bytes(int bm, int brows, int nsa, int nsb) { return (nsa * bm + nsb * brows) * kRB; }
 
 struct I8Src {
   __amdgpu_buffer_rsrc_t a, b0, b1;
 };
 
-// Row of the tile held by 32-row block fm of a wave in row group wm.
-__device__ __forceinline__ int tile_row(int wm, int fm) { return (fm * kWM + wm) * 32; }
+// Row of the tile held by 32-row block fm of a wave in row group wm: blocks
+// are dealt to the row groups in turn, so a partly filled tile keeps every
+// wave busy.
+template <int WM>
+__device__ __forceinline__ int tile_row(int wm, int fm) {
+  return (fm * WM + wm) * 32;
+}
 
-// The K loop of one workgroup; FML of the wave's FM row blocks hold tile rows.
-template <int BN, int NB, int FML, int FM, int FN, int AI, int BI>
+// The K loop of one workgroup, the bf16 kernels' protocol: a slot is refilled
+// right after the barrier that ends its stage's reads, the fragments of the
+// next 32-wide sub-step are read under the current MFMAs, and one barrier per
+// stage waits for the next stage's rows.  FML of the wave's FM row blocks hold
+// tile rows.
+template <int BM, int BN, int WM, int WN, int NSA, int NSB, int NB, int FML, int FM, int FN, int AI, int BI>
 __device__ __forceinline__ void k_loop_i8(char* smem, const I8Src& src, const uint32_t (&a_off)[AI],
                                           const uint32_t (&b_off)[BI], int b_stage, int nk, int a_rows, int tid,
                                           int wm, int wn, i32x16_t (&acc)[NB][FM][FN]) {
-  constexpr int BROWS = NB * BN, WTN = BN / kWN;
-  constexpr int ASLOT = kBM * kRB, BSLOT = BROWS * kRB;
+  constexpr int BROWS = NB * BN, WTN = BN / WN;
+  static_assert(NSA >= 2 && NSB >= NSA, "ring depths");
+  constexpr int ASLOT = BM * kRB, BSLOT = BROWS * kRB;
+  constexpr int KS = 4;  // 32-wide sub-steps per stage
   constexpr int ROWS_PER_LD = 1024 / kRB;
-  static_assert(AI * ROWS_PER_LD * kNW == kBM && BI * ROWS_PER_LD * kNW == BROWS, "loads per wave per stage");
-  static_assert(BI < 16, "vmcnt range");
+  static_assert(AI * ROWS_PER_LD * WM * WN == BM && BI * ROWS_PER_LD * WM * WN == BROWS, "loads per wave per stage");
   char* const sa0 = smem;
-  char* const sb0 = smem + kNSA * ASLOT;
+  char* const sb0 = smem + NSA * ASLOT;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int frag_row = lane & 31, frag_h = lane >> 5;
+  const int frag_row = lane & 31, frag_c = lane >> 5;
 
-  // a stage past the last loads the last one again, into a free slot, so
-  // that every step issues the same number of loads
+  // a stage past the last (in the prologue of a short K) loads the last one
+  // again, into a free slot, so that the prologue issues the same number of
+  // loads; row groups past the tile reload the first one for the same reason
   auto issue_a = [&](int kt) __attribute__((always_inline)) {
-    const int kc = kt < nk ? kt : nk - 1;
-    char* sa = sa0 + (kt % kNSA) * ASLOT;
+    const int ko = (kt < nk ? kt : nk - 1) * kRB;
+    char* sa = sa0 + (kt % NSA) * ASLOT;
 #pragma unroll
     for (int j = 0; j < AI; ++j)
-      dma16(src.a, sa + (wave * AI + j) * 1024, (wave * AI + j) * ROWS_PER_LD < a_rows ? a_off[j] : a_off[0],
-            kc * kRB);
+      dma16(src.a, sa + (wave * AI + j) * 1024, (wave * AI + j) * ROWS_PER_LD < a_rows ? a_off[j] : a_off[0], ko);
   };
   auto issue_b = [&](int kt) __attribute__((always_inline)) {
-    const int kc = kt < nk ? kt : nk - 1;
-    char* sb = sb0 + (kt % kNSB) * BSLOT;
+    const int ko = (kt < nk ? kt : nk - 1) * b_stage;
+    char* sb = sb0 + (kt % NSB) * BSLOT;
 #pragma unroll
     for (int j = 0; j < BI; ++j) {
       const int g = wave * BI + j;
-      dma16((NB == 2 && g * ROWS_PER_LD >= BN) ? src.b1 : src.b0, sb + g * 1024, b_off[j], kc * b_stage);
+      dma16((NB == 2 && g * ROWS_PER_LD >= BN) ? src.b1 : src.b0, sb + g * 1024, b_off[j], ko);
     }
   };
-
-  struct Frags {
-    i32x4_t a[FML > 0 ? FML : 1][2];
-    i32x4_t b[NB][FN][2];
+  using frag_a_t = i32x4_t[FML > 0 ? FML : 1];
+  using frag_b_t = i32x4_t[NB][FN];
+  auto read_frags = [&](int kt, int step, frag_a_t& af, frag_b_t& bfr) __attribute__((always_inline)) {
+    const char* sa = sa0 + (kt % NSA) * ASLOT;
+    const char* sb = sb0 + (kt % NSB) * BSLOT;
+    const int c = step * 2 + frag_c;
+#pragma unroll
+    for (int fm = 0; fm < FML; ++fm)
+      af[fm] = *reinterpret_cast<const i32x4_t*>(sa + swz<kRB>(tile_row<WM>(wm, fm) + frag_row, c));
+#pragma unroll
+    for (int h = 0; h < NB; ++h)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+        bfr[h][fn] = *reinterpret_cast<const i32x4_t*>(sb + swz<kRB>(h * BN + wn * WTN + fn * 32 + frag_row, c));
   };
-  // LDS offsets of this lane's fragment halves per step: the swizzle term is
-  // the same for all fragment rows of a lane (they differ by multiples of 32)
-  static_assert((BN / 2) % 8 == 0, "fragment rows share the swizzle term");
-  uint32_t abase[2][2], bbase[2][2];
+  auto mfmas = [&](const frag_a_t& af, const frag_b_t& bfr) __attribute__((always_inline)) {
 #pragma unroll
-  for (int step = 0; step < 2; ++step)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = step * 4 + frag_h + 2 * j;
-      abase[step][j] = swz<kRB>(tile_row(wm, 0) + frag_row, c);
-      bbase[step][j] = swz<kRB>(wn * WTN + frag_row, c);
-    }
-  auto read_frags = [&](int kt, int step, Frags& f) __attribute__((always_inline)) {
-    const char* sa = sa0 + (kt % kNSA) * ASLOT;
-    const char* sb = sb0 + (kt % kNSB) * BSLOT;
-    constexpr int kFragA = kWM * 32 * kRB;  // bytes between a lane's A fragment rows
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int fm = 0; fm < FML; ++fm)
-        f.a[fm][j] = *reinterpret_cast<const i32x4_t*>(sa + abase[step][j] + fm * kFragA);
+    for (int fm = 0; fm < FML; ++fm)
 #pragma unroll
       for (int h = 0; h < NB; ++h)
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn)
-          f.b[h][fn][j] = *reinterpret_cast<const i32x4_t*>(sb + bbase[step][j] + (h * BN + fn * 32) * kRB);
-    }
+          acc[h][fm][fn] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[fm], bfr[h][fn], acc[h][fm][fn], 0, 0, 0);
   };
-  auto mfmas = [&](const Frags& f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int fm = 0; fm < FML; ++fm)
-#pragma unroll
-        for (int h = 0; h < NB; ++h)
-#pragma unroll
-          for (int fn = 0; fn < FN; ++fn)
-            acc[h][fm][fn] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[fm][j], f.b[h][fn][j], acc[h][fm][fn], 0, 0, 0);
-  };
-  constexpr int NMF = 2 * FML * NB * FN;
-  constexpr int NRD = 2 * (FML + NB * FN);
-  // fragment reads spread under the MFMAs; in step 0 also the A loads
+  constexpr int NMF = FML * NB * FN;
+  constexpr int NRD = FML + NB * FN;
+  // one fragment read under each MFMA; after the barrier also the stage's loads
   auto interleave = [&](bool loads) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NMF; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (i < NRD) __builtin_amdgcn_sched_group_barrier(0x100, NMF < NRD ? 2 : 1, 0);
-      if (loads && i < AI) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (i < NRD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (loads && i < AI + BI) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   };
 
-  issue_a(0);
-  issue_b(0);
-  issue_b(1);
-  asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(BI, 15)) : "memory");  // A(0), B(0) landed
+  // Loads that may still be in flight once A(s) and B(s) have landed are those
+  // issued after A(s): B(s - NSA + NSB) at the same barrier (unless NSB == NSA,
+  // when that is B(s)), and all of the NSA - 1 (prologue) or NSA - 2 (loop)
+  // later barriers.
+  constexpr int VM_AFTER = NSB > NSA ? BI : 0;
+  constexpr int VM_FIRST = VM_AFTER + (NSA - 1) * (AI + BI);
+  constexpr int VM_STAGE = VM_AFTER + (NSA - 2) * (AI + BI);
+  static_assert(VM_FIRST < 64, "vmcnt range");
+#pragma unroll
+  for (int v = -NSB; v < 0; ++v) {
+    if (v + NSA >= 0) issue_a(v + NSA);
+    issue_b(v + NSB);
+  }
+  asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(VM_FIRST, 15)) : "memory");  // A(0), B(0) landed
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  Frags f[2];
-  if constexpr (FML > 0) read_frags(0, 0, f[0]);
-  for (int kt = 0; kt < nk; ++kt) {
-    issue_a(kt + 1);
+  frag_a_t af[2];
+  frag_b_t bf[2];
+  if constexpr (FML > 0) read_frags(0, 0, af[0], bf[0]);
+  auto step = [&](int kt, auto loads) __attribute__((always_inline)) {
+    constexpr bool kLoads = decltype(loads)::value;
     if constexpr (FML > 0) {
-      read_frags(kt, 1, f[1]);
-      mfmas(f[0]);
-      interleave(true);
+#pragma unroll
+      for (int ks = 0; ks + 1 < KS; ++ks) {
+        read_frags(kt, ks + 1, af[(ks + 1) & 1], bf[(ks + 1) & 1]);
+        mfmas(af[ks & 1], bf[ks & 1]);
+        interleave(false);
+      }
     }
-    issue_b(kt + 2);
-    // A(kt+1) and B(kt+1) have landed (B(kt+2) may still be in flight) and
-    // this wave's reads of stage kt are done
-    asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(BI, 0)) : "memory");
+    // A(kt+1) and B(kt+1) have landed and this wave's reads of stage kt are
+    // done, before any wave refills a slot (in the tail by draining the counter)
+    if constexpr (kLoads)
+      asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(VM_STAGE, 0)) : "memory");
+    else
+      asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(0, 0)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if constexpr (FML > 0) {
-      // past the last stage: a slot whose data is never used
-      read_frags(kt + 1, 0, f[0]);
-      mfmas(f[1]);
-      interleave(false);
+    if constexpr (kLoads) {
+      issue_a(kt + NSA);
+      issue_b(kt + NSB);
+    } else if constexpr (NSB > NSA) {
+      if (kt + NSA < nk) issue_a(kt + NSA);  // a stage still to come (uniform branch)
     }
-  }
+    if constexpr (FML > 0) {
+      // past the last stage this reads a slot whose data is not used
+      read_frags(kt + 1, 0, af[0], bf[0]);
+      mfmas(af[1], bf[1]);
+      interleave(kLoads);
+    }
+  };
+  int kt = 0;
+  for (; kt < nk - NSB; ++kt) step(kt, std::true_type{});
+  for (; kt < nk; ++kt) step(kt, std::false_type{});
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still target LDS when the workgroup ends
 }
 
 // One work item (row tile, N block): its K loop and its epilogue.  The
 // workgroup's LDS is free on entry and on return.
-template <int BN, int EPI>
+template <int BM, int BN, int WM, int WN, int NSA, int NSB, int EPI>
 __device__ __forceinline__ void gemm_i8_item(const I8GemmArgs& args, int w, int n_blocks, int dense_tiles, char* smem,
                                              int wave0) {
   constexpr int NB = (EPI == kEpiSwiGLU) ? 2 : 1;
   constexpr int BROWS = NB * BN;
-  constexpr int WTN = BN / kWN;
-  constexpr int FM = kBM / kWM / 32, FN = WTN / 32;
+  constexpr int WTN = BN / WN, NW = WM * WN;
+  constexpr int FM = BM / WM / 32, FN = WTN / 32;
   constexpr int ROWS_PER_LD = 1024 / kRB;
-  constexpr int AI = kBM / (kNW * ROWS_PER_LD), BI = BROWS / (kNW * ROWS_PER_LD);
-  constexpr int LDS_BYTES = kNSA * kBM * kRB + kNSB * BROWS * kRB;
+  constexpr int AI = BM / (NW * ROWS_PER_LD), BI = BROWS / (NW * ROWS_PER_LD);
+  static_assert(FM >= 1 && FM <= 5 && FN >= 1, "tile shape");
 
   constexpr bool kItemLoop = EPI == kEpiBF16;  // resident workgroups walk several items
   const int tid = kItemLoop ? item_thread_index(wave0) : static_cast<int>(threadIdx.x);
   const int lane = tid & (kWave - 1), wave = kItemLoop ? wave0 : __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave / kWN, wn = wave % kWN;
+  const int wm = wave / WN, wn = wave % WN;
 
   int e = 0, nb, lt, nrows;
   int64_t p0;
@@ -202,7 +224,8 @@ __device__ __forceinline__ void gemm_i8_item(const I8GemmArgs& args, int w, int 
   const int K = args.K;
 
   // the scale of tile row tid, kept through the K loop
-  const float my_scale = tid < kBM ? args.As[i8_a_row(args, p0 + (tid < nrows ? tid : nrows - 1))] : 0.f;
+  static_assert(BM <= 64 * NW, "one row scale per thread");
+  const float my_scale = tid < BM ? args.As[i8_a_row(args, p0 + (tid < nrows ? tid : nrows - 1))] : 0.f;
   // ---- byte offsets of the 16-byte chunks this lane fetches ----
   constexpr int CH = kRB / 16;
   uint32_t a_off[AI];
@@ -245,25 +268,50 @@ __device__ __forceinline__ void gemm_i8_item(const I8GemmArgs& args, int w, int 
       for (int fn = 0; fn < FN; ++fn) acc[h][fm][fn] = i32x16_t{};
 
   // 32-row blocks of this wave that hold tile rows (wave-uniform)
-  int fm_live = ((nrows + 31) / 32 - wm + kWM - 1) / kWM;
+  int fm_live = ((nrows + 31) / 32 - wm + WM - 1) / WM;
   fm_live = fm_live < 0 ? 0 : (fm_live > FM ? FM : fm_live);
   const int nk = K / kRB;
-  static_assert(FM == 2, "cases below");
   switch (fm_live) {
-    case 0:
-      k_loop_i8<BN, NB, 0, FM, FN, AI, BI>(smem, src, a_off, b_off, b_stage, nk, nrows, tid, wm, wn, acc);
-      break;
-    case 1:
-      k_loop_i8<BN, NB, 1, FM, FN, AI, BI>(smem, src, a_off, b_off, b_stage, nk, nrows, tid, wm, wn, acc);
-      break;
+#define MOE_CASE(n)                                                                                                \
+  case n:                                                                                                          \
+    if constexpr (n <= FM)                                                                                         \
+      k_loop_i8<BM, BN, WM, WN, NSA, NSB, NB, n, FM, FN, AI, BI>(smem, src, a_off, b_off, b_stage, nk, nrows, tid,   \
+                                                                 wm, wn, acc);                                     \
+    break;
+    MOE_CASE(0)
+    MOE_CASE(1)
+    MOE_CASE(2)
+    MOE_CASE(3)
+    MOE_CASE(4)
+    MOE_CASE(5)
+#undef MOE_CASE
     default:
-      k_loop_i8<BN, NB, 2, FM, FN, AI, BI>(smem, src, a_off, b_off, b_stage, nk, nrows, tid, wm, wn, acc);
       break;
   }
 
   // ---- epilogue: scales, then rows leave through LDS in 16-byte pieces ----
   // The MFMA layout gives lane l column l % 32 of rows 8*(r/4) + 4*(l/32) +
-  // r%4 of each 32 x 32 block.
+  // r%4 of each 32 x 32 block.  The tile (or a band of it) is written to LDS
+  // row by row, then copied out by all threads.
+  constexpr int ESZ = EPI == kEpiBF16 ? 2 : 4;
+  constexpr int CS = BN * ESZ + 16;                  // LDS row stride (padded against bank conflicts)
+  constexpr int SCALE_AT = ring_bytes(BM, BROWS, NSA, NSB) - BM * 4;  // row scales, past the staged band
+  constexpr int FMP_FIT = SCALE_AT / CS / (WM * 32);
+  constexpr int FMP = FMP_FIT < FM ? FMP_FIT : FM;   // 32-row blocks per row group and band
+  constexpr int NBANDS = (FM + FMP - 1) / FMP;
+  static_assert(FMP >= 1, "epilogue bands");
+  constexpr int BAND = FMP * WM * 32;
+  constexpr int CPR = BN * ESZ / 16, EPC = 16 / ESZ;  // chunks per row, elements per chunk
+  // In pass `it` of a band, wave w stores rows it * RSTEP + w * RPI + lane /
+  // CPR.  Each row's output row is found once, before any store, and passed
+  // on by a cross-lane read (a table load among the stores waits for them).
+  constexpr int RPI = 64 / CPR, RSTEP = RPI * NW;
+  static_assert(64 % CPR == 0 && BAND % RSTEP == 0, "copy-out mapping");
+  int row_entry = -1;
+  {
+    const int r = (lane / RPI) * RSTEP + wave * RPI + lane % RPI;
+    if (r < nrows) row_entry = static_cast<int>(i8_c_row(args, p0 + r));
+  }
   float sb[NB][FN];
 #pragma unroll
   for (int h = 0; h < NB; ++h)
@@ -274,136 +322,75 @@ __device__ __forceinline__ void gemm_i8_item(const I8GemmArgs& args, int w, int 
       sb[h][fn] = (h ? args.Bs1 : args.Bs0)[static_cast<int64_t>(e) * args.N + n];
     }
   __syncthreads();  // every wave is done with the K loop's LDS
-  constexpr int kScaleAt = LDS_BYTES - kBM * 4;  // row scales, past every staged tile
-  float* row_s = reinterpret_cast<float*>(smem + kScaleAt);
-  if (tid < kBM) row_s[tid] = my_scale;
+  float* row_s = reinterpret_cast<float*>(smem + SCALE_AT);
+  if (tid < BM) row_s[tid] = my_scale;
   __syncthreads();
-  auto value = [&](int h, int fm, int fn, int r, float s) {
-    return static_cast<float>(acc[h][fm][fn][r]) * s * sb[h][fn];
-  };
-  if constexpr (EPI == kEpiSwiGLU) {
-    constexpr int VS = BN * 4 + 16;  // fp32 row stride of the staged tile
-    static_assert(kBM * VS <= kScaleAt, "staged tile fits");
+  const bool whole = args.N % EPC == 0 && args.ldc % EPC == 0;
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
+  for (int band = 0; band < NBANDS; ++band) {
+    if (band > 0 && band * BAND >= nrows) break;  // workgroup-uniform
+#pragma unroll
+    for (int fm = band * FMP; fm < (band + 1) * FMP && fm < FM; ++fm) {
       if (fm >= fm_live) continue;  // wave-uniform
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
-        const int row0 = tile_row(wm, fm) + r4 * 8 + (lane >> 5) * 4;
+        const int row0 = tile_row<WM>(wm, fm) + r4 * 8 + (lane >> 5) * 4;
         const f32x4_t s = *reinterpret_cast<const f32x4_t*>(row_s + row0);
+        char* to = smem + (row0 - band * BAND) * CS;
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
+        for (int fn = 0; fn < FN; ++fn) {
+          const int col_l = wn * WTN + fn * 32 + (lane & 31);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float*>(smem + (row0 + i) * VS + (wn * WTN + fn * 32 + (lane & 31)) * 4) =
-                silu_mul(value(0, fm, fn, r4 * 4 + i, s[i]), value(NB - 1, fm, fn, r4 * 4 + i, s[i]));
-      }
-    }
-    __syncthreads();
-    constexpr int CPR = BN * 4 / 16;
-    for (int idx = tid; idx < nrows * CPR; idx += 64 * kNW) {
-      const int row = idx / CPR, ch = idx - row * CPR;
-      const int col = n0 + ch * 4;
-      const int64_t crow = i8_c_row(args, p0 + row);
-      if (col >= args.N || crow < 0) continue;  // N % 128 == 0: a chunk is all in or out
-      *reinterpret_cast<f32x4_t*>(static_cast<float*>(args.C) + crow * args.ldc + col) =
-          *reinterpret_cast<const f32x4_t*>(smem + row * VS + ch * 16);
-    }
-  } else if constexpr (EPI == kEpiF32) {
-    // one 128-row band per 32-row block index fm
-    constexpr int CS = BN * 4 + 16;
-    constexpr int BAND = kWM * 32;
-    static_assert(BAND * CS <= kScaleAt, "staged band fits");
-    constexpr int CPR = BN * 4 / 16;
-    const bool whole = args.N % 4 == 0 && args.ldc % 4 == 0;
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-      if (fm * BAND >= nrows) break;  // workgroup-uniform
-      if (fm > 0) __syncthreads();    // the previous band's copy-out is done with the LDS
-      if (fm < fm_live) {             // wave-uniform
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const int row_b = wm * 32 + r4 * 8 + (lane >> 5) * 4;
-          const f32x4_t s = *reinterpret_cast<const f32x4_t*>(row_s + fm * BAND + row_b);
-#pragma unroll
-          for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float*>(smem + (row_b + i) * CS + (wn * WTN + fn * 32 + (lane & 31)) * 4) =
-                  value(0, fm, fn, r4 * 4 + i, s[i]);
+          for (int i = 0; i < 4; ++i) {
+            float v = static_cast<float>(acc[0][fm][fn][r4 * 4 + i]) * s[i] * sb[0][fn];
+            if constexpr (EPI == kEpiSwiGLU)
+              v = silu_mul(v, static_cast<float>(acc[NB - 1][fm][fn][r4 * 4 + i]) * s[i] * sb[NB - 1][fn]);
+            if constexpr (ESZ == 4)
+              *reinterpret_cast<float*>(to + i * CS + col_l * 4) = v;
+            else
+              *reinterpret_cast<uint16_t*>(to + i * CS + col_l * 2) = f32_to_bf16(v);
+          }
         }
       }
-      __syncthreads();
-      const int band_rows = min(BAND, nrows - fm * BAND);
-      for (int idx = tid; idx < band_rows * CPR; idx += 64 * kNW) {
-        const int row = idx / CPR, ch = idx - row * CPR;
-        const int col = n0 + ch * 4;
-        const int64_t crow = i8_c_row(args, p0 + fm * BAND + row);
-        if (col >= args.N || crow < 0) continue;
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(smem + row * CS + ch * 16);
-        float* c = static_cast<float*>(args.C) + crow * args.ldc + col;
-        if (whole)
-          *reinterpret_cast<f32x4_t*>(c) = v;
-        else
-          for (int i = 0; i < 4 && col + i < args.N; ++i) c[i] = v[i];
-      }
-    }
-  } else {
-    constexpr int CS = BN * 2 + 16;  // bf16 row stride of the staged tile
-    static_assert(kBM * CS <= kScaleAt, "staged tile fits");
-    constexpr int CPR = BN * 2 / 16;
-    // In pass `it`, wave w stores tile rows it * RSTEP + w * RPI + lane / CPR.
-    // A row table's entries are read once, before any store, and passed on by
-    // a cross-lane read (a table load among the stores would wait for them).
-    constexpr int RPI = 64 / CPR, RSTEP = RPI * kNW;
-    static_assert(64 % CPR == 0 && kBM <= 64 * kNW, "copy-out mapping");
-    int row_entry = -1;
-    {
-      const int r = (lane / RPI) * RSTEP + wave * RPI + lane % RPI;
-      if (r < nrows) row_entry = static_cast<int>(i8_c_row(args, p0 + r));
-    }
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-      if (fm >= fm_live) continue;  // wave-uniform
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int row0 = tile_row(wm, fm) + r4 * 8 + (lane >> 5) * 4;
-        const f32x4_t s = *reinterpret_cast<const f32x4_t*>(row_s + row0);
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint16_t*>(smem + (row0 + i) * CS + (wn * WTN + fn * 32 + (lane & 31)) * 2) =
-                f32_to_bf16(value(0, fm, fn, r4 * 4 + i, s[i]));
-      }
     }
     __syncthreads();
-    const bool whole = args.N % 8 == 0 && args.ldc % 8 == 0;
-    for (int it = 0; it * RSTEP < nrows; ++it) {
-      const int row = it * RSTEP + wave * RPI + lane / CPR, ch = lane % CPR;
-      const int crow = __shfl(row_entry, it * RPI + lane / CPR);
-      const int col = n0 + ch * 8;
-      if (row >= nrows || col >= args.N || crow < 0) continue;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + row * CS + ch * 16);
-      uint16_t* c = static_cast<uint16_t*>(args.C) + static_cast<int64_t>(crow) * args.ldc + col;
-      if (whole)
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(c));
-      else
+    const int band_rows = min(BAND, nrows - band * BAND);
+    for (int it = 0; it * RSTEP < band_rows; ++it) {
+      const int row_b = it * RSTEP + wave * RPI + lane / CPR, ch = lane % CPR;
+      const int crow = __shfl(row_entry, (band * BAND / RSTEP + it) * RPI + lane / CPR);
+      const int col = n0 + ch * EPC;
+      if (row_b >= band_rows || col >= args.N || crow < 0) continue;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + row_b * CS + ch * 16);
+      char* dst = static_cast<char*>(args.C) + (static_cast<int64_t>(crow) * args.ldc + col) * ESZ;
+      if (whole) {
+        // bf16 rows are next read long after they leave the caches
+        if constexpr (ESZ == 2)
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst));
+        else
+          *reinterpret_cast<u32x4_t*>(dst) = v;
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col + i < args.N) c[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i % 2)));
+        for (int i = 0; i < EPC; ++i) {
+          if (col + i >= args.N) continue;
+          if constexpr (ESZ == 4)
+            reinterpret_cast<uint32_t*>(dst)[i] = v[i];
+          else
+            reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i % 2)));
+        }
+      }
     }
+    if (band + 1 < NBANDS) __syncthreads();  // the next band reuses the LDS
   }
 }
 
-// Work items are cut into 8 contiguous runs, one per XCD, as in the MXFP8
-// kernels: workgroup b takes item b / 8 of the run of XCD b mod 8, and the
-// bf16 epilogue's resident workgroups walk their run side by side, so that one
-// item's output stores drain under the next one's first loads.
-template <int BN, int EPI>
-__global__ __launch_bounds__(64 * kNW) void gemm_i8_kernel(const I8GemmArgs args, int dense_tiles) {
+// Work items are cut into 8 contiguous runs, one per XCD, as in the bf16 and
+// MXFP8 kernels: workgroup b takes item b / 8 of the run of XCD b mod 8, and
+// the bf16 epilogue's resident workgroups walk their run side by side, so that
+// one item's output stores drain under the next one's first loads.
+template <int BM, int BN, int WM, int WN, int NSA, int NSB, int EPI>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs args, int dense_tiles) {
   constexpr int NB = (EPI == kEpiSwiGLU) ? 2 : 1;
-  __shared__ __attribute__((aligned(1024))) char smem[kNSA * kBM * kRB + kNSB * NB * BN * kRB];
+  __shared__ __attribute__((aligned(1024))) char smem[ring_bytes(BM, NB * BN, NSA, NSB)];
   const int n_blocks = (args.N + BN - 1) / BN;
   const int xcd = static_cast<int>(blockIdx.x) % kXcds;
   int run0, len;
@@ -422,52 +409,118 @@ __global__ __launch_bounds__(64 * kNW) void gemm_i8_kernel(const I8GemmArgs args
   const int per_xcd = static_cast<int>(gridDim.x) / kXcds;  // the grid is a multiple of kXcds
   const int wave0 = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   if constexpr (EPI != kEpiBF16) {
-    if (first < len) gemm_i8_item<BN, EPI>(args, run0 + first, n_blocks, dense_tiles, smem, wave0);
+    if (first < len) gemm_i8_item<BM, BN, WM, WN, NSA, NSB, EPI>(args, run0 + first, n_blocks, dense_tiles, smem, wave0);
   } else {
     for (int local = first; local < len; local += per_xcd) {
       if (local > first) __syncthreads();  // the previous item's copy-out has read the LDS
-      gemm_i8_item<BN, EPI>(args, __builtin_amdgcn_readfirstlane(run0 + local), n_blocks, dense_tiles, smem, wave0);
+      gemm_i8_item<BM, BN, WM, WN, NSA, NSB, EPI>(args, __builtin_amdgcn_readfirstlane(run0 + local), n_blocks, dense_tiles,
+                                        smem, wave0);
     }
   }
 }
 
-template <int BN, int EPI>
+template <int BM, int BN, int WM, int WN, int NSA, int NSB, int EPI>
 hipError_t run_i8(const I8GemmArgs& a, hipStream_t stream) {
   const int64_t n_blocks = (a.N + BN - 1) / BN;
-  const int64_t dense_tiles = a.tiles ? 0 : (static_cast<int64_t>(a.dense_rows) + kBM - 1) / kBM;
+  const int64_t dense_tiles = a.tiles ? 0 : (static_cast<int64_t>(a.dense_rows) + BM - 1) / BM;
   const int64_t work = (a.tiles ? a.max_tiles : dense_tiles) * n_blocks;
   if (work <= 0) return hipSuccess;
   if (work > 0x7ffffff0) return hipErrorInvalidValue;
-  auto kernel = gemm_i8_kernel<BN, EPI>;
+  auto kernel = gemm_i8_kernel<BM, BN, WM, WN, NSA, NSB, EPI>;
   // with room for balanced runs of up to tile_run_cap tiles on every XCD
   int64_t cap = a.tiles ? int64_t(kXcds) * tile_run_cap(a.max_tiles) * n_blocks : work;
   if (EPI == kEpiBF16) {
     static std::atomic<int64_t> resident_cache{0};
     int64_t resident = resident_cache.load(std::memory_order_relaxed);
     if (resident <= 0) {
-      resident = resident_workgroups(reinterpret_cast<const void*>(kernel), 64 * kNW);
+      resident = resident_workgroups(reinterpret_cast<const void*>(kernel), 64 * WM * WN);
       if (resident <= 0) return hipErrorInvalidValue;
       resident_cache.store(resident, std::memory_order_relaxed);
     }
     cap = std::min(work, resident);
   }
   const int64_t grid = (cap + kXcds - 1) / kXcds * kXcds;
-  kernel<<<static_cast<unsigned>(grid), 64 * kNW, 0, stream>>>(a, static_cast<int>(dense_tiles));
+  kernel<<<static_cast<unsigned>(grid), 64 * WM * WN, 0, stream>>>(a, static_cast<int>(dense_tiles));
   return hipGetLastError();
 }
 
+// 320- and 256-row tiles: 8 waves, two per SIMD, 64 x 128 or 160 x 64 outputs
+// a wave.  128- and 64-row tiles: fewer outputs a workgroup, two workgroups or
+// more per CU.
+template <int EPI>
+hipError_t run_height(const I8GemmArgs& a, hipStream_t stream) {
+  constexpr int kHalf = EPI == kEpiSwiGLU ? 2 : 1;  // SwiGLU: gate and up share the columns of a tile
+  switch (a.tile_rows) {
+    case 320:
+      return run_i8<320, 256 / kHalf, 2, 4, 2, 2, EPI>(a, stream);
+    case 256:
+      return run_i8<256, 256 / kHalf, 4, 2, 2, 3, EPI>(a, stream);
+    case 128:
+      return run_i8<128, 128 / kHalf, 4, 2, 2, 3, EPI>(a, stream);
+    case 64:
+      return run_i8<64, 128 / kHalf, 2, 2, 2, 3, EPI>(a, stream);
+    default:
+      return hipErrorInvalidValue;
+  }
+}
+
 }  // namespace
+
+// Heights for `rows` rows spread over `groups` weight matrices of N rows.
+//
+// Routed, measured for whole layers (D x I, experts): up to 4 rows an expert
+// the few-rows kernel (7168 x 2048, 256 experts, 64 tokens: 1.68 ms against
+// 1.66 with 64-row tiles; 4 tokens: 0.30 against 0.34), up to 48 rows 64-row
+// tiles (512 tokens: 2.04 ms against 2.07 with 128 and 2.41 with the few-rows
+// kernel), then by how many rounds of 256-row items the chip runs: with five or
+// more, 256-row tiles (2048 tokens: 2.43 against 2.49 ms with 128), 320-row ones
+// where segments of about 256 rows would often need two (8192 tokens: 4.32 ms
+// against 4.69 with 256 and 5.29 with 128); with fewer, 128-row tiles, whose
+// items fill the last round better (2048 x 768, 128 experts, 4096 tokens: 0.50
+// ms against 0.51; 2048 tokens: 0.32 against 0.37).
+//
+// Dense: the few-rows kernel while its workgroups fit the chip at once (256 x
+// 2048 x 7168: 24 us against 32 with 64-row tiles), else the least rounds times
+// the measured cost of a round (us per 128-byte stage: 64-row tiles 0.94 with
+// two workgroups on every CU and 0.57 with one, 128-row tiles 1.49 and 0.80,
+// 256-row 1.85, 320-row 2.2).
+int i8_tile_rows(int64_t rows, int64_t groups, int64_t N) {
+  const int64_t known = device_compute_units(), cus = known > 0 ? known : 256;
+  auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  if (groups > 1) {
+    if (rows <= 4 * groups) return kI8RowsBM;
+    if (rows <= 48 * groups) return 64;
+    const int64_t items = groups * ceil_div(rows, 256 * groups) * ceil_div(N, 128);
+    if (items < 5 * cus) return 128;
+    return rows >= 192 * groups && rows <= 320 * groups ? 320 : 256;
+  }
+  if (ceil_div(rows, kI8RowsBM) * ceil_div(N, 64) <= cus) return kI8RowsBM;
+  int best = 0;
+  double least = 0.0;
+  auto consider = [&](int bm, int bn, int per_cu, double one, double full) {
+    const int64_t items = ceil_div(rows, bm) * ceil_div(N, bn);
+    const double cost = items <= cus ? one : static_cast<double>(ceil_div(items, per_cu * cus)) * full;
+    if (!best || cost < least) {
+      best = bm;
+      least = cost;
+    }
+  };
+  consider(64, 128, 2, 0.57, 0.94);
+  consider(128, 128, 2, 0.80, 1.49);
+  consider(256, 256, 1, 1.85, 1.85);
+  consider(320, 256, 1, 2.2, 2.2);
+  return best;
+}
 
 hipError_t launch_gemm_i8_tiles(const I8GemmArgs& a, int epilogue, hipStream_t stream) {
   if (a.tiles && !a.tile_runs) return hipErrorInvalidValue;
   switch (epilogue) {
     case kEpiSwiGLU:
-      if (a.N % 4 || a.ldc % 4) return hipErrorInvalidValue;
-      return run_i8<128, kEpiSwiGLU>(a, stream);
+      return run_height<kEpiSwiGLU>(a, stream);
     case kEpiBF16:
-      return run_i8<256, kEpiBF16>(a, stream);
+      return run_height<kEpiBF16>(a, stream);
     case kEpiF32:
-      return run_i8<256, kEpiF32>(a, stream);
+      return run_height<kEpiF32>(a, stream);
     default:
       return hipErrorInvalidValue;
   }

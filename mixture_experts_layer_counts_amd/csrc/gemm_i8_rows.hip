@@ -179,7 +179,7 @@ hipError_t launch_gemm_i8(const I8GemmArgs& a, int epilogue, hipStream_t stream)
   for (const void* p : {static_cast<const void*>(a.A), static_cast<const void*>(a.B0),
                         static_cast<const void*>(epilogue == kEpiSwiGLU ? a.B1 : a.B0), static_cast<const void*>(a.C)})
     if (!p || reinterpret_cast<uintptr_t>(p) % 16) return hipErrorInvalidValue;
-  if (a.tile_rows == kI8BM) return launch_gemm_i8_tiles(a, epilogue, stream);
+  if (a.tile_rows != kI8RowsBM) return launch_gemm_i8_tiles(a, epilogue, stream);
   switch (epilogue) {
     case kEpiSwiGLU:
       return run_rows<2, kEpiSwiGLU>(a, stream);

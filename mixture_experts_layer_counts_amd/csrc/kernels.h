@@ -185,7 +185,7 @@ struct I8GemmArgs {
   const int32_t* tile_count;
   const int32_t* tile_runs;
   int max_tiles;
-  int tile_rows;  // height of the tile lists, which picks the kernel: kI8RowsBM or kI8BM
+  int tile_rows;  // height of the tile lists, which picks the kernel (i8_tile_rows)
   int dense_rows;
 };
 // Rows outside the operand (a table not built by the schedule kernels) read
@@ -199,9 +199,9 @@ __device__ __forceinline__ int64_t i8_c_row(const I8GemmArgs& a, int64_t p) {
   return r >= 0 && r < a.c_rows ? r : -1;
 }
 constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel (gemm_i8_rows.hip)
-constexpr int kI8BM = 256;     // tile rows of the LDS-staged kernel (gemm_i8.hip)
-// Tile height for `rows` rows spread over `groups` weight matrices.
-inline int i8_tile_rows(int64_t rows, int64_t groups) { return rows > 32 * groups ? kI8BM : kI8RowsBM; }
+// Tile height for `rows` rows spread over `groups` weight matrices: that of the
+// few-rows kernel, or 64, 128, 256 or 320 (gemm_i8.hip).
+int i8_tile_rows(int64_t rows, int64_t groups, int64_t N);
 hipError_t launch_gemm_i8_tiles(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 

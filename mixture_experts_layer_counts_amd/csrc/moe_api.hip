@@ -116,7 +116,7 @@ Layout layout_of(const moe_shape* s) {
   const moe::RoutedTiling tiling = s->precision == MOE_MXFP8
                                        ? moe::RoutedTiling{moe::gemm_mx_routed_bm(), 0, 0}
                                    : s->precision == MOE_INT8
-                                       ? moe::RoutedTiling{moe::i8_tile_rows(mb_rows, Lx), 0, 0}
+                                       ? moe::RoutedTiling{moe::i8_tile_rows(mb_rows, Lx, s->I), 0, 0}
                                        : moe::gemm_routed_tiling(mb_rows, s->max_rows, Lx, s->I, s->D,
                                                                  s->pipeline != 0);
   const int bm = tiling.bm;
@@ -488,7 +488,7 @@ moe::I8GemmArgs dense_i8(const int8_t* A, const float* As, int64_t M, const void
   g.C = C;
   g.ldc = N;
   g.c_rows = M;
-  g.tile_rows = moe::i8_tile_rows(M, 1);
+  g.tile_rows = moe::i8_tile_rows(M, 1, N);
   g.dense_rows = static_cast<int>(M);
   return g;
 }
