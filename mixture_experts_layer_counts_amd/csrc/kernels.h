@@ -204,6 +204,8 @@ constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel (gemm_i8_rows
 int i8_tile_rows(int64_t rows, int64_t groups, int64_t N);
 hipError_t launch_gemm_i8_tiles(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
+// Two few-rows products in one launch: both SwiGLU, or bf16 and fp32.
+hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream);
 
 // Rows of bf16 or fp32 [.][K] -> int8 [.][Kp] (zeros past K) and one scale per
 // row.  Row i of the launch goes to row i, or with `sched` schedule position p
@@ -222,6 +224,9 @@ struct QuantI8Args {
   int* err;
 };
 hipError_t launch_quantize_rows_i8(const QuantI8Args& args, bool src_f32, int64_t rows, hipStream_t stream);
+// The rows of two fp32 matrices in one launch.
+hipError_t launch_quantize_two_i8(const QuantI8Args& a, int64_t rows_a, const QuantI8Args& b, int64_t rows_b,
+                                  hipStream_t stream);
 
 // Tiling of the routed bf16 GEMMs for minibatches of mb_rows rows, max_rows
 // routed rows in all over `experts` local experts, intermediate width I and

@@ -460,9 +460,9 @@ hipError_t routed_minibatch_mx(const moe_shape* shape, const moe_weights* w, con
   return moe::launch_gemm_mx(d, moe::kEpiBF16, s);
 }
 
-// The K-quantised rows of a [rows, K] matrix, in place order.
-hipError_t quantize_i8(const void* src, bool src_f32, int64_t rows, int64_t K, int8_t* q, float* scale, hipStream_t s,
-                       const int32_t* limit = nullptr, int64_t p_begin = 0) {
+// Rows of a [rows, K] matrix quantised in place order.
+moe::QuantI8Args quant_args(const void* src, int64_t K, int8_t* q, float* scale, const int32_t* limit = nullptr,
+                            int64_t p_begin = 0) {
   moe::QuantI8Args a{};
   a.src = src;
   a.K = a.Kp = K;
@@ -470,7 +470,7 @@ hipError_t quantize_i8(const void* src, bool src_f32, int64_t rows, int64_t K, i
   a.scale = scale;
   a.limit = limit;
   a.p_begin = p_begin;
-  return moe::launch_quantize_rows_i8(a, src_f32, rows, s);
+  return a;
 }
 
 // C = A B^T of quantised rows, dense.
@@ -493,76 +493,48 @@ moe::I8GemmArgs dense_i8(const int8_t* A, const float* As, int64_t M, const void
   return g;
 }
 
-// The shared expert in int8: x quantised per token, up/gate with SwiGLU into
-// fp32 h, h quantised per token, down into fp32 rows for the combine.
-hipError_t shared_expert_i8(const moe_shape* shape, const moe_weights* w, const void* x_local, const Layout& L,
-                            void* ws, hipStream_t s) {
+// An int8 FFN over some rows: x's rows, the up/gate product with SwiGLU into
+// fp32 h, h's rows, and the down product.
+struct I8Ffn {
+  moe::I8GemmArgs up, down;
+  moe::QuantI8Args h;
+  int64_t h_rows;
+  int down_epi;
+};
+
+// The shared expert: x quantised per token, h quantised per token, fp32 rows
+// for the combine.
+I8Ffn shared_ffn_i8(const moe_shape* shape, const moe_weights* w, const int8_t* xq, const float* xs, const Layout& L,
+                    void* ws) {
   const int64_t T = shape->T, D = shape->D, Is = shape->I_shared;
-  int8_t* xq = at<int8_t>(ws, L.xs_q);
-  float* xs = at<float>(ws, L.xs_s);
-  int8_t* hq = at<int8_t>(ws, L.h_shared);
-  float* hs = at<float>(ws, L.hs_s);
+  I8Ffn f{};
   float* h32 = at<float>(ws, L.hs32);
-  {
-    ProbeScope probe(MOE_K_SHARED_UP, s);
-    hipError_t e = quantize_i8(x_local, false, T, D, xq, xs, s);
-    if (e != hipSuccess) return e;
-    moe::I8GemmArgs u = dense_i8(xq, xs, T, w->ws_gate, w->ss_gate, Is, D, h32);
-    u.B1 = static_cast<const int8_t*>(w->ws_up);
-    u.Bs1 = reinterpret_cast<const float*>(w->ss_up);
-    e = moe::launch_gemm_i8(u, moe::kEpiSwiGLU, s);
-    if (e != hipSuccess) return e;
-  }
-  ProbeScope probe(MOE_K_SHARED_DOWN, s);
-  hipError_t e = quantize_i8(h32, true, T, Is, hq, hs, s);
-  if (e != hipSuccess) return e;
-  return moe::launch_gemm_i8(dense_i8(hq, hs, T, w->ws_down, w->ss_down, D, Is, at<float>(ws, L.shared_out)),
-                             moe::kEpiF32, s);
+  f.up = dense_i8(xq, xs, T, w->ws_gate, w->ss_gate, Is, D, h32);
+  f.up.B1 = static_cast<const int8_t*>(w->ws_up);
+  f.up.Bs1 = reinterpret_cast<const float*>(w->ss_up);
+  f.h = quant_args(h32, Is, at<int8_t>(ws, L.h_shared), at<float>(ws, L.hs_s));
+  f.h_rows = T;
+  f.down = dense_i8(f.h.q, f.h.scale, T, w->ws_down, w->ss_down, D, Is, at<float>(ws, L.shared_out));
+  f.down_epi = moe::kEpiF32;
+  return f;
 }
 
-// One minibatch of the routed experts in int8.  With one source rank every
-// token was quantised once (first minibatch) and the up/gate GEMM reads its
-// rows through the schedule table; with several the routed rows are quantised
-// into ring slots.
-hipError_t routed_minibatch_i8(const moe_shape* shape, const moe_weights* w, const void* x_src,
-                               const int32_t* sched_src, const int32_t* expert_offsets, const Layout& L, void* ws,
-                               int64_t m, int64_t p_begin, int64_t rows, hipStream_t s) {
-  const int64_t D = shape->D, I = shape->I, C = shape->ring_rows, R = shape->num_src_ranks;
-  const int32_t* limit = expert_offsets + shape->experts_per_rank;
-  int8_t* xq = at<int8_t>(ws, L.ring);
-  float* xs = at<float>(ws, L.ring_s);
-  int8_t* hq = at<int8_t>(ws, L.h);
-  float* hs = at<float>(ws, L.h_s);
+// One minibatch of the routed experts.  With one source rank the tokens are
+// quantised once and up/gate reads its rows through the schedule table; with
+// several the routed rows are quantised into ring slots.
+I8Ffn routed_ffn_i8(const moe_shape* shape, const moe_weights* w, const int32_t* sched_src,
+                    const int32_t* expert_offsets, const Layout& L, void* ws, int64_t m, int64_t p_begin,
+                    int64_t rows) {
+  const int64_t D = shape->D, I = shape->I, R = shape->num_src_ranks;
+  I8Ffn f{};
   float* h32 = at<float>(ws, L.h32);
-  if (R > 1 || m == 0) {
-    ProbeScope probe(MOE_K_GATHER, s);
-    hipError_t e;
-    if (R == 1) {
-      e = quantize_i8(x_src, false, shape->T, D, xq, xs, s);
-    } else {
-      moe::QuantI8Args a{};
-      a.src = x_src;
-      a.K = a.Kp = D;
-      a.q = xq;
-      a.scale = xs;
-      a.limit = limit;
-      a.p_begin = p_begin;
-      a.sched = sched_src;
-      a.k = static_cast<int>(shape->k);
-      a.src_rows = R * shape->T;
-      a.ring_rows = C;
-      a.err = at<int>(ws, L.err);
-      e = moe::launch_quantize_rows_i8(a, false, rows, s);
-    }
-    if (e != hipSuccess) return e;
-  }
-  moe::I8GemmArgs u{};
-  u.A = xq;
-  u.As = xs;
-  u.a_rows = R == 1 ? shape->T : C;
+  moe::I8GemmArgs& u = f.up;
+  u.A = at<int8_t>(ws, L.ring);
+  u.As = at<float>(ws, L.ring_s);
+  u.a_rows = R == 1 ? shape->T : shape->ring_rows;
   u.a_idx = R == 1 ? sched_src : nullptr;
   u.a_div = static_cast<int>(shape->k);
-  u.a_mod = C;
+  u.a_mod = shape->ring_rows;
   u.B0 = static_cast<const int8_t*>(w->w_gate);
   u.B1 = static_cast<const int8_t*>(w->w_up);
   u.Bs0 = reinterpret_cast<const float*>(w->s_gate);
@@ -579,17 +551,12 @@ hipError_t routed_minibatch_i8(const moe_shape* shape, const moe_weights* w, con
   u.tile_runs = at<int32_t>(ws, L.tile_runs) + m * moe::kTileRunBounds;
   u.max_tiles = L.max_tiles;
   u.tile_rows = L.routed_bm;
-  {
-    ProbeScope probe(MOE_K_UP_GATE, s);
-    const hipError_t e = moe::launch_gemm_i8(u, moe::kEpiSwiGLU, s);
-    if (e != hipSuccess) return e;
-  }
-  ProbeScope probe(MOE_K_DOWN, s);
-  const hipError_t e = quantize_i8(h32, true, rows, I, hq, hs, s, limit, p_begin);
-  if (e != hipSuccess) return e;
-  moe::I8GemmArgs d = u;
-  d.A = hq;
-  d.As = hs;
+  f.h = quant_args(h32, I, at<int8_t>(ws, L.h), at<float>(ws, L.h_s), expert_offsets + shape->experts_per_rank, p_begin);
+  f.h_rows = rows;
+  moe::I8GemmArgs& d = f.down;
+  d = u;
+  d.A = f.h.q;
+  d.As = f.h.scale;
   d.a_rows = rows;
   d.a_idx = nullptr;
   d.a_sub = p_begin;
@@ -606,7 +573,80 @@ hipError_t routed_minibatch_i8(const moe_shape* shape, const moe_weights* w, con
   d.c_rows = L.y_rows;
   d.c_idx = R == 1 ? sched_src : nullptr;
   d.c_sub = 0;
-  return moe::launch_gemm_i8(d, moe::kEpiBF16, s);
+  f.down_epi = moe::kEpiBF16;
+  return f;
+}
+
+hipError_t run_ffn_i8(const I8Ffn& f, int up_id, int down_id, hipStream_t s) {
+  {
+    ProbeScope probe(up_id, s);
+    const hipError_t e = moe::launch_gemm_i8(f.up, moe::kEpiSwiGLU, s);
+    if (e != hipSuccess) return e;
+  }
+  ProbeScope probe(down_id, s);
+  const hipError_t e = moe::launch_quantize_rows_i8(f.h, true, f.h_rows, s);
+  return e == hipSuccess ? moe::launch_gemm_i8(f.down, f.down_epi, s) : e;
+}
+
+// The int8 experts of moe_forward: those of the routed and the shared expert
+// that are int8.  `shared` and `routed` say which.
+hipError_t experts_i8(const moe_shape* shape, const moe_weights* w, const void* x_src, const void* x_local,
+                      const int32_t* sched_src, const int32_t* expert_offsets, const Layout& L, void* ws, bool shared,
+                      bool routed, hipStream_t s) {
+  const int64_t T = shape->T, D = shape->D, b = shape->minibatch_rows, R = shape->num_src_ranks;
+  int8_t* rq = at<int8_t>(ws, L.ring);
+  float* rs = at<float>(ws, L.ring_s);
+  const bool tokens = routed && R == 1;  // the routed experts read the tokens' quantised rows
+  if (tokens) {
+    ProbeScope probe(MOE_K_GATHER, s);
+    const hipError_t e = moe::launch_quantize_rows_i8(quant_args(x_src, D, rq, rs), false, T, s);
+    if (e != hipSuccess) return e;
+  }
+  const bool same_x = tokens && x_src == x_local;
+  I8Ffn sh{};
+  if (shared) {
+    int8_t* xq = same_x ? rq : at<int8_t>(ws, L.xs_q);
+    float* xs = same_x ? rs : at<float>(ws, L.xs_s);
+    if (!same_x) {
+      ProbeScope probe(MOE_K_SHARED_UP, s);
+      const hipError_t e = moe::launch_quantize_rows_i8(quant_args(x_local, D, xq, xs), false, T, s);
+      if (e != hipSuccess) return e;
+    }
+    sh = shared_ffn_i8(shape, w, xq, xs, L, ws);
+    // a few tokens: the shared expert rides in the routed experts' launches
+    if (tokens && L.n_minibatches == 1 && L.routed_bm == moe::kI8RowsBM && sh.up.tile_rows == moe::kI8RowsBM &&
+        sh.down.tile_rows == moe::kI8RowsBM) {
+      const I8Ffn f = routed_ffn_i8(shape, w, sched_src, expert_offsets, L, ws, 0, 0, shape->max_rows);
+      {
+        ProbeScope probe(MOE_K_UP_GATE, s);
+        const hipError_t e = moe::launch_gemm_i8_pair(f.up, moe::kEpiSwiGLU, sh.up, moe::kEpiSwiGLU, s);
+        if (e != hipSuccess) return e;
+      }
+      ProbeScope probe(MOE_K_DOWN, s);
+      const hipError_t e = moe::launch_quantize_two_i8(f.h, f.h_rows, sh.h, sh.h_rows, s);
+      return e == hipSuccess ? moe::launch_gemm_i8_pair(f.down, f.down_epi, sh.down, sh.down_epi, s) : e;
+    }
+    const hipError_t e = run_ffn_i8(sh, MOE_K_SHARED_UP, MOE_K_SHARED_DOWN, s);
+    if (e != hipSuccess) return e;
+  }
+  for (int64_t m = 0; routed && m < L.n_minibatches; ++m) {
+    const int64_t p_begin = m * b, rows = std::min<int64_t>(b, shape->max_rows - p_begin);
+    if (R > 1) {
+      ProbeScope probe(MOE_K_GATHER, s);
+      moe::QuantI8Args a = quant_args(x_src, D, rq, rs, expert_offsets + shape->experts_per_rank, p_begin);
+      a.sched = sched_src;
+      a.k = static_cast<int>(shape->k);
+      a.src_rows = R * T;
+      a.ring_rows = shape->ring_rows;
+      a.err = at<int>(ws, L.err);
+      const hipError_t e = moe::launch_quantize_rows_i8(a, false, rows, s);
+      if (e != hipSuccess) return e;
+    }
+    const hipError_t e = run_ffn_i8(routed_ffn_i8(shape, w, sched_src, expert_offsets, L, ws, m, p_begin, rows),
+                                    MOE_K_UP_GATE, MOE_K_DOWN, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -797,9 +837,7 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   //    it needs no dispatch, so it goes first)
   if (T > 0 && shared_mx) {
     MOE_TRY_HIP(shared_expert_mx(shape, w, x_local, L, ws, s));
-  } else if (T > 0 && shared_i8) {
-    MOE_TRY_HIP(shared_expert_i8(shape, w, x_local, L, ws, s));
-  } else if (T > 0) {
+  } else if (T > 0 && !shared_i8) {
     moe::GemmArgs g{};
     g.k_splits = 1;
     g.A = static_cast<const uint16_t*>(x_local);
@@ -939,17 +977,13 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
       ProbeScope probe(MOE_K_PIPELINE, s);
       MOE_TRY_HIP(moe::launch_pipeline(pa, moe::RoutedTiling{L.routed_bm, L.bn_up, L.bn_down}, s));
     }
-  } else {
+  } else if (!i8) {
     for (int64_t m = 0; m < L.n_minibatches; ++m) {
       const int64_t p_begin = m * b;
       const int64_t rows = std::min<int64_t>(b, shape->max_rows - p_begin);
       if (mx) {
         MOE_TRY_HIP(
             routed_minibatch_mx(shape, w, x_src, sched_src, expert_offsets, route_dst, L, ws, m, p_begin, rows, s));
-        continue;
-      }
-      if (i8) {
-        MOE_TRY_HIP(routed_minibatch_i8(shape, w, x_src, sched_src, expert_offsets, L, ws, m, p_begin, rows, s));
         continue;
       }
       MOE_TRY_HIP(gather(m));
@@ -961,6 +995,9 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
       MOE_TRY_HIP(moe::launch_gemm(down_args(m, h), moe::kEpiBF16, s));
     }
   }
+
+  if (i8 || shared_i8)
+    MOE_TRY_HIP(experts_i8(shape, w, x_src, x_local, sched_src, expert_offsets, L, ws, shared_i8 && T > 0, i8, s));
 
   // 4. fixed-order gate-weighted combine
   ProbeScope probe(MOE_K_COMBINE, s);
@@ -1016,12 +1053,8 @@ moe_status moe_quantize_int8(const void* src, int32_t src_dtype, int64_t rows, i
       reinterpret_cast<uintptr_t>(scale) % 4)
     return MOE_ERR_INVALID_ARG;
   if (rows >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
-  moe::QuantI8Args a{};
-  a.src = src;
-  a.K = K;
+  moe::QuantI8Args a = quant_args(src, K, q, scale);
   a.Kp = (K + 127) / 128 * 128;
-  a.q = q;
-  a.scale = scale;
   return hip_status(moe::launch_quantize_rows_i8(a, f32, rows, static_cast<hipStream_t>(stream)));
 }
 

@@ -38,22 +38,49 @@ __device__ __forceinline__ void load_chunk(const T* __restrict__ src, int64_t c,
   }
 }
 
-// round(127 v / m), ties to even.  r = 127 / m in fp64 leaves the product on
-// the wrong side of a half only when the quotient is within 2^-50 of it; the
-// remainder 127 v - q m is exact in fp64 and decides those.
-__device__ __forceinline__ int quotient(float v, float m, double r) {
-  const double x = static_cast<double>(v);
-  double q = rint(x * r);
-  const double d2 = 2.0 * fma(-q, static_cast<double>(m), 127.0 * x);
+// round(127 v / m), ties to even, exactly: the remainder 127 v - q m is exact in
+// fp64 and decides the values whose quotient is next to a half.
+__device__ __forceinline__ int exact_quotient(float v, float m) {
+  const double x = 127.0 * static_cast<double>(v);
+  double q = rint(x / static_cast<double>(m));
+  const double d2 = 2.0 * fma(-q, static_cast<double>(m), x);
   const bool odd = static_cast<int>(q) & 1;
   if (d2 > m || (d2 == m && odd)) q += 1.0;
   if (d2 < -m || (d2 == -m && odd)) q -= 1.0;
   return static_cast<int>(q);
 }
 
+// Eight quotients as bytes.  In fp32 the quotient v r with r = 127 / m is off by
+// at most 127 2^-23 (r's rounding and the product's), so it is right unless it
+// lies within 2^-15 of a half; adding 1.5 2^23 rounds it to an integer in the
+// sum's low bits.  The exact form then redoes the chunks that hold such a
+// value, one in a thousand or so, and rows whose r would leave fp32's range.
+// (fp64 throughout took 59 us for 8192 x 7168 bf16, bound by arithmetic.)
+__device__ __forceinline__ uint2 quotients(const float (&v)[kChunk], float m, float r, bool exact) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t b[kChunk];
+  float near = 1.f;
+#pragma unroll
+  for (int e = 0; e < kChunk; ++e) {
+    const float y = fmaf(v[e], r, kMagic);
+    b[e] = __float_as_uint(y);
+    const float f = fmaf(v[e], r, kMagic - y);  // the fraction, in [-0.5, 0.5]
+    near = fminf(near, 0.5f - fabsf(f));
+  }
+  if (exact || near < 0x1p-15f) {
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) b[e] = static_cast<uint32_t>(exact_quotient(v[e], m));
+  }
+  auto pack = [&](int i) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[i + 3], b[i + 2], 0x0c0c0400u);
+    return lo | (hi << 16);
+  };
+  return make_uint2(pack(0), pack(4));
+}
+
 template <bool VEC, typename T>
-__global__ __launch_bounds__(kThreads) void quantize_rows_i8_kernel(const QuantI8Args a) {
-  const int64_t i = blockIdx.x;
+__device__ __forceinline__ void quantize_row(const QuantI8Args& a, int64_t i) {
   int64_t from = i, to = i;
   if (a.limit && a.p_begin + i >= *a.limit) return;  // behind the last routed row
   if (a.sched) {
@@ -106,18 +133,13 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_i8_kernel(const QuantI
 #pragma unroll
   for (int w = 0; w < kThreads / kWave; ++w) bits = part[w] > bits ? part[w] : bits;
 
-  const bool finite = bits < 0x7f800000u;
+  const bool some = bits && bits < 0x7f800000u;  // neither all zero nor not finite
   const float m = __uint_as_float(bits);
-  const double r = finite && bits ? 127.0 / static_cast<double>(m) : 0.0;
-  if (tid == 0) a.scale[to] = finite ? m / 127.f : __uint_as_float(0x7fc00000u);
+  if (tid == 0) a.scale[to] = bits < 0x7f800000u ? m / 127.f : __uint_as_float(0x7fc00000u);
+  const float r = some ? 127.f / m : 0.f;
+  const bool exact = some && m < 0x1p-100f;  // r past fp32's range, or close
   auto put = [&](int64_t c, const float(&w)[kChunk]) {
-    uint32_t out[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      const int n = finite && bits ? quotient(w[e], m, r) : 0;
-      out[e / 4] |= (static_cast<uint32_t>(n) & 0xffu) << (8 * (e % 4));
-    }
-    *reinterpret_cast<uint2*>(q + c * kChunk) = make_uint2(out[0], out[1]);
+    *reinterpret_cast<uint2*>(q + c * kChunk) = some ? quotients(w, m, r, exact) : make_uint2(0, 0);
   };
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) {
@@ -131,12 +153,40 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_i8_kernel(const QuantI
   }
 }
 
+template <bool VEC, typename T>
+__global__ __launch_bounds__(kThreads) void quantize_rows_i8_kernel(const QuantI8Args a) {
+  quantize_row<VEC, T>(a, blockIdx.x);
+}
+
+// The rows of two matrices in one launch: the first rows0 workgroups take a's.
+__global__ __launch_bounds__(kThreads) void quantize_two_i8_kernel(const QuantI8Args a, const QuantI8Args b,
+                                                                   int rows0) {
+  const int i = blockIdx.x;
+  if (i < rows0)
+    quantize_row<true, float>(a, i);
+  else
+    quantize_row<true, float>(b, i - rows0);
+}
+
+bool valid(const QuantI8Args& a) {
+  return a.K > 0 && a.Kp >= a.K && a.Kp % 16 == 0 && reinterpret_cast<uintptr_t>(a.q) % 8 == 0;
+}
+
 }  // namespace
+
+hipError_t launch_quantize_two_i8(const QuantI8Args& a, int64_t rows_a, const QuantI8Args& b, int64_t rows_b,
+                                  hipStream_t stream) {
+  if (rows_a <= 0 || rows_b <= 0 || rows_a + rows_b > 0x7fffffff || !valid(a) || !valid(b)) return hipErrorInvalidValue;
+  for (const QuantI8Args* x : {&a, &b})
+    if (x->K % 4 || reinterpret_cast<uintptr_t>(x->src) % 16) return hipErrorInvalidValue;
+  quantize_two_i8_kernel<<<static_cast<unsigned>(rows_a + rows_b), kThreads, 0, stream>>>(a, b,
+                                                                                          static_cast<int>(rows_a));
+  return hipGetLastError();
+}
 
 hipError_t launch_quantize_rows_i8(const QuantI8Args& a, bool src_f32, int64_t rows, hipStream_t stream) {
   if (rows <= 0) return hipSuccess;
-  if (rows > 0x7fffffff || a.K <= 0 || a.Kp < a.K || a.Kp % 16 || reinterpret_cast<uintptr_t>(a.q) % 8)
-    return hipErrorInvalidValue;
+  if (rows > 0x7fffffff || !valid(a)) return hipErrorInvalidValue;
   const int64_t per16 = src_f32 ? 4 : 8;  // elements in 16 bytes
   const bool vec = a.K % per16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
   const dim3 grid(static_cast<unsigned>(rows)), block(kThreads);
