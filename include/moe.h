@@ -483,6 +483,18 @@ moe_status moe_quantize_int8(const void* src, int32_t src_dtype, int64_t rows, i
 moe_status moe_matmul_int8(const int8_t* a, const float* a_scale, int64_t M, const int8_t* b, const float* b_scale,
                            int64_t N, int64_t K, void* out, int32_t out_dtype, void* stream);
 
+/*
+ * moe_quantize_int8 of x [M, K] (bf16 or fp32) followed by moe_matmul_int8 with
+ * weights w [N, Kp] and scales w_scale [N] as moe_quantize_int8 writes them from
+ * [N, K] (Kp = K rounded up to 128): the same bits, in one launch for a few
+ * rows.  ws: device workspace of moe_linear_int8_workspace_bytes, 16-byte
+ * aligned (NULL where that is 0).  w and out 16-byte aligned, x to its element.
+ */
+moe_status moe_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+moe_status moe_linear_int8(const void* x, int32_t x_dtype, int64_t M, int64_t K, const int8_t* w,
+                           const float* w_scale, int64_t N, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                           void* stream);
+
 /* Read the sticky device error word (MOE_DEVERR_* bits).  SYNCHRONISES the
  * stream: diagnostics only, never on the hot path. */
 moe_status moe_get_device_error(const moe_shape* shape, const void* ws, size_t ws_bytes,

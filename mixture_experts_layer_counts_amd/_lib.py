@@ -92,6 +92,10 @@ _SIGS = {
     "moe_quantize_int8": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]),
     "moe_matmul_int8": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, _P, ctypes.c_int64, ctypes.c_int64, _P,
                                        ctypes.c_int32, _P]),
+    "moe_linear_int8_workspace_bytes": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_linear_int8": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_int64,
+                                       _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "moe_get_device_error": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.c_size_t, _P,
                                             ctypes.POINTER(ctypes.c_int32)]),
     "moe_backward_prepare": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights), _P,

@@ -7,6 +7,7 @@ of the work.  Names follow include/moe.h: ``route``, ``schedule``,
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Dict, Optional, Tuple
 
@@ -20,7 +21,17 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current device's current stream, as a handle (the handle alone: a
+    torch.cuda.Stream object would cost as much as a kernel launch)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """``device`` as the current one (nothing to do where it already is)."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device: torch.device) -> None:
@@ -441,7 +452,7 @@ def quantize_int8(src: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     _need_int8_source(src, "src")
     K = src.shape[-1]
     rows = src.numel() // K
-    with torch.cuda.device(src.device):
+    with _on(src.device):
         q = torch.empty(src.shape[:-1] + ((K + 127) // 128 * 128,), dtype=torch.int8, device=src.device)
         scale = torch.empty(src.shape[:-1], dtype=torch.float32, device=src.device)
         _lib.check("moe_quantize_int8", lib.moe_quantize_int8(_ptr(src), _INT8_DTYPES[src.dtype], rows, K, _ptr(q),
@@ -466,7 +477,7 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     _need(b_scale, "b_scale", torch.float32, (b.shape[0],), dev)
     if out_dtype not in _INT8_DTYPES:
         raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
-    with torch.cuda.device(dev):
+    with _on(dev):
         out = torch.empty((M, b.shape[0]), dtype=out_dtype, device=dev)
         _lib.check("moe_matmul_int8", lib.moe_matmul_int8(
             _ptr(a), _ptr(a_scale), M, _ptr(b), _ptr(b_scale), b.shape[0], K, _ptr(out), _INT8_DTYPES[out_dtype],
@@ -483,9 +494,23 @@ def linear_int8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     K = x.shape[-1]
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != (K + 127) // 128 * 128:
         raise ValueError(f"w must be int8 [N, {(K + 127) // 128 * 128}] for {K} columns of x")
-    q, scale = quantize_int8(x.view(-1, K))
-    out = matmul_int8(q, scale, w, w_scale, x.dtype if out_dtype is None else out_dtype)
-    return out.view(x.shape[:-1] + (w.shape[0],))
+    lib, dev = _lib.load(), x.device
+    N = w.shape[0]
+    _need(w, "w", torch.int8, w.shape, dev)
+    _need(w_scale, "w_scale", torch.float32, (N,), dev)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _INT8_DTYPES:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    M = x.numel() // K
+    nbytes = ctypes.c_size_t(0)
+    _lib.check("moe_linear_int8_workspace_bytes", lib.moe_linear_int8_workspace_bytes(M, N, K, ctypes.byref(nbytes)))
+    with _on(dev):
+        out = torch.empty(x.shape[:-1] + (N,), dtype=out_dtype, device=dev)
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev) if nbytes.value else None
+        _lib.check("moe_linear_int8", lib.moe_linear_int8(
+            _ptr(x), _INT8_DTYPES[x.dtype], M, K, _ptr(w), _ptr(w_scale), N, _ptr(out), _INT8_DTYPES[out_dtype],
+            _ptr(ws), nbytes.value, _stream()))
+    return out
 
 
 def tile_int8(q: torch.Tensor) -> torch.Tensor:

@@ -1,0 +1,99 @@
+// Rows to 8-bit integers, device pieces shared by the quantiser and the products
+// that quantise their own activations.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+constexpr int kI8Chunk = 8;  // elements per thread and step: 8 bytes of q, 16 or 32 bytes read
+
+__device__ __forceinline__ float i8_as_f32(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ float i8_as_f32(float v) { return v; }
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void i8_load_chunk(const T* __restrict__ src, int64_t c, int64_t K, float (&v)[kI8Chunk]) {
+  const int64_t k0 = c * kI8Chunk;
+  if (VEC && k0 + kI8Chunk <= K) {
+    T t[kI8Chunk];
+    constexpr int kWords = kI8Chunk * sizeof(T) / 16;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      reinterpret_cast<u32x4_t*>(t)[i] = reinterpret_cast<const u32x4_t*>(src + k0)[i];
+#pragma unroll
+    for (int i = 0; i < kI8Chunk; ++i) v[i] = i8_as_f32(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kI8Chunk; ++i) v[i] = k0 + i < K ? i8_as_f32(src[k0 + i]) : 0.f;
+  }
+}
+
+// round(127 v / m), ties to even, exactly: the remainder 127 v - q m is exact in
+// fp64 and decides the values whose quotient is next to a half.
+__device__ __forceinline__ int i8_exact_quotient(float v, float m) {
+  const double x = 127.0 * static_cast<double>(v);
+  double q = rint(x / static_cast<double>(m));
+  const double d2 = 2.0 * fma(-q, static_cast<double>(m), x);
+  const bool odd = static_cast<int>(q) & 1;
+  if (d2 > m || (d2 == m && odd)) q += 1.0;
+  if (d2 < -m || (d2 == -m && odd)) q -= 1.0;
+  return static_cast<int>(q);
+}
+
+// Eight quotients as bytes.  In fp32 the quotient v r with r = 127 / m is off by
+// at most 127 2^-23 (r's rounding and the product's), so it is right unless it
+// lies within 2^-15 of a half; adding 1.5 2^23 rounds it to an integer in the
+// sum's low bits.  The exact form then redoes the chunks that hold such a
+// value, one in a thousand or so, and rows whose r would leave fp32's range.
+// (fp64 throughout took 59 us for 8192 x 7168 bf16, bound by arithmetic.)
+__device__ __forceinline__ uint2 i8_quotients(const float (&v)[kI8Chunk], float m, float r, bool exact) {
+  constexpr float kMagic = 12582912.f;
+  uint32_t b[kI8Chunk];
+  float near = 1.f;
+#pragma unroll
+  for (int e = 0; e < kI8Chunk; ++e) {
+    const float y = fmaf(v[e], r, kMagic);
+    b[e] = __float_as_uint(y);
+    const float f = fmaf(v[e], r, kMagic - y);  // the fraction, in [-0.5, 0.5]
+    near = fminf(near, 0.5f - fabsf(f));
+  }
+  if (exact || near < 0x1p-15f) {
+#pragma unroll
+    for (int e = 0; e < kI8Chunk; ++e) b[e] = static_cast<uint32_t>(i8_exact_quotient(v[e], m));
+  }
+  auto pack = [&](int i) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[i + 3], b[i + 2], 0x0c0c0400u);
+    return lo | (hi << 16);
+  };
+  return make_uint2(pack(0), pack(4));
+}
+
+// Largest |v| of a chunk as bits, against `bits`: NaN above infinity above every number.
+__device__ __forceinline__ uint32_t i8_max_bits(const float (&v)[kI8Chunk], uint32_t bits) {
+#pragma unroll
+  for (int e = 0; e < kI8Chunk; ++e) {
+    const uint32_t b = __float_as_uint(v[e]) & 0x7fffffffu;
+    bits = b > bits ? b : bits;
+  }
+  return bits;
+}
+
+// How a row with the largest magnitude `bits` is quantised.
+struct I8RowScale {
+  float m, r, scale;
+  bool some, exact;
+  __device__ __forceinline__ explicit I8RowScale(uint32_t bits) {
+    const bool finite = bits < 0x7f800000u;
+    some = bits && finite;  // neither all zero nor not finite
+    m = __uint_as_float(bits);
+    scale = finite ? m / 127.f : __uint_as_float(0x7fc00000u);
+    r = some ? 127.f / m : 0.f;
+    exact = some && m < 0x1p-100f;  // r past fp32's range, or close
+  }
+  __device__ __forceinline__ uint2 operator()(const float (&v)[kI8Chunk]) const {
+    return some ? i8_quotients(v, m, r, exact) : make_uint2(0, 0);
+  }
+};
+
+}  // namespace moe

@@ -29,6 +29,10 @@ struct RouterArgs {
   bool top2;  // groups rank by their two largest, else by their largest
   bool renorm;
   float scale;
+  // set by the launcher: experts per group, the factor that divides by it, lanes per group
+  int group_size;
+  uint32_t group_magic;
+  int group_lanes;
 };
 constexpr int kMaxGroups = 64;
 // planes, parts, part_stride, logits, idx, gate, err: as launch_topk_gate
@@ -204,6 +208,11 @@ constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel (gemm_i8_rows
 int i8_tile_rows(int64_t rows, int64_t groups, int64_t N);
 hipError_t launch_gemm_i8_tiles(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
+// A dense product of M bf16 or fp32 rows [M][K] that quantises them itself, where
+// linear_i8_fused says so (a.A and a.As unused; a.K is K rounded up to 128).
+bool linear_i8_fused(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear_i8_fused(const I8GemmArgs& a, const void* x, bool x_f32, int64_t K, int epilogue,
+                                  hipStream_t stream);
 // Two few-rows products in one launch: both SwiGLU, or bf16 and fp32.
 hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream);
 

@@ -379,7 +379,7 @@ bool valid_router(const moe_shape* s, const moe_router* r) {
 
 moe::RouterArgs router_args(const moe_router* r) {
   return moe::RouterArgs{r->score == MOE_SCORE_SIGMOID, r->groups, r->kept_groups, r->group_score == MOE_GROUP_TOP2,
-                         r->renorm != 0, r->scale};
+                         r->renorm != 0, r->scale, 0, 0, 0};
 }
 
 // One minibatch of the routed experts in MXFP8 (MoK paper §3.4 "MXFP8
@@ -1073,6 +1073,52 @@ moe_status moe_matmul_int8(const int8_t* a, const float* a_scale, int64_t M, con
   return hip_status(moe::launch_gemm_i8(dense_i8(a, a_scale, M, b, b_scale, N, K, out),
                                         out_dtype == MOE_DT_F32 ? moe::kEpiF32 : moe::kEpiBF16,
                                         static_cast<hipStream_t>(stream)));
+}
+
+// Sizes of a linear product: MOE_OK, or why not.
+static moe_status linear_sizes(int64_t M, int64_t N, int64_t K, int64_t* Kp, size_t* ws) {
+  constexpr int64_t kLimit = int64_t(1) << 31;
+  if (M < 0 || N < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (K > 65536 || M >= kLimit || N >= kLimit) return MOE_ERR_UNSUPPORTED;
+  *Kp = (K + 127) / 128 * 128;
+  if (M * *Kp >= kLimit || N * *Kp >= kLimit) return MOE_ERR_UNSUPPORTED;
+  // the quantised rows, then their scales
+  *ws = M == 0 || N == 0 || moe::linear_i8_fused(M, N, *Kp) ? 0 : M * *Kp + sizeof(float) * M;
+  return MOE_OK;
+}
+
+moe_status moe_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  int64_t Kp;
+  return bytes ? linear_sizes(M, N, K, &Kp, bytes) : MOE_ERR_INVALID_ARG;
+}
+
+moe_status moe_linear_int8(const void* x, int32_t x_dtype, int64_t M, int64_t K, const int8_t* w,
+                           const float* w_scale, int64_t N, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                           void* stream) {
+  if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DT_BF16 && out_dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  int64_t Kp = 0;
+  size_t need = 0;
+  const moe_status st = linear_sizes(M, N, K, &Kp, &need);
+  if (st != MOE_OK) return st;
+  if (M == 0 || N == 0) return MOE_OK;
+  const bool f32 = x_dtype == MOE_DT_F32;
+  if (!x || !w || !w_scale || !out || (need && !ws)) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2) || reinterpret_cast<uintptr_t>(w) % 16 ||
+      reinterpret_cast<uintptr_t>(w_scale) % 4 || reinterpret_cast<uintptr_t>(out) % 16 ||
+      reinterpret_cast<uintptr_t>(ws) % 16)
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int epi = out_dtype == MOE_DT_F32 ? moe::kEpiF32 : moe::kEpiBF16;
+  int8_t* q = static_cast<int8_t*>(ws);
+  float* scale = need ? at<float>(ws, M * Kp) : nullptr;
+  const moe::I8GemmArgs g = dense_i8(q, scale, M, w, w_scale, N, Kp, out);
+  if (!need) return hip_status(moe::launch_linear_i8_fused(g, x, f32, K, epi, s));
+  moe::QuantI8Args a = quant_args(x, K, q, scale);
+  a.Kp = Kp;
+  MOE_TRY_HIP(moe::launch_quantize_rows_i8(a, f32, M, s));
+  return hip_status(moe::launch_gemm_i8(g, epi, s));
 }
 
 moe_status moe_probe_begin(int32_t kernel_id, int32_t max_launches) {

@@ -8,6 +8,7 @@
 // row stays in registers between its maximum and its quotients.
 
 #include "common.h"
+#include "i8.h"
 #include "kernels.h"
 
 namespace moe {
@@ -15,69 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 8;  // elements per thread and step: 8 bytes of q, 16 or 32 bytes read
-constexpr int kHeld = 4;   // chunks a thread keeps; longer rows (over 8192) are read twice
-
-__device__ __forceinline__ float as_f32(uint16_t v) { return bf16_to_f32(v); }
-__device__ __forceinline__ float as_f32(float v) { return v; }
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_chunk(const T* __restrict__ src, int64_t c, int64_t K, float (&v)[kChunk]) {
-  const int64_t k0 = c * kChunk;
-  if (VEC && k0 + kChunk <= K) {
-    T t[kChunk];
-    constexpr int kWords = kChunk * sizeof(T) / 16;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i)
-      reinterpret_cast<u32x4_t*>(t)[i] = reinterpret_cast<const u32x4_t*>(src + k0)[i];
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = as_f32(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = k0 + i < K ? as_f32(src[k0 + i]) : 0.f;
-  }
-}
-
-// round(127 v / m), ties to even, exactly: the remainder 127 v - q m is exact in
-// fp64 and decides the values whose quotient is next to a half.
-__device__ __forceinline__ int exact_quotient(float v, float m) {
-  const double x = 127.0 * static_cast<double>(v);
-  double q = rint(x / static_cast<double>(m));
-  const double d2 = 2.0 * fma(-q, static_cast<double>(m), x);
-  const bool odd = static_cast<int>(q) & 1;
-  if (d2 > m || (d2 == m && odd)) q += 1.0;
-  if (d2 < -m || (d2 == -m && odd)) q -= 1.0;
-  return static_cast<int>(q);
-}
-
-// Eight quotients as bytes.  In fp32 the quotient v r with r = 127 / m is off by
-// at most 127 2^-23 (r's rounding and the product's), so it is right unless it
-// lies within 2^-15 of a half; adding 1.5 2^23 rounds it to an integer in the
-// sum's low bits.  The exact form then redoes the chunks that hold such a
-// value, one in a thousand or so, and rows whose r would leave fp32's range.
-// (fp64 throughout took 59 us for 8192 x 7168 bf16, bound by arithmetic.)
-__device__ __forceinline__ uint2 quotients(const float (&v)[kChunk], float m, float r, bool exact) {
-  constexpr float kMagic = 12582912.f;
-  uint32_t b[kChunk];
-  float near = 1.f;
-#pragma unroll
-  for (int e = 0; e < kChunk; ++e) {
-    const float y = fmaf(v[e], r, kMagic);
-    b[e] = __float_as_uint(y);
-    const float f = fmaf(v[e], r, kMagic - y);  // the fraction, in [-0.5, 0.5]
-    near = fminf(near, 0.5f - fabsf(f));
-  }
-  if (exact || near < 0x1p-15f) {
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) b[e] = static_cast<uint32_t>(exact_quotient(v[e], m));
-  }
-  auto pack = [&](int i) {
-    const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(b[i + 3], b[i + 2], 0x0c0c0400u);
-    return lo | (hi << 16);
-  };
-  return make_uint2(pack(0), pack(4));
-}
+constexpr int kHeld = 4;  // chunks a thread keeps; longer rows (over 8192) are read twice
 
 template <bool VEC, typename T>
 __device__ __forceinline__ void quantize_row(const QuantI8Args& a, int64_t i) {
@@ -95,32 +34,25 @@ __device__ __forceinline__ void quantize_row(const QuantI8Args& a, int64_t i) {
   }
   const T* __restrict__ src = static_cast<const T*>(a.src) + from * a.K;
   int8_t* __restrict__ q = a.q + to * a.Kp;
-  const int64_t chunks = a.Kp / kChunk;
+  const int64_t chunks = a.Kp / kI8Chunk;
   const int tid = threadIdx.x;
 
-  float v[kHeld][kChunk];
-  uint32_t bits = 0;  // largest |v| as bits: NaN above infinity above every number
-  auto take = [&](const float(&w)[kChunk]) {
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      const uint32_t b = __float_as_uint(w[e]) & 0x7fffffffu;
-      bits = b > bits ? b : bits;
-    }
-  };
+  float v[kHeld][kI8Chunk];
+  uint32_t bits = 0;
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) {
     const int64_t c = tid + h * kThreads;
     if (c < chunks)
-      load_chunk<VEC>(src, c, a.K, v[h]);
+      i8_load_chunk<VEC>(src, c, a.K, v[h]);
     else
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) v[h][e] = 0.f;
-    take(v[h]);
+      for (int e = 0; e < kI8Chunk; ++e) v[h][e] = 0.f;
+    bits = i8_max_bits(v[h], bits);
   }
   for (int64_t c = tid + kHeld * kThreads; c < chunks; c += kThreads) {
-    float w[kChunk];
-    load_chunk<VEC>(src, c, a.K, w);
-    take(w);
+    float w[kI8Chunk];
+    i8_load_chunk<VEC>(src, c, a.K, w);
+    bits = i8_max_bits(w, bits);
   }
   __shared__ uint32_t part[kThreads / kWave];
 #pragma unroll
@@ -133,22 +65,17 @@ __device__ __forceinline__ void quantize_row(const QuantI8Args& a, int64_t i) {
 #pragma unroll
   for (int w = 0; w < kThreads / kWave; ++w) bits = part[w] > bits ? part[w] : bits;
 
-  const bool some = bits && bits < 0x7f800000u;  // neither all zero nor not finite
-  const float m = __uint_as_float(bits);
-  if (tid == 0) a.scale[to] = bits < 0x7f800000u ? m / 127.f : __uint_as_float(0x7fc00000u);
-  const float r = some ? 127.f / m : 0.f;
-  const bool exact = some && m < 0x1p-100f;  // r past fp32's range, or close
-  auto put = [&](int64_t c, const float(&w)[kChunk]) {
-    *reinterpret_cast<uint2*>(q + c * kChunk) = some ? quotients(w, m, r, exact) : make_uint2(0, 0);
-  };
+  const I8RowScale quant(bits);
+  if (tid == 0) a.scale[to] = quant.scale;
+  auto put = [&](int64_t c, const float(&w)[kI8Chunk]) { *reinterpret_cast<uint2*>(q + c * kI8Chunk) = quant(w); };
 #pragma unroll
   for (int h = 0; h < kHeld; ++h) {
     const int64_t c = tid + h * kThreads;
     if (c < chunks) put(c, v[h]);
   }
   for (int64_t c = tid + kHeld * kThreads; c < chunks; c += kThreads) {
-    float w[kChunk];
-    load_chunk<VEC>(src, c, a.K, w);
+    float w[kI8Chunk];
+    i8_load_chunk<VEC>(src, c, a.K, w);
     put(c, w);
   }
 }

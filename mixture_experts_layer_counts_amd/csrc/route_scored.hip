@@ -7,6 +7,15 @@
 // arithmetic at the rate of unpacked fp32.  A candidate is one double, the
 // choosing value with its 10 low mantissa bits replaced by the expert id, so
 // that a maximum of doubles is the arg-max with ties to the lower id.
+//
+// What bounds the choice is arithmetic (a row of 256 logits is 1 KB, and 8192
+// of them a microsecond or two of memory), so a wave takes four tokens: 16 lanes
+// and, at 256 experts, 16 registers each.  A lane sorts its candidates once; then
+// the sorted lists of two lanes meet log2(16) times, each time keeping the 8 (or
+// 16) largest of both by one bitonic merge, with the partner's list coming by
+// DPP inside the 16-lane row.  Rounds of a wave-wide arg-max (a token a wave,
+// k rounds of six crossbar steps) took 26 us for 8192 tokens where this takes
+// 10.6, and 10.0 for one where this takes 4.8.
 
 #include "common.h"
 #include "kernels.h"
@@ -44,11 +53,19 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l > 3.402823466e38f ? 3.402823466e38f : l;
 }
 
+// 1 / d for 1 <= d < 2^1020: two Newton steps from the hardware's estimate
+// (some 2^-26), exact to the last place or two.
+__device__ __forceinline__ double recip64(double d) {
+  double y = __builtin_amdgcn_rcp(d);
+  y = fma(fma(-d, y, 1.0), y, y);
+  return fma(fma(-d, y, 1.0), y, y);
+}
+
 // 1 / (1 + exp(-l)); exp(700) is still finite.
 __device__ __forceinline__ double sigmoid64(float l) {
-  const double x = static_cast<double>(l);
-  const double c = x < -700.0 ? -700.0 : (x > 700.0 ? 700.0 : x);
-  return l == -INFINITY ? 0.0 : 1.0 / (1.0 + exp64(-c));
+  const float c = fminf(fmaxf(l, -700.f), 700.f);
+  const double s = recip64(1.0 + exp64(-static_cast<double>(c)));
+  return l == -INFINITY ? 0.0 : s;
 }
 
 // exp(l - m) for l <= m; 0 where it is below exp(-700).
@@ -57,24 +74,138 @@ __device__ __forceinline__ double exp_below(float l, float m) {
   return d > -700.0 ? exp64(d) : 0.0;
 }
 
-// Reductions over the LPT consecutive lanes of one token; every lane gets the result.
-template <int LPT>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int d = 1; d < LPT; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+// Maximum and minimum of two candidates (never NaN).  As instructions of their
+// own: fmax would first quieten each operand that comes from a bit pattern.
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+
+// ---- the lanes of one token: LPT = 16 (a DPP row), 32 or 64 consecutive ones ----
+// Step d of a butterfly over them: the pair (this lane's value, its partner's),
+// in either order.  Steps 0 .. 3 pair lanes of a row (lane ^ 1, lane ^ 2, the
+// mirror in 8 lanes and the mirror in 16, each of which joins two halves that
+// agree within themselves), step 4 two rows, step 5 two halves of the wave.
+template <int STEP>
+__device__ __forceinline__ void partner32(uint32_t x, uint32_t& a, uint32_t& b) {
+  constexpr int kDpp[4] = {0xB1, 0x4E, 0x141, 0x140};
+  if constexpr (STEP < 4) {
+    a = x;
+    b = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kDpp[STEP < 4 ? STEP : 0], 0xF, 0xF, false));
+  } else if constexpr (STEP == 4) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    a = r[0];
+    b = r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    a = r[0];
+    b = r[1];
+  }
+}
+template <int STEP>
+__device__ __forceinline__ void partner64(double x, double& a, double& b) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));
+  uint32_t al, bl, ah, bh;
+  partner32<STEP>(static_cast<uint32_t>(u), al, bl);
+  partner32<STEP>(static_cast<uint32_t>(u >> 32), ah, bh);
+  a = __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(ah) << 32 | al));
+  b = __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(bh) << 32 | bl));
+}
+
+template <int LPT, int STEP = 0>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr ((1 << STEP) < LPT) {
+    uint32_t a, b;
+    partner32<STEP>(__float_as_uint(v), a, b);
+    return lanes_max<LPT, STEP + 1>(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
   return v;
 }
-template <int LPT>
-__device__ __forceinline__ double group_max(double v) {
-#pragma unroll
-  for (int d = 1; d < LPT; d *= 2) v = fmax(v, __shfl_xor(v, d));
+template <int LPT, int STEP = 0>
+__device__ __forceinline__ double lanes_sum(double v) {
+  if constexpr ((1 << STEP) < LPT) {
+    double a, b;
+    partner64<STEP>(v, a, b);
+    return lanes_sum<LPT, STEP + 1>(a + b);
+  }
   return v;
 }
-template <int LPT>
-__device__ __forceinline__ double group_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < LPT; d *= 2) v += __shfl_xor(v, d);
+template <int LPT, int STEP = 0>
+__device__ __forceinline__ uint32_t lanes_or(uint32_t v) {
+  if constexpr ((1 << STEP) < LPT) {
+    uint32_t a, b;
+    partner32<STEP>(v, a, b);
+    return lanes_or<LPT, STEP + 1>(a | b);
+  }
   return v;
+}
+
+// The two largest of `lanes` (a power of two) neighbouring lanes' pairs.
+template <int LPT, int STEP = 0>
+__device__ __forceinline__ void lanes_two(double& best, double& next, int lanes) {
+  if constexpr ((1 << STEP) < LPT) {
+    if ((1 << STEP) >= lanes) return;  // uniform
+    double a, b, c, d;
+    partner64<STEP>(best, a, b);
+    partner64<STEP>(next, c, d);
+    best = max64(a, b);
+    next = max64(min64(a, b), max64(c, d));
+    lanes_two<LPT, STEP + 1>(best, next, lanes);
+  }
+}
+
+// ---- sorted lists in registers (falling order) ----
+__device__ __forceinline__ void order(double& hi, double& lo) {
+  const double a = hi, b = lo;
+  hi = max64(a, b);
+  lo = min64(a, b);
+}
+// A bitonic list of N into falling order.
+template <int N>
+__device__ __forceinline__ void bitonic(double* v) {
+#pragma unroll
+  for (int d = N / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & d) == 0) order(v[i], v[i + d]);
+}
+// Any list of N (a power of two) into falling order: runs of 1, 2, 4, ... merged,
+// every other run turned round by the index it is compared at.
+template <int N>
+__device__ __forceinline__ void sort_list(double* v) {
+#pragma unroll
+  for (int run = 2; run <= N; run *= 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & (run / 2)) == 0) {
+        const int o = (i & ~(run - 1)) + (run - 1) - (i & (run - 1));  // mirror in the run
+        order(v[i], v[o]);
+      }
+#pragma unroll
+    for (int d = run / 4; d > 0; d /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((i & d) == 0) order(v[i], v[i + d]);
+  }
+}
+// The K largest of every lane's list of K, in falling order, on all LPT lanes.
+template <int K, int LPT, int STEP = 0>
+__device__ __forceinline__ void lanes_best(double (&v)[K]) {
+  if constexpr ((1 << STEP) < LPT) {
+    double a[K], b[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) partner64<STEP>(v[i], a[i], b[i]);
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = max64(a[i], b[K - 1 - i]);
+    bitonic<K>(v);
+    lanes_best<K, LPT, STEP + 1>(v);
+  }
 }
 
 // Candidate of expert e, and the id back from it.
@@ -87,119 +218,210 @@ __device__ __forceinline__ int candidate_id(double key) {
   return key < 0.0 ? low : 1023 - low;
 }
 
-// LPT lanes per token, EPL logits per lane (LPT * EPL >= E): lane j holds
-// experts 4 (LPT q + j) .. + 3 for q = 0, 1, ...
+// EPL experts per lane (LPT * EPL >= E): lane j holds experts 4 (LPT q + j) ..
+// + 3 for q = 0, 1, ...
 template <int LPT, int EPL>
 __device__ __forceinline__ int expert_of(int j, int i) {
   return ((i >> 2) * LPT + j) * 4 + (i & 3);
 }
+// A row of E floats into that layout (past E: `fill`), in 16-byte pieces if VEC.
+template <int LPT, int EPL, bool VEC>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int j, int E, float fill, float (&v)[EPL]) {
+#pragma unroll
+  for (int q = 0; q < EPL / 4; ++q) {
+    const int e = expert_of<LPT, EPL>(j, 4 * q);
+    if (VEC) {
+      f32x4_t x = {fill, fill, fill, fill};
+      if (e < E) x = *reinterpret_cast<const f32x4_t*>(row + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * q + i] = x[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * q + i] = e + i < E ? row[e + i] : fill;
+    }
+  }
+}
 
-template <int LPT, int EPL>
+template <int K, int LPT, int EPL, bool VEC>
 __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const float* __restrict__ planes, int parts,
                                                            int64_t part_stride, const float* __restrict__ bias,
                                                            float* __restrict__ logits, int T, int E, int k,
                                                            int32_t* __restrict__ idx, float* __restrict__ gate,
                                                            int* err) {
   constexpr int TPB = 256 / LPT;  // tokens per block
-  __shared__ double c_s[TPB][LPT * EPL];
+  extern __shared__ double c_s[];  // [TPB][LPT * EPL], only for groups that are read from LDS
   __shared__ float l_s[TPB][LPT * EPL];
-  __shared__ double g_s[TPB][kMaxGroups];
+  __shared__ double g_s[TPB][kMaxGroups];  // padded to a multiple of four groups
   const int tok_b = static_cast<int>(threadIdx.x) / LPT, j = static_cast<int>(threadIdx.x) % LPT;
   const int token = blockIdx.x * TPB + tok_b;
   const bool live = token < T;
   const int64_t row = static_cast<int64_t>(live ? token : T - 1) * E;
 
   float l[EPL];
-  double c[EPL];
+  load_row<LPT, EPL, VEC>(planes + row, j, E, 0.f, l);
+  for (int p = 1; p < parts; ++p) {
+    float more[EPL];
+    load_row<LPT, EPL, VEC>(planes + row + p * part_stride, j, E, 0.f, more);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] += more[i];
+  }
+  float b[EPL];
+  if (bias) load_row<LPT, EPL, VEC>(bias, j, E, 0.f, b);
   bool bad = false;
-  float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = expert_of<LPT, EPL>(j, i);
-    float v = -INFINITY;
-    if (e < E) {
-      v = planes[row + e];
-      for (int p = 1; p < parts; ++p) v += planes[row + p * part_stride + e];
-      if (planes != logits && live) logits[row + e] = v;
-      bad |= !__builtin_isfinite(v);
-    }
-    l[i] = clean_logit(v);
-    l_s[tok_b][e] = l[i];
-    m = fmaxf(m, l[i]);
+    if (planes != logits && live && e < E) logits[row + e] = l[i];
+    bad |= !__builtin_isfinite(l[i]);
+    if (!bias) b[i] = 0.f;
+    bad |= !__builtin_isfinite(b[i]);
+    l[i] = e < E ? clean_logit(l[i]) : -INFINITY;
   }
-  double sum = 0.0;
-  if (!r.sigmoid) {
-    m = group_max<LPT>(m);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sum += exp_below(l[i], m);
-    sum = group_sum<LPT>(sum);
-  }
-  // score of a logit (0 for every expert of a token whose logits are all -inf)
-  auto score = [&](float v) { return r.sigmoid ? sigmoid64(v) : (v == -INFINITY ? 0.0 : exp_below(v, m) / sum); };
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = expert_of<LPT, EPL>(j, i);
-    c[i] = kLast;
-    if (e < E) {
-      const float b = bias ? bias[e] : 0.f;
-      bad |= !__builtin_isfinite(b);
-      const double v = score(l[i]) + b;
-      c[i] = v > kLast ? (v < -kLast ? v : -kLast) : kLast;
-    }
-    c_s[tok_b][e] = c[i];
-  }
+  for (int q = 0; q < EPL / 4; ++q)
+    *reinterpret_cast<f32x4_t*>(&l_s[tok_b][expert_of<LPT, EPL>(j, 4 * q)]) =
+        f32x4_t{l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]};
   if (live && bad) raise_error(err, kErrNonFinite);
 
-  // groups: each lane ranks some of them by counting the better ones
-  uint64_t kept = ~uint64_t(0);
-  const int size = E / r.groups;
-  if (r.kept_groups < r.groups) {
-    __syncthreads();
-    for (int g = j; g < r.groups; g += LPT) {
-      double a = -INFINITY, b = -INFINITY;
-      for (int e = g * size; e < (g + 1) * size; ++e) {
-        const double v = c_s[tok_b][e];
-        b = fmax(b, fmin(a, v));
-        a = fmax(a, v);
-      }
-      g_s[tok_b][g] = r.top2 && size > 1 ? a + b : a;
+  // scores, then choosing values
+  double c[EPL];
+  float m = 0.f;
+  double inv = 1.0;  // softmax: 1 / sum
+  if (r.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = sigmoid64(l[i]);
+  } else {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+    m = lanes_max<LPT>(m);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      c[i] = l[i] == -INFINITY ? 0.0 : exp_below(l[i], m);
+      sum += c[i];
     }
+    sum = lanes_sum<LPT>(sum);
+    inv = sum > 0.0 ? recip64(sum) : 0.0;  // at least 1, or 0 for a token whose logits are all -inf
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] *= inv;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const double v = c[i] + static_cast<double>(b[i]);
+    c[i] = v > kLast ? (v < -kLast ? v : -kLast) : kLast;
+    if (expert_of<LPT, EPL>(j, i) >= E) c[i] = -INFINITY;
+  }
+
+  // groups: their scores into g_s, then each is ranked by counting the better ones
+  uint64_t kept = ~uint64_t(0);
+  if (r.kept_groups < r.groups) {
+    const int size = r.group_size;
+    if (r.group_lanes == 0) {
+      // a group is 1, 2, 4, ... neighbouring lanes' quads: the two largest by
+      // the first steps of the butterfly, in registers
+#pragma unroll
+      for (int q = 0; q < EPL / 4; ++q) {
+        const double h0 = max64(c[4 * q], c[4 * q + 1]), l0 = min64(c[4 * q], c[4 * q + 1]);
+        const double h1 = max64(c[4 * q + 2], c[4 * q + 3]), l1 = min64(c[4 * q + 2], c[4 * q + 3]);
+        double best = max64(h0, h1), next = max64(min64(h0, h1), max64(l0, l1));
+        lanes_two<LPT>(best, next, size / 4);
+        const int e = expert_of<LPT, EPL>(j, 4 * q);
+        if (e < E && e % size == 0) g_s[tok_b][e / size] = r.top2 ? best + next : best;
+      }
+    } else {
+      // any other size: group_lanes lanes read one together
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c_s[tok_b * LPT * EPL + expert_of<LPT, EPL>(j, i)] = c[i];
+      __syncthreads();
+      const int sub = r.group_lanes, part = j & (sub - 1);
+      for (int g = j / sub; g < r.groups; g += LPT / sub) {
+        const double* cg = &c_s[tok_b * LPT * EPL + g * size];
+        double best = -INFINITY, next = -INFINITY;
+        for (int e = part; e < size; e += sub) {
+          const double v = cg[e];
+          next = max64(next, min64(best, v));
+          best = max64(best, v);
+        }
+        for (int d = 1; d < sub; d *= 2) {
+          const double ob = __shfl_xor(best, d), on = __shfl_xor(next, d);
+          next = max64(min64(best, ob), max64(next, on));
+          best = max64(best, ob);
+        }
+        if (part == 0) g_s[tok_b][g] = r.top2 && size > 1 ? best + next : best;
+      }
+    }
+    for (int g = r.groups + j; g < (r.groups + 3) / 4 * 4; g += LPT) g_s[tok_b][g] = -INFINITY;
     __syncthreads();
-    uint64_t mine = 0;
+    uint32_t lo = 0, hi = 0;
     for (int g = j; g < r.groups; g += LPT) {
       int better = 0;
       const double v = g_s[tok_b][g];
-      for (int o = 0; o < r.groups; ++o) {
-        const double u = g_s[tok_b][o];
-        better += u > v || (u == v && o < g);
+      for (int o = 0; o < r.groups; o += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double u = g_s[tok_b][o + i];
+          better += u > v || (u == v && o + i < g);
+        }
       }
-      mine |= better < r.kept_groups ? uint64_t(1) << g : 0;
+      const uint32_t bit = better < r.kept_groups ? 1u << (g & 31) : 0u;
+      lo |= g < 32 ? bit : 0u;
+      hi |= g < 32 ? 0u : bit;
     }
-#pragma unroll
-    for (int d = 1; d < LPT; d *= 2) mine |= __shfl_xor(mine, d);
-    kept = mine;
+    lo = lanes_or<LPT>(lo);
+    hi = r.groups > 32 ? lanes_or<LPT>(hi) : 0u;
+    kept = static_cast<uint64_t>(hi) << 32 | lo;
   }
+  // e / size as (e * group_magic) >> 20
+  auto in = [&](int e) { return (kept >> ((static_cast<uint32_t>(e) * r.group_magic) >> 20)) & 1; };
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = expert_of<LPT, EPL>(j, i);
-    c[i] = e < E && (kept >> (r.groups > 1 ? e / size : 0)) & 1 ? candidate(c[i], e) : -INFINITY;
+  for (int q = 0; q < EPL / 4; ++q) {
+    const int e = expert_of<LPT, EPL>(j, 4 * q);
+    const bool quad = in(e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool ok = r.group_size % 4 == 0 ? quad : in(e + i);  // uniform: a quad lies in one group
+      const double v = c[4 * q + i];
+      c[4 * q + i] = ok && v > -INFINITY ? candidate(v, e + i) : -INFINITY;
+    }
   }
 
-  // k rounds of a maximum over the token's lanes; lane s keeps slot s
-  int my_id = 0;
-  for (int s = 0; s < k; ++s) {
-    double best = c[0];
+  // the K largest: each lane's own, then the lanes'
+  double best[K];
+  if constexpr (EPL <= K) {
+    constexpr int N = EPL <= 4 ? 4 : (EPL <= 8 ? 8 : 16);
+    double list[N];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) best = fmax(best, c[i]);
-    best = group_max<LPT>(best);
+    for (int i = 0; i < N; ++i) list[i] = i < EPL ? c[i < EPL ? i : 0] : -INFINITY;
+    sort_list<N>(list);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = c[i] == best ? -INFINITY : c[i];
-    if (j == s) my_id = candidate_id(best);
+    for (int i = 0; i < K; ++i) best[i] = i < N ? list[i < N ? i : 0] : -INFINITY;
+  } else {
+    static_assert(EPL <= 2 * K, "two lists a lane");
+    double more[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) best[i] = c[i];
+#pragma unroll
+    for (int i = 0; i < K; ++i) more[i] = K + i < EPL ? c[K + i < EPL ? K + i : 0] : -INFINITY;
+    sort_list<K>(best);
+    sort_list<K>(more);
+#pragma unroll
+    for (int i = 0; i < K; ++i) best[i] = max64(best[i], more[K - 1 - i]);
+    bitonic<K>(best);
   }
+  lanes_best<K, LPT>(best);
+
+  // lane s takes slot s
+  double mine = best[0];
+#pragma unroll
+  for (int i = 1; i < K; ++i) mine = j == i ? best[i] : mine;
+  const int my_id = candidate_id(mine);
   __syncthreads();  // l_s is whole
-  double w = j < k ? score(l_s[tok_b][my_id]) : 0.0;
+  const float my_l = l_s[tok_b][j < k ? my_id : 0];
+  double w = 0.0;
+  if (j < k) w = r.sigmoid ? sigmoid64(my_l) : (my_l == -INFINITY ? 0.0 : exp_below(my_l, m) * inv);
   if (r.renorm) {
-    const double W = group_sum<LPT>(w);
+    const double W = lanes_sum<LPT>(w);
     w = W > 0.0 ? w / W : 0.0;
   }
   if (live && j < k) {
@@ -208,22 +430,20 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
   }
 }
 
-// One token per LPT lanes; the row of dlogits is put together in LDS.
-template <int LPT, int EPL, bool BF16>
+// One token per LPT lanes; the chosen experts' terms are put in their places in LDS.
+template <int LPT, int EPL, bool BF16, bool VEC>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const float* __restrict__ logits,
                                                              const int32_t* __restrict__ idx,
                                                              const float* __restrict__ dgate, int T, int E, int k,
                                                              float* __restrict__ out32, uint16_t* __restrict__ out16,
                                                              int ld, int* err) {
   constexpr int TPB = 256 / LPT;
-  __shared__ float dw_s[TPB][LPT * EPL];  // dw of the chosen experts, 0 elsewhere
+  __shared__ double dw_s[TPB][LPT * EPL];  // the chosen experts' terms, 0 elsewhere
   const int tok_b = static_cast<int>(threadIdx.x) / LPT, j = static_cast<int>(threadIdx.x) % LPT;
   const int token = blockIdx.x * TPB + tok_b;
   const bool live = token < T;
   const int64_t row = static_cast<int64_t>(live ? token : T - 1) * E;
   const int64_t krow = static_cast<int64_t>(live ? token : T - 1) * k;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) dw_s[tok_b][expert_of<LPT, EPL>(j, i)] = 0.f;
 
   int id = j < k ? idx[krow + j] : -1;
   if (j < k && (id < 0 || id >= E)) {
@@ -236,66 +456,131 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const
   // softmax scores that are not renormalised need the maximum and the sum of
   // the whole row; renormalised ones only their ratios among the chosen
   const bool dense = !r.sigmoid && !r.renorm;
-  float l[EPL];
+  double z[EPL];
   float m = lj;
+  double inv = 1.0;
   if (dense) {
+    float l[EPL];
+    load_row<LPT, EPL, VEC>(logits + row, j, E, -INFINITY, l);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = expert_of<LPT, EPL>(j, i);
-      l[i] = e < E ? clean_logit(logits[row + e]) : -INFINITY;
+      l[i] = clean_logit(l[i]);
       m = fmaxf(m, l[i]);
     }
-  }
-  m = group_max<LPT>(m);
-  double sum = 1.0;
-  if (dense) {
-    sum = 0.0;
+    m = lanes_max<LPT>(m);
+    double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sum += exp_below(l[i], m);
-    sum = group_sum<LPT>(sum);
+    for (int i = 0; i < EPL; ++i) {
+      z[i] = l[i] == -INFINITY ? 0.0 : exp_below(l[i], m);
+      sum += z[i];
+    }
+    sum = lanes_sum<LPT>(sum);
+    inv = sum > 0.0 ? recip64(sum) : 0.0;
+  } else if (!r.sigmoid) {
+    m = lanes_max<LPT>(m);
   }
-  auto score = [&](float v) { return r.sigmoid ? sigmoid64(v) : (v == -INFINITY ? 0.0 : exp_below(v, m) / sum); };
-  const double s = id >= 0 ? score(lj) : 0.0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) dw_s[tok_b][expert_of<LPT, EPL>(j, i)] = 0.0;
+  double s = 0.0;
+  if (id >= 0) s = r.sigmoid ? sigmoid64(lj) : (lj == -INFINITY ? 0.0 : exp_below(lj, m) * inv);
   double dw = dg * r.scale;
   if (r.renorm) {
-    const double W = group_sum<LPT>(s);
-    const double mean = W > 0.0 ? group_sum<LPT>(dw * s) / W : 0.0;
+    const double W = lanes_sum<LPT>(s);
+    const double mean = W > 0.0 ? lanes_sum<LPT>(dw * s) / W : 0.0;
     dw = W > 0.0 ? (dw - mean) / W : 0.0;
   }
   // the softmax's own mean, sum_s s_s dw_s: zero for renormalised gates
-  const double mean = dense ? group_sum<LPT>(s * dw) : 0.0;
+  const double mean = dense ? lanes_sum<LPT>(s * dw) : 0.0;
   __syncthreads();
-  if (id >= 0) atomicAdd(&dw_s[tok_b][id], static_cast<float>(dense ? dw : r.sigmoid ? s * (1.0 - s) * dw : s * dw));
+  if (id >= 0) atomicAdd(&dw_s[tok_b][id], dense ? dw : r.sigmoid ? s * (1.0 - s) * dw : s * dw);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = expert_of<LPT, EPL>(j, i);
-    if (!live || e >= (BF16 ? ld : E)) continue;
-    float v = dw_s[tok_b][e];
-    if (dense) v = static_cast<float>(score(l[i]) * (v - mean));
-    if constexpr (BF16)
-      out16[static_cast<int64_t>(token) * ld + e] = f32_to_bf16(v);
-    else
-      out32[static_cast<int64_t>(token) * ld + e] = v;
+  for (int q = 0; q < EPL / 4; ++q) {
+    const int e = expert_of<LPT, EPL>(j, 4 * q);
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double t = dw_s[tok_b][e + i];
+      v[i] = static_cast<float>(dense ? z[4 * q + i] * inv * (t - mean) : t);
+    }
+    if (!live) continue;
+    const int64_t at = static_cast<int64_t>(token) * ld + e;
+    if constexpr (BF16) {  // rows of ld, a multiple of 64
+      if (e < ld) *reinterpret_cast<uint2*>(out16 + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else if constexpr (VEC) {
+      if (e < E) *reinterpret_cast<f32x4_t*>(out32 + at) = f32x4_t{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < E) out32[at + i] = v[i];
+    }
   }
 }
 
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// What the kernels need of the groups.
+RouterArgs with_groups(RouterArgs r, int E, int lanes) {
+  r.group_size = E / r.groups;
+  r.group_magic = (1u << 20) / static_cast<uint32_t>(r.group_size) + 1;  // exact for e < 1024
+  const int quads = r.group_size / 4;
+  if (r.group_size % 4 == 0 && (quads & (quads - 1)) == 0 && quads <= lanes) {
+    r.group_lanes = 0;  // in registers
+    return r;
+  }
+  // lanes that read one group together: a power of two that divides its size
+  r.group_lanes = 1;
+  while (2 * r.group_lanes * r.groups <= lanes && r.group_size % (2 * r.group_lanes) == 0) r.group_lanes *= 2;
+  return r;
+}
+
+// Experts a lane holds at most, and the lanes of a token for them.
+int lanes_for(int E) { return E <= 256 ? 16 : (E <= 512 ? 32 : 64); }
+// Up to this many tokens, with at most 512 experts, a whole wave takes a token,
+// four or eight experts a lane: with two waves or less for every SIMD its
+// shorter chain of fp64 instructions is what counts (256 experts in 8 groups:
+// one token 4.8 us against 7.3 with 16 lanes, 2048 tokens 6.2 against 7.8; 4096
+// tokens 8.9 against 8.0).
+constexpr int kWaveTokens = 2048;
+
 }  // namespace
 
-hipError_t launch_route_scored(const RouterArgs& r, const float* planes, int parts, int64_t part_stride,
+hipError_t launch_route_scored(const RouterArgs& args, const float* planes, int parts, int64_t part_stride,
                                const float* bias, float* logits, int T, int E, int k, int32_t* idx, float* gate,
                                int* err, hipStream_t stream) {
   if (T <= 0) return hipSuccess;
-  if (parts < 1 || parts > kMaxRouterParts || E > 1024 || k > 16 || r.groups > kMaxGroups) return hipErrorInvalidValue;
-#define MOE_RUN(LPT, EPL)                                                                                          \
-  route_scored_kernel<LPT, EPL><<<(T + 256 / LPT - 1) / (256 / LPT), 256, 0, stream>>>(                            \
-      r, planes, parts, part_stride, bias, logits, T, E, k, idx, gate, err)
-  if (E <= 256)
-    MOE_RUN(64, 4);
-  else if (E <= 512)
-    MOE_RUN(64, 8);
-  else
-    MOE_RUN(64, 16);
+  if (parts < 1 || parts > kMaxRouterParts || E > 1024 || k > 16 || args.groups > kMaxGroups || E % args.groups)
+    return hipErrorInvalidValue;
+  const bool wave = E <= 512 && T <= kWaveTokens;
+  const int lanes = wave ? 64 : lanes_for(E);
+  const RouterArgs r = with_groups(args, E, lanes);
+  const bool vec = E % 4 == 0 && part_stride % 4 == 0 && aligned16(planes) && aligned16(bias) && aligned16(logits);
+  const int blocks = (T + 256 / lanes - 1) / (256 / lanes);
+#define MOE_RUN(K, LPT, EPL)                                                                                        \
+  (vec ? route_scored_kernel<K, LPT, EPL, true> : route_scored_kernel<K, LPT, EPL, false>)                          \
+      <<<blocks, 256, r.group_lanes ? sizeof(double) * 256 * EPL : 0, stream>>>(                                    \
+          r, planes, parts, part_stride, bias, logits, T, E, k, idx, gate, err)
+#define MOE_RUN_K(LPT, EPL) \
+  if (k <= 8)               \
+    MOE_RUN(8, LPT, EPL);   \
+  else                      \
+    MOE_RUN(16, LPT, EPL)
+  if (wave && E <= 256) {
+    MOE_RUN_K(64, 4);
+  } else if (wave) {
+    MOE_RUN_K(64, 8);
+  } else if (E <= 128) {
+    MOE_RUN_K(16, 8);
+  } else if (lanes == 16) {
+    MOE_RUN_K(16, 16);
+  } else if (E <= 384) {
+    MOE_RUN_K(32, 12);
+  } else if (lanes == 32) {
+    MOE_RUN_K(32, 16);
+  } else {
+    MOE_RUN_K(64, 16);
+  }
+#undef MOE_RUN_K
 #undef MOE_RUN
   return hipGetLastError();
 }
@@ -305,24 +590,23 @@ hipError_t launch_route_backward(const RouterArgs& r, const float* logits, const
                                  hipStream_t stream) {
   if (T <= 0) return hipSuccess;
   if (E > 1024 || ld < E || ld > 1024 || k > 16 || !out32 == !out16) return hipErrorInvalidValue;
-#define MOE_RUN(LPT, EPL, BF16)                                                                                    \
-  route_backward_kernel<LPT, EPL, BF16><<<(T + 256 / LPT - 1) / (256 / LPT), 256, 0, stream>>>(                    \
-      r, logits, idx, dgate, T, E, k, out32, out16, ld, err)
-  if (out16) {
-    if (ld <= 256)
-      MOE_RUN(64, 4, true);
-    else if (ld <= 512)
-      MOE_RUN(64, 8, true);
-    else
-      MOE_RUN(64, 16, true);
-  } else {
-    if (ld <= 256)
-      MOE_RUN(64, 4, false);
-    else if (ld <= 512)
-      MOE_RUN(64, 8, false);
-    else
-      MOE_RUN(64, 16, false);
-  }
+  if (out16 && (ld % 4 || reinterpret_cast<uintptr_t>(out16) % 8)) return hipErrorInvalidValue;
+  const bool vec = E % 4 == 0 && aligned16(logits) && aligned16(out32);
+  const int lanes = lanes_for(ld), blocks = (T + 256 / lanes - 1) / (256 / lanes);
+#define MOE_RUN(LPT, EPL)                                                                                         \
+  (out16 ? (vec ? route_backward_kernel<LPT, EPL, true, true> : route_backward_kernel<LPT, EPL, true, false>)     \
+         : (vec ? route_backward_kernel<LPT, EPL, false, true> : route_backward_kernel<LPT, EPL, false, false>))  \
+      <<<blocks, 256, 0, stream>>>(r, logits, idx, dgate, T, E, k, out32, out16, ld, err)
+  if (ld <= 128)
+    MOE_RUN(16, 8);
+  else if (lanes == 16)
+    MOE_RUN(16, 16);
+  else if (ld <= 384)
+    MOE_RUN(32, 12);
+  else if (lanes == 32)
+    MOE_RUN(32, 16);
+  else
+    MOE_RUN(64, 16);
 #undef MOE_RUN
   return hipGetLastError();
 }

@@ -15,6 +15,8 @@
 //           expert offsets S_l (block-wide scan);
 //   place : o = chunk base + local ordinal, then the closed form above (M
 //           staged in LDS); writes the table row and its inverse.
+// A single rank with few routes gets the whole of it in one workgroup
+// (sched_small_kernel).
 
 #include "common.h"
 #include "gemm_common.h"
@@ -202,9 +204,72 @@ __global__ __launch_bounds__(256) void sched_place_kernel(const int32_t* __restr
   }
 }
 
+// The whole schedule in one workgroup, for one source rank with at most 1024
+// routes (where three launches would cost three times the work): one route per
+// thread, its rank among its wave's equal routes by ballots, per-wave counts
+// turned into prefixes over the waves, and the expert offsets by a block scan.
+// With one rank the closed form is S_l + o.
+__global__ __launch_bounds__(1024) void sched_small_kernel(const int32_t* __restrict__ A, int NK, int L,
+                                                           int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                                                           int64_t max_rows, int32_t* __restrict__ sched_src,
+                                                           int32_t* __restrict__ route_dst, int* err) {
+  __shared__ uint16_t wcnt[16][kMaxExperts];  // routes of each wave to each expert, then of the waves before it
+  __shared__ int start_s[kMaxExperts];
+  const int tid = threadIdx.x, w = tid / kWave, lane = lane_id();
+  for (int i = tid; i < 16 * kMaxExperts / 2; i += 1024) reinterpret_cast<uint32_t*>(wcnt)[i] = 0;
+  __syncthreads();
+  int l = -1;
+  if (tid < NK) {
+    l = A[tid];
+    if (l < 0 || l >= L) {
+      raise_error(err, kErrExpertRange);
+      l = -1;
+    }
+  }
+  const int nbits = 32 - __clz(L);
+  uint64_t same = __ballot(l >= 0);
+  for (int bit = 0; bit < nbits; ++bit) {
+    const bool set = (l >> bit) & 1;
+    const uint64_t bal = __ballot(set);
+    same &= set ? bal : ~bal;
+  }
+  const int rank = __popcll(same & ((lane == 0) ? 0ull : (~0ull >> (kWave - lane))));
+  if (l >= 0 && rank == 0) wcnt[w][l] = static_cast<uint16_t>(__popcll(same));
+  __syncthreads();
+  int cnt = 0;
+  if (tid < L) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int n = wcnt[v][tid];
+      wcnt[v][tid] = static_cast<uint16_t>(cnt);
+      cnt += n;
+    }
+    counts[tid] = cnt;
+  }
+  int total = 0;
+  const int start = block_exclusive_scan_1024(cnt, &total);
+  if (tid < L) {
+    offsets[tid] = start;
+    start_s[tid] = start;
+  }
+  if (tid == 0) {
+    offsets[L] = total;
+    if (total > max_rows) raise_error(err, kErrRowOverflow);
+  }
+  __syncthreads();
+  if (tid >= NK) return;
+  const int64_t pos = l >= 0 ? int64_t(start_s[l]) + wcnt[w][l] + rank : max_rows;
+  if (pos < max_rows) sched_src[pos] = tid;
+  route_dst[tid] = pos < max_rows ? static_cast<int32_t>(pos) : -1;
+}
+
 hipError_t launch_schedule(const int32_t* routes, int R, int NK, int c, int L, int E_total, int64_t max_rows,
                            int32_t* counts, int32_t* offsets, int32_t* sched_src, int32_t* route_dst,
                            const SchedScratch& s, int* err, hipStream_t stream) {
+  if (R == 1 && c == 0 && L == E_total && NK <= 1024) {
+    sched_small_kernel<<<1, 1024, 0, stream>>>(routes, NK, L, counts, offsets, max_rows, sched_src, route_dst, err);
+    return hipGetLastError();
+  }
   const int nch = sched_chunks(NK);
   if (NK > 0) {
     sched_count_kernel<<<dim3(nch, R), 256, 0, stream>>>(routes, NK, c, L, E_total, nch, s.ord_local, s.chunk_cnt,
