@@ -472,12 +472,14 @@ hipError_t run_height(const I8GemmArgs& a, hipStream_t stream) {
 // the few-rows kernel (7168 x 2048, 256 experts, 64 tokens: 1.68 ms against
 // 1.66 with 64-row tiles; 4 tokens: 0.30 against 0.34), up to 48 rows 64-row
 // tiles (512 tokens: 2.04 ms against 2.07 with 128 and 2.41 with the few-rows
-// kernel), then by how many rounds of 256-row items the chip runs: with five or
-// more, 256-row tiles (2048 tokens: 2.43 against 2.49 ms with 128), 320-row ones
-// where segments of about 256 rows would often need two (8192 tokens: 4.32 ms
-// against 4.69 with 256 and 5.29 with 128); with fewer, 128-row tiles, whose
-// items fill the last round better (2048 x 768, 128 experts, 4096 tokens: 0.50
-// ms against 0.51; 2048 tokens: 0.32 against 0.37).
+// kernel).  From 192 rows on 320-row tiles, whose waves read the fewest bytes
+// per product, where their items make two rounds over the chip (8192 tokens:
+// 4.23 ms against 4.68 with 256 and 5.18 with 128; 1024 x 1024, 32 experts, 512
+// rows each: 187 us against 206 and 196); between, 256-row tiles if their items
+// make five rounds (2048 tokens: 2.40 ms against 2.47 with 128 and 2.63 with
+// 320), else 128-row tiles, which fill the last round better (2048 x 768, 128
+// experts, 128 rows each: 307 us against 332 with 256; 1024 x 1024, 32 experts,
+// 256 rows each: 134 us against 145 with 320).
 //
 // Dense: the few-rows kernel while its workgroups fit the chip at once (256 x
 // 2048 x 7168: 24 us against 32 with 64-row tiles), else the least rounds times
@@ -490,9 +492,9 @@ int i8_tile_rows(int64_t rows, int64_t groups, int64_t N) {
   if (groups > 1) {
     if (rows <= 4 * groups) return kI8RowsBM;
     if (rows <= 48 * groups) return 64;
-    const int64_t items = groups * ceil_div(rows, 256 * groups) * ceil_div(N, 128);
-    if (items < 5 * cus) return 128;
-    return rows >= 192 * groups && rows <= 320 * groups ? 320 : 256;
+    const auto items = [&](int bm) { return groups * ceil_div(rows, bm * groups) * ceil_div(N, 128); };
+    if (rows >= 192 * groups) return items(320) >= 2 * cus ? 320 : 128;
+    return items(256) >= 5 * cus ? 256 : 128;
   }
   if (ceil_div(rows, kI8RowsBM) * ceil_div(N, 64) <= cus) return kI8RowsBM;
   int best = 0;
