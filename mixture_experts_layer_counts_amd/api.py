@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -35,6 +36,9 @@ def _on(device: torch.device):
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device: torch.device) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device != device:
@@ -91,6 +95,33 @@ def router_for(score: str = "sigmoid", groups: int = 1, kept_groups: int = 1, gr
     return r
 
 
+def _weight_specs(s: _lib.MoeShape):
+    """(moe_weights field, name in ``weights``, dtype, shape) of every tensor ``forward`` reads."""
+    L, D, I, Is = s.experts_per_rank, s.D, s.I, s.I_shared
+    routed = (("gate", I, D), ("up", I, D), ("down", D, I))
+    shared = (("gate", Is, D), ("up", Is, D), ("down", D, Is))
+    out = []
+    for n, N, K in routed:
+        if s.precision == _lib.MOE_BF16:
+            # row-major [L, N, K], or K-tiled [L, K/64, N, 64] (tile_bf16)
+            out.append(("w_" + n, "w_" + n, torch.bfloat16, (L, K // 64, N, 64) if s.weights_tiled else (L, N, K)))
+            continue
+        # row-major [L, N, K] bytes, or K-tiled [L, K/128, N, 128] (tile_mxfp8, tile_int8)
+        shp = (L, K // 128, N, 128) if s.weights_tiled else (L, N, K)
+        if s.precision == _lib.MOE_INT8:  # int8 and a scale per row (quantize_int8)
+            out += [("w_" + n, "q_" + n, torch.int8, shp), ("s_" + n, "s_" + n, torch.float32, (L, N))]
+        else:
+            out += [("w_" + n, "q_" + n, torch.uint8, shp), ("s_" + n, "s_" + n, torch.uint8, (L, K // 128, N, 4))]
+    for n, N, K in shared:
+        if s.shared_precision == _lib.MOE_BF16:
+            out.append(("ws_" + n, "ws_" + n, torch.bfloat16, (N, K)))
+        elif s.shared_precision == _lib.MOE_INT8:
+            out += [("ws_" + n, "qs_" + n, torch.int8, (N, K)), ("ss_" + n, "ss_" + n, torch.float32, (N,))]
+        else:  # E4M3 bytes and packed scales (quantize_mxfp8, pack_mxfp8_scales)
+            out += [("ws_" + n, "qs_" + n, torch.uint8, (N, K)), ("ss_" + n, "ss_" + n, torch.uint8, (K // 128, N, 4))]
+    return out
+
+
 class MoELayer:
     """One layer's shape plus its device workspace, on ``device``."""
 
@@ -107,6 +138,8 @@ class MoELayer:
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=self.device)
         _lib.check("moe_workspace_init",
                    self.lib.moe_workspace_init(ctypes.byref(shape), _ptr(self.ws), self.ws_bytes, _stream()))
+
+        self._weight_specs = _weight_specs(shape)
 
     # -- sizes -------------------------------------------------------------
     @property
@@ -186,53 +219,15 @@ class MoELayer:
     def forward(self, weights: Dict[str, torch.Tensor], x_src: torch.Tensor, x_local: torch.Tensor,
                 gate: torch.Tensor, sched: Dict[str, torch.Tensor], out32: bool = True,
                 out: Optional[torch.Tensor] = None, out_f32: Optional[torch.Tensor] = None):
-        s, dev = self.shape, self.device
-        L, D, I, Is = s.experts_per_rank, s.D, s.I, s.I_shared
+        s, dev, D = self.shape, self.device, self.shape.D
         _need(x_local, "x_local", torch.bfloat16, (s.T, D), dev)
         _need(x_src, "x_src", torch.bfloat16, (s.num_src_ranks * s.T, D), dev)
         _need(gate, "gate", torch.float32, (s.T, s.k), dev)
         w = _lib.MoeWeights()
-        if s.precision == _lib.MOE_BF16:
-            for n, (N, K) in (("w_gate", (I, D)), ("w_up", (I, D)), ("w_down", (D, I))):
-                # row-major [L, N, K], or K-tiled [L, K/64, N, 64] (tile_bf16)
-                _need(weights[n], n, torch.bfloat16, (L, K // 64, N, 64) if s.weights_tiled else (L, N, K), dev)
-                setattr(w, n, _ptr(weights[n]))
-        elif s.precision == _lib.MOE_INT8:
-            for n, qn, sn, shp in (("w_gate", "q_gate", "s_gate", (L, I, D)), ("w_up", "q_up", "s_up", (L, I, D)),
-                                   ("w_down", "q_down", "s_down", (L, D, I))):
-                # row-major [L, N, K], or K-tiled [L, K/128, N, 128] (tile_int8); scales [L, N]
-                _need(weights[qn], qn, torch.int8,
-                      (L, shp[2] // 128, shp[1], 128) if s.weights_tiled else shp, dev)
-                _need(weights[sn], sn, torch.float32, shp[:2], dev)
-                setattr(w, n, _ptr(weights[qn]))
-                setattr(w, sn, _ptr(weights[sn]))
-        else:
-            for n, qn, sn, shp in (("w_gate", "q_gate", "s_gate", (L, I, D)), ("w_up", "q_up", "s_up", (L, I, D)),
-                                   ("w_down", "q_down", "s_down", (L, D, I))):
-                # row-major [L, N, K] bytes, or K-tiled [L, K/128, N, 128] (tile_mxfp8)
-                _need(weights[qn], qn, torch.uint8,
-                      (L, shp[2] // 128, shp[1], 128) if s.weights_tiled else shp, dev)
-                _need(weights[sn], sn, torch.uint8, (L, shp[2] // 128, shp[1], 4), dev)
-                setattr(w, n, _ptr(weights[qn]))
-                setattr(w, sn, _ptr(weights[sn]))
-        if s.shared_precision == _lib.MOE_BF16:
-            for n, shp in (("ws_gate", (Is, D)), ("ws_up", (Is, D)), ("ws_down", (D, Is))):
-                _need(weights[n], n, torch.bfloat16, shp, dev)
-                setattr(w, n, _ptr(weights[n]))
-        elif s.shared_precision == _lib.MOE_INT8:  # int8 "qs_*" and row scales "ss_*" (quantize_int8)
-            for n, qn, sn, shp in (("ws_gate", "qs_gate", "ss_gate", (Is, D)), ("ws_up", "qs_up", "ss_up", (Is, D)),
-                                   ("ws_down", "qs_down", "ss_down", (D, Is))):
-                _need(weights[qn], qn, torch.int8, shp, dev)
-                _need(weights[sn], sn, torch.float32, shp[:1], dev)
-                setattr(w, n, _ptr(weights[qn]))
-                setattr(w, sn, _ptr(weights[sn]))
-        else:  # E4M3 bytes "qs_*" and packed scales "ss_*" (quantize_mxfp8, pack_mxfp8_scales)
-            for n, qn, sn, shp in (("ws_gate", "qs_gate", "ss_gate", (Is, D)), ("ws_up", "qs_up", "ss_up", (Is, D)),
-                                   ("ws_down", "qs_down", "ss_down", (D, Is))):
-                _need(weights[qn], qn, torch.uint8, shp, dev)
-                _need(weights[sn], sn, torch.uint8, (shp[1] // 128, shp[0], 4), dev)
-                setattr(w, n, _ptr(weights[qn]))
-                setattr(w, sn, _ptr(weights[sn]))
+        for field, name, dtype, shp in self._weight_specs:
+            t = weights[name]
+            _need(t, name, dtype, shp, dev)
+            setattr(w, field, t.data_ptr())
         if out is None:
             out = torch.empty((s.T, D), dtype=torch.bfloat16, device=dev)
         _need(out, "out", torch.bfloat16, (s.T, D), dev)
@@ -485,6 +480,14 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _linear_ws_bytes(M: int, N: int, K: int) -> int:
+    nbytes = ctypes.c_size_t(0)
+    _lib.check("moe_linear_int8_workspace_bytes",
+               _lib.load().moe_linear_int8_workspace_bytes(M, N, K, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
 def linear_int8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
                 out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """x [..., K] (bf16 or fp32) -> [..., N]: x's rows quantised (quantize_int8),
@@ -502,14 +505,13 @@ def linear_int8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     if out_dtype not in _INT8_DTYPES:
         raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
     M = x.numel() // K
-    nbytes = ctypes.c_size_t(0)
-    _lib.check("moe_linear_int8_workspace_bytes", lib.moe_linear_int8_workspace_bytes(M, N, K, ctypes.byref(nbytes)))
+    nbytes = _linear_ws_bytes(M, N, K)
     with _on(dev):
         out = torch.empty(x.shape[:-1] + (N,), dtype=out_dtype, device=dev)
-        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev) if nbytes.value else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         _lib.check("moe_linear_int8", lib.moe_linear_int8(
             _ptr(x), _INT8_DTYPES[x.dtype], M, K, _ptr(w), _ptr(w_scale), N, _ptr(out), _INT8_DTYPES[out_dtype],
-            _ptr(ws), nbytes.value, _stream()))
+            _ptr(ws), nbytes, _stream()))
     return out
 
 

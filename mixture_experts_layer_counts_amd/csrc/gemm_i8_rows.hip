@@ -171,22 +171,32 @@ __device__ __forceinline__ void rows_item(const I8GemmArgs& a, int e, int64_t p0
                                        [&](int rb) { return a.As[arow[rb]]; });
 }
 
-template <int NBL, int WAVES, int EPI>
-__device__ __forceinline__ void rows_block(const I8GemmArgs& a, int block, i32x4_t* red) {
-  const int n_blocks = (a.N + 16 * NBL - 1) / (16 * NBL);
-  const int ti = block / n_blocks, n0 = block % n_blocks * 16 * NBL;
-  int e = 0, nrows;
-  int64_t p0;
+// Block `block` of a product in blocks of COLS columns: its expert, rows and
+// first column; false if there is none (past the last tile).
+template <int COLS>
+__device__ __forceinline__ bool find_block(const I8GemmArgs& a, int block, int& e, int64_t& p0, int& nrows, int& n0) {
+  const int n_blocks = (a.N + COLS - 1) / COLS;
+  const int ti = block / n_blocks;
+  n0 = block % n_blocks * COLS;
   if (a.tiles) {
-    if (ti >= *a.tile_count) return;
+    if (ti >= *a.tile_count) return false;
     const int4 t = a.tiles[ti];
     e = t.x & 1023;
     p0 = t.y;
     nrows = t.z;
   } else {
+    e = 0;
     p0 = static_cast<int64_t>(ti) * kI8RowsBM;
     nrows = static_cast<int>(min(static_cast<int64_t>(kI8RowsBM), a.dense_rows - p0));
   }
+  return true;
+}
+
+template <int NBL, int WAVES, int EPI>
+__device__ __forceinline__ void rows_block(const I8GemmArgs& a, int block, i32x4_t* red) {
+  int e, nrows, n0;
+  int64_t p0;
+  if (!find_block<16 * NBL>(a, block, e, p0, nrows, n0)) return;
   if (nrows <= 16)
     rows_item<NBL, 1, WAVES, EPI>(a, e, p0, nrows, n0, red);
   else
@@ -206,71 +216,102 @@ __global__ __launch_bounds__(WAVES* kWave) void gemm_i8_rows_kernel(const I8Gemm
     rows_block<NBL, WAVES, EPI1>(b, block - blocks0, red);
 }
 
-// A product that quantises its own activations, for one or two rows: every
-// workgroup reads them (out of L2) and keeps their quotients in LDS, which costs
-// less than a launch before it (1 x 2048 x 7168: 10.4 us against 15.2, 2 rows
-// 12.3 against 14.9; three rows already 15.3 against 14.7).  a: B, Bs, N, K (the padded width), C, ldc and
-// dense_rows = M.
-constexpr int kFusedWaves = 8, kFusedRows = 2, kFusedLds = 48 * 1024;
+// ---- products that quantise their own activations, one or two rows at a time: every workgroup reads its rows x [.][K] (out of L2) and keeps their
+// quotients in LDS, which costs less than a launch before it (1 x 2048 x 7168:
+// 10.4 us against 15.2, 2 rows 12.3 against 14.9; three rows already 15.3
+// against 14.7).  a: as for the other products, without A and As. ----
+constexpr int kFusedRows = 2, kFusedLds = 48 * 1024;
 
-template <int NBL, int EPI, bool VEC, typename T>
-__global__ __launch_bounds__(kFusedWaves* kWave) void linear_i8_rows_kernel(const I8GemmArgs a,
-                                                                            const T* __restrict__ x, int K) {
-  __shared__ __attribute__((aligned(16))) char xq[kFusedLds];
-  __shared__ i32x4_t red[kFusedWaves * NBL * kWave];
-  __shared__ uint32_t part[kFusedRows][kFusedWaves];
+template <int NBL, int WAVES, int EPI, bool VEC, typename T>
+__device__ __forceinline__ void fused_block(const I8GemmArgs& a, const T* __restrict__ x, int K, int per, int block,
+                                            char* xq, i32x4_t* red, uint32_t (&part)[kFusedRows][WAVES]) {
+  int e, tile_rows, n0;
+  int64_t p0;
+  if (!find_block<16 * NBL>(a, block, e, p0, tile_rows, n0)) return;
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int M = a.dense_rows, chunks = a.K / kI8Chunk;
-  const int stride = a.K + 16;  // 16 rows at one K position fall on distinct banks
-  for (int m = 0; m < M; ++m) {
-    uint32_t bits = 0;
-    for (int c = tid; c < chunks; c += kFusedWaves * kWave) {
-      float v[kI8Chunk];
-      i8_load_chunk<VEC>(x + static_cast<int64_t>(m) * K, c, K, v);
-      bits = i8_max_bits(v, bits);
-    }
+  const int chunks = a.K / kI8Chunk;
+  const int stride = a.K + 16;  // rows at one K position fall on distinct banks
+  // `per` rows at a time: all of a tile's, unless a token names its expert twice
+  for (int base = 0; base < tile_rows; base += per) {
+    const int nrows = tile_rows - base < per ? tile_rows - base : per;
+    if (base > 0) __syncthreads();  // the rows before are done with the LDS
+    for (int m = 0; m < nrows; ++m) {
+      const T* __restrict__ row = x + i8_a_row(a, p0 + base + m) * K;
+      uint32_t bits = 0;
+      for (int c = tid; c < chunks; c += WAVES * kWave) {
+        float v[kI8Chunk];
+        i8_load_chunk<VEC>(row, c, K, v);
+        bits = i8_max_bits(v, bits);
+      }
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-      const uint32_t o = __shfl_xor(bits, d);
-      bits = o > bits ? o : bits;
+      for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t o = __shfl_xor(bits, d);
+        bits = o > bits ? o : bits;
+      }
+      if (lane == 0) part[m][wave] = bits;
     }
-    if (lane == 0) part[m][wave] = bits;
-  }
-  __syncthreads();
-  auto row_bits = [&](int m) {
-    uint32_t bits = 0;
+    __syncthreads();
+    auto row_bits = [&](int m) {
+      uint32_t bits = 0;
 #pragma unroll
-    for (int w = 0; w < kFusedWaves; ++w) bits = part[m][w] > bits ? part[m][w] : bits;
-    return bits;
-  };
-  for (int m = 0; m < M; ++m) {
-    const I8RowScale quant(row_bits(m));
-    for (int c = tid; c < chunks; c += kFusedWaves * kWave) {
-      float v[kI8Chunk];
-      i8_load_chunk<VEC>(x + static_cast<int64_t>(m) * K, c, K, v);
-      *reinterpret_cast<uint2*>(xq + m * stride + c * kI8Chunk) = quant(v);
+      for (int w = 0; w < WAVES; ++w) bits = part[m][w] > bits ? part[m][w] : bits;
+      return bits;
+    };
+    for (int m = 0; m < nrows; ++m) {
+      const T* __restrict__ row = x + i8_a_row(a, p0 + base + m) * K;
+      const I8RowScale quant(row_bits(m));
+      for (int c = tid; c < chunks; c += WAVES * kWave) {
+        float v[kI8Chunk];
+        i8_load_chunk<VEC>(row, c, K, v);
+        *reinterpret_cast<uint2*>(xq + m * stride + c * kI8Chunk) = quant(v);
+      }
     }
+    __syncthreads();
+    const int row = (lane & 15) < nrows ? lane & 15 : nrows - 1;
+    const LdsRows rows{xq + row * stride + (lane >> 4) * 16};
+    i32x4_t acc[1][NBL][1];
+    rows_sums<1, NBL, 1, WAVES>(a, e, n0, rows, wave, lane, acc);
+    rows_finish<1, NBL, 1, WAVES, EPI>(a, e, p0 + base, nrows, n0, red, wave, lane, acc,
+                                       [&](int) { return I8RowScale(row_bits(row)).scale; });
   }
-  __syncthreads();
-  const int n0 = static_cast<int>(blockIdx.x) * 16 * NBL;
-  const int row = (lane & 15) < M ? lane & 15 : M - 1;
-  const LdsRows rows{xq + row * stride + (lane >> 4) * 16};
-  i32x4_t acc[1][NBL][1];
-  rows_sums<1, NBL, 1, kFusedWaves>(a, 0, n0, rows, wave, lane, acc);
-  rows_finish<1, NBL, 1, kFusedWaves, EPI>(a, 0, 0, M, n0, red, wave, lane, acc,
-                                           [&](int) { return I8RowScale(row_bits(row)).scale; });
+}
+
+template <int WAVES, int EPI, bool VEC, typename T>
+__global__ __launch_bounds__(WAVES* kWave) void linear_i8_rows_kernel(const I8GemmArgs a, const T* __restrict__ x,
+                                                                      int K) {
+  extern __shared__ __attribute__((aligned(16))) char xq[];
+  __shared__ i32x4_t red[WAVES * kWave];
+  __shared__ uint32_t part[kFusedRows][WAVES];
+  fused_block<1, WAVES, EPI, VEC>(a, x, K, a.dense_rows, blockIdx.x, xq, red, part);
+}
+
+// Two products over fp32 rows of their K (both a multiple of 128).
+template <int NBL, int WAVES, int EPI0, int EPI1>
+__global__ __launch_bounds__(WAVES* kWave) void fused_pair_i8_kernel(const I8GemmArgs a, const float* __restrict__ xa,
+                                                                     const I8GemmArgs b, const float* __restrict__ xb,
+                                                                     int per, int blocks0) {
+  extern __shared__ __attribute__((aligned(16))) char xq[];
+  __shared__ i32x4_t red[WAVES * NBL * kWave];
+  __shared__ uint32_t part[kFusedRows][WAVES];
+  const int block = blockIdx.x;
+  if (block < blocks0)
+    fused_block<NBL, WAVES, EPI0, true>(a, xa, a.K, per, block, xq, red, part);
+  else
+    fused_block<NBL, WAVES, EPI1, true>(b, xb, b.K, per, block - blocks0, xq, red, part);
 }
 
 template <int EPI, typename T>
 hipError_t run_linear(const I8GemmArgs& a, const void* x, int64_t K, hipStream_t stream) {
+  constexpr int kWaves = 8;
   const T* src = static_cast<const T*>(x);
   const bool vec = K % (16 / sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
-  const dim3 grid((a.N + 15) / 16), block(kFusedWaves * kWave);
+  const dim3 grid((a.N + 15) / 16), block(kWaves * kWave);
+  const size_t lds = static_cast<size_t>(a.dense_rows) * (a.K + 16);
   if (vec)
-    linear_i8_rows_kernel<1, EPI, true, T><<<grid, block, 0, stream>>>(a, src, static_cast<int>(K));
+    linear_i8_rows_kernel<kWaves, EPI, true, T><<<grid, block, lds, stream>>>(a, src, static_cast<int>(K));
   else
-    linear_i8_rows_kernel<1, EPI, false, T><<<grid, block, 0, stream>>>(a, src, static_cast<int>(K));
+    linear_i8_rows_kernel<kWaves, EPI, false, T><<<grid, block, lds, stream>>>(a, src, static_cast<int>(K));
   return hipGetLastError();
 }
 
@@ -340,19 +381,33 @@ hipError_t launch_gemm_i8(const I8GemmArgs& a, int epilogue, hipStream_t stream)
   }
 }
 
-bool linear_i8_fused(int64_t M, int64_t N, int64_t K) {
-  return M <= kFusedRows && M * (K + 16) <= kFusedLds;
-}
+bool linear_i8_fused(int64_t M, int64_t K) { return M <= kFusedRows && M * (K + 16) <= kFusedLds; }
 
 hipError_t launch_linear_i8_fused(const I8GemmArgs& a, const void* x, bool x_f32, int64_t K, int epilogue,
                                   hipStream_t stream) {
-  if (!x || K > a.K || K <= a.K - kStage || a.K % kStage || !linear_i8_fused(a.dense_rows, a.N, a.K))
+  if (!x || K > a.K || K <= a.K - kStage || a.K % kStage || !linear_i8_fused(a.dense_rows, a.K))
     return hipErrorInvalidValue;
   if (epilogue == kEpiBF16)
     return x_f32 ? run_linear<kEpiBF16, float>(a, x, K, stream) : run_linear<kEpiBF16, uint16_t>(a, x, K, stream);
   if (epilogue == kEpiF32)
     return x_f32 ? run_linear<kEpiF32, float>(a, x, K, stream) : run_linear<kEpiF32, uint16_t>(a, x, K, stream);
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_fused_pair_i8(const I8GemmArgs& a, const float* xa, const I8GemmArgs& b, const float* xb,
+                                int64_t rows, hipStream_t stream) {
+  for (const I8GemmArgs* x : {&a, &b})
+    if (x->K % kStage || x->N <= 0 || !linear_i8_fused(rows, x->K)) return hipErrorInvalidValue;
+  if (!xa || !xb || reinterpret_cast<uintptr_t>(xa) % 16 || reinterpret_cast<uintptr_t>(xb) % 16)
+    return hipErrorInvalidValue;
+  constexpr int kBlocks = 4, kWaves = 4;  // 64 columns and four waves, as for products of this size elsewhere
+  const int64_t first = rows_blocks(a, 16 * kBlocks), work = first + rows_blocks(b, 16 * kBlocks);
+  if (work > 0x7fffffff) return hipErrorInvalidValue;
+  const size_t lds = static_cast<size_t>(rows) * ((a.K > b.K ? a.K : b.K) + 16);
+  fused_pair_i8_kernel<kBlocks, kWaves, kEpiBF16, kEpiF32>
+      <<<static_cast<unsigned>(work), kWaves * kWave, lds, stream>>>(a, xa, b, xb, static_cast<int>(rows),
+                                                                           static_cast<int>(first));
+  return hipGetLastError();
 }
 
 hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream) {

@@ -210,9 +210,14 @@ hipError_t launch_gemm_i8_tiles(const I8GemmArgs& args, int epilogue, hipStream_
 hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 // A dense product of M bf16 or fp32 rows [M][K] that quantises them itself, where
 // linear_i8_fused says so (a.A and a.As unused; a.K is K rounded up to 128).
-bool linear_i8_fused(int64_t M, int64_t N, int64_t K);
+bool linear_i8_fused(int64_t M, int64_t K);
 hipError_t launch_linear_i8_fused(const I8GemmArgs& a, const void* x, bool x_f32, int64_t K, int epilogue,
                                   hipStream_t stream);
+// Two products (bf16 and fp32) over fp32 rows [.][K] that quantise them
+// themselves, `rows` rows of a tile at a time; linear_i8_fused(rows, K) holds for
+// both.
+hipError_t launch_fused_pair_i8(const I8GemmArgs& a, const float* xa, const I8GemmArgs& b, const float* xb,
+                                int64_t rows, hipStream_t stream);
 // Two few-rows products in one launch: both SwiGLU, or bf16 and fp32.
 hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream);
 
@@ -233,6 +238,11 @@ struct QuantI8Args {
   int* err;
 };
 hipError_t launch_quantize_rows_i8(const QuantI8Args& args, bool src_f32, int64_t rows, hipStream_t stream);
+// Rows of bf16 into int8, and the tile lists of one minibatch
+// (launch_build_tiles), in one launch.
+hipError_t launch_rows_and_tiles_i8(const QuantI8Args& args, int64_t rows, const int32_t* offsets, int L,
+                                    int64_t max_rows, int BM, int max_tiles, int4* tiles, int32_t* tile_count,
+                                    int32_t* runs, hipStream_t stream);
 // The rows of two fp32 matrices in one launch.
 hipError_t launch_quantize_two_i8(const QuantI8Args& a, int64_t rows_a, const QuantI8Args& b, int64_t rows_b,
                                   hipStream_t stream);

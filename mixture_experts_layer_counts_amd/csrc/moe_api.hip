@@ -588,6 +588,48 @@ hipError_t run_ffn_i8(const I8Ffn& f, int up_id, int down_id, hipStream_t s) {
   return e == hipSuccess ? moe::launch_gemm_i8(f.down, f.down_epi, s) : e;
 }
 
+// Routed and shared experts int8, on one GPU, with so few tokens in one
+// minibatch that all products take the few-rows kernels: the shared expert then
+// rides in the routed experts' launches.
+bool few_tokens_i8(const moe_shape* s, const Layout& L, const void* x_src, const void* x_local) {
+  return s->precision == MOE_INT8 && s->shared_precision == MOE_INT8 && s->num_src_ranks == 1 && s->T > 0 &&
+         x_src == x_local && reinterpret_cast<uintptr_t>(x_src) % 16 == 0 && L.n_minibatches == 1 &&
+         L.routed_bm == moe::kI8RowsBM && moe::i8_tile_rows(s->T, 1, s->I_shared) == moe::kI8RowsBM &&
+         moe::i8_tile_rows(s->T, 1, s->D) == moe::kI8RowsBM;
+}
+
+// Its launches: tokens quantised beside the tile list, up/gate of both, h's rows
+// (within the down product for one or two tokens), down of both.
+hipError_t few_tokens_experts_i8(const moe_shape* shape, const moe_weights* w, const void* x,
+                                 const int32_t* sched_src, const int32_t* expert_offsets, const Layout& L, void* ws,
+                                 hipStream_t s) {
+  const int64_t T = shape->T, D = shape->D;
+  int8_t* xq = at<int8_t>(ws, L.ring);
+  float* xs = at<float>(ws, L.ring_s);
+  hipError_t e;
+  {
+    ProbeScope probe(MOE_K_GATHER, s);
+    e = moe::launch_rows_and_tiles_i8(quant_args(x, D, xq, xs), T, expert_offsets,
+                                      static_cast<int>(shape->experts_per_rank), shape->max_rows, L.routed_bm,
+                                      L.max_tiles, at<int4>(ws, L.tiles), at<int32_t>(ws, L.tile_count),
+                                      at<int32_t>(ws, L.tile_runs), s);
+    if (e != hipSuccess) return e;
+  }
+  const I8Ffn f = routed_ffn_i8(shape, w, sched_src, expert_offsets, L, ws, 0, 0, shape->max_rows);
+  const I8Ffn sh = shared_ffn_i8(shape, w, xq, xs, L, ws);
+  {
+    ProbeScope probe(MOE_K_UP_GATE, s);
+    e = moe::launch_gemm_i8_pair(f.up, moe::kEpiSwiGLU, sh.up, moe::kEpiSwiGLU, s);
+    if (e != hipSuccess) return e;
+  }
+  ProbeScope probe(MOE_K_DOWN, s);
+  if (moe::linear_i8_fused(T, shape->I) && moe::linear_i8_fused(T, shape->I_shared))
+    return moe::launch_fused_pair_i8(f.down, static_cast<const float*>(f.h.src), sh.down,
+                                     static_cast<const float*>(sh.h.src), T, s);
+  e = moe::launch_quantize_two_i8(f.h, f.h_rows, sh.h, sh.h_rows, s);
+  return e == hipSuccess ? moe::launch_gemm_i8_pair(f.down, f.down_epi, sh.down, sh.down_epi, s) : e;
+}
+
 // The int8 experts of moe_forward: those of the routed and the shared expert
 // that are int8.  `shared` and `routed` say which.
 hipError_t experts_i8(const moe_shape* shape, const moe_weights* w, const void* x_src, const void* x_local,
@@ -613,19 +655,6 @@ hipError_t experts_i8(const moe_shape* shape, const moe_weights* w, const void* 
       if (e != hipSuccess) return e;
     }
     sh = shared_ffn_i8(shape, w, xq, xs, L, ws);
-    // a few tokens: the shared expert rides in the routed experts' launches
-    if (tokens && L.n_minibatches == 1 && L.routed_bm == moe::kI8RowsBM && sh.up.tile_rows == moe::kI8RowsBM &&
-        sh.down.tile_rows == moe::kI8RowsBM) {
-      const I8Ffn f = routed_ffn_i8(shape, w, sched_src, expert_offsets, L, ws, 0, 0, shape->max_rows);
-      {
-        ProbeScope probe(MOE_K_UP_GATE, s);
-        const hipError_t e = moe::launch_gemm_i8_pair(f.up, moe::kEpiSwiGLU, sh.up, moe::kEpiSwiGLU, s);
-        if (e != hipSuccess) return e;
-      }
-      ProbeScope probe(MOE_K_DOWN, s);
-      const hipError_t e = moe::launch_quantize_two_i8(f.h, f.h_rows, sh.h, sh.h_rows, s);
-      return e == hipSuccess ? moe::launch_gemm_i8_pair(f.down, f.down_epi, sh.down, sh.down_epi, s) : e;
-    }
     const hipError_t e = run_ffn_i8(sh, MOE_K_SHARED_UP, MOE_K_SHARED_DOWN, s);
     if (e != hipSuccess) return e;
   }
@@ -826,7 +855,8 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
 
   // 1. tile lists of every minibatch (and their XCD runs), from the
   // device-side expert offsets
-  {
+  const bool few_i8 = few_tokens_i8(shape, L, x_src, x_local);
+  if (!few_i8) {
     ProbeScope probe(MOE_K_TILES, s);
     MOE_TRY_HIP(moe::launch_build_tiles(expert_offsets, Lx, b, shape->max_rows, bm,
                                         static_cast<int>(L.n_minibatches), L.max_tiles,
@@ -996,7 +1026,9 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
     }
   }
 
-  if (i8 || shared_i8)
+  if (few_i8)
+    MOE_TRY_HIP(few_tokens_experts_i8(shape, w, x_src, sched_src, expert_offsets, L, ws, s));
+  else if (i8 || shared_i8)
     MOE_TRY_HIP(experts_i8(shape, w, x_src, x_local, sched_src, expert_offsets, L, ws, shared_i8 && T > 0, i8, s));
 
   // 4. fixed-order gate-weighted combine
@@ -1083,7 +1115,7 @@ static moe_status linear_sizes(int64_t M, int64_t N, int64_t K, int64_t* Kp, siz
   *Kp = (K + 127) / 128 * 128;
   if (M * *Kp >= kLimit || N * *Kp >= kLimit) return MOE_ERR_UNSUPPORTED;
   // the quantised rows, then their scales
-  *ws = M == 0 || N == 0 || moe::linear_i8_fused(M, N, *Kp) ? 0 : M * *Kp + sizeof(float) * M;
+  *ws = M == 0 || N == 0 || moe::linear_i8_fused(M, *Kp) ? 0 : M * *Kp + sizeof(float) * M;
   return MOE_OK;
 }
 

@@ -20,6 +20,7 @@
 
 #include "common.h"
 #include "gemm_common.h"
+#include "i8.h"
 #include "kernels.h"
 
 namespace moe {
@@ -317,11 +318,10 @@ int sched_chunks(int NK) { return NK > 0 ? (NK + kSchedChunk - 1) / kSchedChunk 
 // non-empty).  Balanced runs stay far inside the cap: a tile costs between 1
 // and 2 times BM / 32 units, so a run of one eighth of the cost holds at most
 // about a quarter of the tiles.
-__global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __restrict__ offsets, int L, int64_t b,
-                                                           int64_t max_rows, int BM, int max_tiles,
-                                                           int4* __restrict__ tiles, int32_t* __restrict__ tile_count,
-                                                           int32_t* __restrict__ runs) {
-  const int m = blockIdx.x, l = threadIdx.x;
+__device__ __forceinline__ void build_tiles(int m, const int32_t* __restrict__ offsets, int L, int64_t b,
+                                            int64_t max_rows, int BM, int max_tiles, int4* __restrict__ tiles,
+                                            int32_t* __restrict__ tile_count, int32_t* __restrict__ runs) {
+  const int l = threadIdx.x;
   // rows past max_rows were never placed (the schedule flagged the overflow)
   const int64_t P = offsets[L] < max_rows ? offsets[L] : max_rows;
   const int64_t lo = static_cast<int64_t>(m) * b;
@@ -390,6 +390,40 @@ __global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __rest
     }
     r[kXcds] = count_pos;
   }
+}
+
+__global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __restrict__ offsets, int L, int64_t b,
+                                                           int64_t max_rows, int BM, int max_tiles,
+                                                           int4* __restrict__ tiles, int32_t* __restrict__ tile_count,
+                                                           int32_t* __restrict__ runs) {
+  build_tiles(blockIdx.x, offsets, L, b, max_rows, BM, max_tiles, tiles, tile_count, runs);
+}
+
+// The first steps of a layer of int8 experts with a few tokens, neither of
+// which needs the other: workgroup 0 builds the tile list, the others quantise
+// a row each.
+__global__ __launch_bounds__(1024) void rows_and_tiles_i8_kernel(const QuantI8Args a,
+                                                                 const int32_t* __restrict__ offsets, int L,
+                                                                 int64_t max_rows, int BM, int max_tiles,
+                                                                 int4* __restrict__ tiles,
+                                                                 int32_t* __restrict__ tile_count,
+                                                                 int32_t* __restrict__ runs) {
+  if (blockIdx.x == 0)
+    build_tiles(0, offsets, L, max_rows, max_rows, BM, max_tiles, tiles, tile_count, runs);
+  else
+    i8_quantize_row<1024, true, uint16_t>(a, blockIdx.x - 1);
+}
+
+hipError_t launch_rows_and_tiles_i8(const QuantI8Args& a, int64_t rows, const int32_t* offsets, int L,
+                                    int64_t max_rows, int BM, int max_tiles, int4* tiles, int32_t* tile_count,
+                                    int32_t* runs, hipStream_t stream) {
+  if (rows <= 0 || rows >= 0x7fffffff || a.K % 8 || a.Kp != a.K || reinterpret_cast<uintptr_t>(a.src) % 16 ||
+      reinterpret_cast<uintptr_t>(a.q) % 8)
+    return hipErrorInvalidValue;
+  if (runs && static_cast<int64_t>(max_tiles) * kTileRunFrac >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  rows_and_tiles_i8_kernel<<<static_cast<unsigned>(rows + 1), 1024, 0, stream>>>(a, offsets, L, max_rows, BM,
+                                                                                 max_tiles, tiles, tile_count, runs);
+  return hipGetLastError();
 }
 
 // Dense tile list: one segment [0, rows) of expert 0, split as the routed

@@ -75,7 +75,9 @@ def reference(q, s, wq, ws, dtype):
 
 MATS = [(1, 1, 128), (1, 2048, 7168), (2, 17, 256), (15, 33, 384), (16, 64, 128), (17, 1001, 1536), (32, 130, 2048),
         (33, 257, 640), (64, 512, 1024), (100, 96, 128), (255, 300, 256), (257, 511, 384), (777, 1001, 1536),
-        (1024, 768, 2048), (513, 8, 65536)]
+        (1024, 768, 2048), (513, 8, 65536),
+        # sizes for which the product takes tiles of 64, 128, 256 and 320 rows
+        (777, 2048, 128), (2047, 2048, 256), (2050, 7168, 128), (2400, 8190, 128)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -175,6 +177,11 @@ LAYERS = [  # workload, minibatch, ring
     (synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian"), None, None),
     (synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian"), 256, 512),
     (synth.Workload("skewed", T=1100, D=384, I=128, E=24, k=6, I_shared=256, seed=8, routing="zipf"), None, None),
+    # 25, 64 and 200 rows an expert: tiles of 64, 256 and 320 rows (those above take 32 and 128)
+    (synth.Workload("rows25", T=100, D=256, I=256, E=16, k=4, I_shared=128, seed=10, routing="gaussian"), None, None),
+    (synth.Workload("rows64", T=1024, D=128, I=1280, E=128, k=8, I_shared=128, seed=11, routing="gaussian"), None,
+     None),
+    (synth.Workload("rows200", T=3200, D=128, I=1024, E=64, k=4, I_shared=128, seed=12, routing="zipf"), None, None),
     (synth.Workload("single", T=700, D=128, I=128, E=1, k=1, I_shared=128, seed=9, routing="gaussian"), None, None),
 ]
 
@@ -319,6 +326,26 @@ def test_int8_layer_with_a_scored_router_in_a_graph():
     # and the eager step is the oracle's
     want, tol = oracle(w, {**inp, "x": x.cpu()}, got["idx"].cpu().numpy(), got["gate"].cpu().numpy())
     assert np.all(np.abs(got["out32"].cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 40])
+def test_int8_layer_with_an_expert_named_twice(T):
+    # routes are the caller's: a token may name an expert more than once, and then counts it each time
+    dev = need_gpu()
+    w = synth.Workload("twice", T=T, D=256, I=128, E=4, k=4, I_shared=128, seed=6, routing="gaussian")
+    say("int8 twice", T)
+    inp = synth.make_inputs(w)
+    idx = torch.zeros((T, 4), dtype=torch.int32)
+    idx[:, 2:] = 3
+    gate = torch.rand((T, 4), generator=torch.Generator().manual_seed(T))
+    m = make(w, dev)
+    x = inp["x"].to(dev)
+    _, out32 = m.forward(quantised(inp, dev), x, x, gate.to(dev), m.schedule(idx.to(dev)))
+    torch.cuda.synchronize()
+    assert m.device_error() == 0
+    both = torch.stack([gate[:, :2].sum(1), gate[:, 2:].sum(1)], dim=1).numpy()
+    want, tol = oracle(w, inp, np.tile(np.array([[0, 3]]), (T, 1)), both)
+    assert np.all(np.abs(out32.cpu().numpy() - want) <= tol)
 
 
 def test_int8_layer_without_tokens():

@@ -58,6 +58,13 @@ CASES = [  # T, E, k, bias, router
     (77, 513, 9, False, dict(score="sigmoid", groups=27, kept_groups=13)),
     (50, 64, 8, True, dict(score="softmax", groups=64, kept_groups=8)),
     (128, 100, 12, False, dict(score="sigmoid", groups=2, kept_groups=1, group_score="max")),
+    # enough tokens that several share a wave
+    (2101, 256, 8, True, dict(score="sigmoid", groups=8, kept_groups=4, scale=2.5)),
+    (2060, 100, 12, True, dict(score="softmax", groups=25, kept_groups=7)),
+    (2049, 384, 6, False, dict(score="softmax", groups=12, kept_groups=5, group_score="max", renorm=False)),
+    (2051, 500, 16, True, dict(score="sigmoid", groups=20, kept_groups=3)),
+    (2050, 128, 9, False, dict(score="sigmoid", groups=4, kept_groups=1)),
+    (2053, 201, 3, True, dict(score="softmax", renorm=False)),
 ]
 
 
