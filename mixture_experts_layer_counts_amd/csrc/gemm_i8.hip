@@ -16,10 +16,17 @@
 // not matter as long as A and B agree, and integer sums do not depend on their
 // order.  A sum of 65536 products stays below 2^30.
 //
-// The scales are applied once, to the int32 sums: a row's from LDS, a column's
-// from a register.  Epilogues, staged through LDS so that rows leave in 16-byte
-// stores: SwiGLU in fp32 (h is quantised when its whole row is known), bf16
-// scattered to the rows' routes, and fp32 in 128-row bands.
+// The scales are applied once, to the int32 sums.  Epilogues: SwiGLU in fp32 (h
+// is quantised when its whole row is known), bf16 scattered to the rows'
+// routes, and fp32.
+//
+// A workgroup's next item begins under its epilogue: the first loads are issued
+// before the stores, so they need not wait for them, and the stores drain under
+// the next K loop's first stages (the waits count them).  That took the down
+// product of the 7168 x 2048 layer at 8192 tokens from 1.36 to 1.30 ms, an 8192
+// x 7168 x 2048 product from 140 to 134 us, and the 2048 x 768 layer of 128
+// experts at 8192 tokens from 737 to 694 us; the one workgroup on a CU
+// otherwise wrote 160 KB with no load in flight.
 
 #include <algorithm>
 #include <atomic>
@@ -42,10 +49,6 @@ constexpr int kRB = 128;  // bytes (K elements) of one stage row
 // rows n - 1 stages ahead.
 constexpr int ring_bytes(int bm, int brows, int nsa, int nsb) { return (nsa * bm + nsb * brows) * kRB; }
 
-struct I8Src {
-  __amdgpu_buffer_rsrc_t a, b0, b1;
-};
-
 // Row of the tile held by 32-row block fm of a wave in row group wm: blocks
 // are dealt to the row groups in turn, so a partly filled tile keeps every
 // wave busy.
@@ -54,45 +57,72 @@ __device__ __forceinline__ int tile_row(int wm, int fm) {
   return (fm * WM + wm) * 32;
 }
 
+// One item's operands as this lane fetches them.
+template <int AI, int BI>
+struct I8Stream {
+  __amdgpu_buffer_rsrc_t a, b0, b1;
+  uint32_t a_off[AI], b_off[BI];  // byte offsets of the 16-byte chunks of stage 0
+  int b_stage;                    // bytes from one stage of a weight row to the next
+  int nk, a_rows;
+};
+
+// The loads of stage kt into its ring slots (lane l's 16 bytes land at base +
+// 16 l).  A stage past the last (in the prologue of a short K) loads the last
+// one again, into a free slot, so that the prologue issues the same number of
+// loads; row groups past the tile reload the first one for the same reason.
+template <int BM, int NSA, int AI, int BI>
+__device__ __forceinline__ void issue_a(char* smem, const I8Stream<AI, BI>& s, int wave, int kt) {
+  constexpr int ROWS_PER_LD = 1024 / kRB;
+  const int ko = (kt < s.nk ? kt : s.nk - 1) * kRB;
+  char* sa = smem + (kt % NSA) * (BM * kRB);
+#pragma unroll
+  for (int j = 0; j < AI; ++j)
+    dma16(s.a, sa + (wave * AI + j) * 1024, (wave * AI + j) * ROWS_PER_LD < s.a_rows ? s.a_off[j] : s.a_off[0], ko);
+}
+template <int BM, int BN, int NB, int NSA, int NSB, int AI, int BI>
+__device__ __forceinline__ void issue_b(char* smem, const I8Stream<AI, BI>& s, int wave, int kt) {
+  constexpr int ROWS_PER_LD = 1024 / kRB;
+  const int ko = (kt < s.nk ? kt : s.nk - 1) * s.b_stage;
+  char* sb = smem + NSA * BM * kRB + (kt % NSB) * (NB * BN * kRB);
+#pragma unroll
+  for (int j = 0; j < BI; ++j) {
+    const int g = wave * BI + j;
+    dma16((NB == 2 && g * ROWS_PER_LD >= BN) ? s.b1 : s.b0, sb + g * 1024, s.b_off[j], ko);
+  }
+}
+
+// Wait until at most N vector memory operations are outstanding, plus what a
+// previous epilogue's `stores` (issued after every load waited for) may be:
+// rounded down to one of a few counts.
+template <int N, int FULL>
+__device__ __forceinline__ void wait_behind(int stores) {
+  constexpr int kFull = N + FULL < 63 ? N + FULL : 63, kHalf = N + FULL / 2 < 63 ? N + FULL / 2 : 63;
+  if (stores >= FULL)
+    asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(kFull, 0)) : "memory");
+  else if (stores >= FULL / 2)
+    asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(kHalf, 0)) : "memory");
+  else
+    asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(N, 0)) : "memory");
+}
+
 // The K loop of one workgroup, the bf16 kernels' protocol: a slot is refilled
 // right after the barrier that ends its stage's reads, the fragments of the
 // next 32-wide sub-step are read under the current MFMAs, and one barrier per
-// stage waits for the next stage's rows.  FML of the wave's FM row blocks hold
-// tile rows.
-template <int BM, int BN, int WM, int WN, int NSA, int NSB, int NB, int FML, int FM, int FN, int AI, int BI>
-__device__ __forceinline__ void k_loop_i8(char* smem, const I8Src& src, const uint32_t (&a_off)[AI],
-                                          const uint32_t (&b_off)[BI], int b_stage, int nk, int a_rows, int tid,
+// stage waits for the next stage's rows.  The first stages' loads are in flight
+// on entry, behind them `stores` stores of the previous item; the ring is free
+// on return.  FML of the wave's FM row blocks hold tile rows.
+template <int BM, int BN, int WM, int WN, int NSA, int NSB, int NB, int FML, int FM, int FN, int STORES, int AI, int BI>
+__device__ __forceinline__ void k_loop_i8(char* smem, const I8Stream<AI, BI>& src, int stores, int wave, int lane,
                                           int wm, int wn, i32x16_t (&acc)[NB][FM][FN]) {
   constexpr int BROWS = NB * BN, WTN = BN / WN;
   static_assert(NSA >= 2 && NSB >= NSA, "ring depths");
   constexpr int ASLOT = BM * kRB, BSLOT = BROWS * kRB;
   constexpr int KS = 4;  // 32-wide sub-steps per stage
-  constexpr int ROWS_PER_LD = 1024 / kRB;
-  static_assert(AI * ROWS_PER_LD * WM * WN == BM && BI * ROWS_PER_LD * WM * WN == BROWS, "loads per wave per stage");
   char* const sa0 = smem;
   char* const sb0 = smem + NSA * ASLOT;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int frag_row = lane & 31, frag_c = lane >> 5;
+  const int nk = src.nk;
 
-  // a stage past the last (in the prologue of a short K) loads the last one
-  // again, into a free slot, so that the prologue issues the same number of
-  // loads; row groups past the tile reload the first one for the same reason
-  auto issue_a = [&](int kt) __attribute__((always_inline)) {
-    const int ko = (kt < nk ? kt : nk - 1) * kRB;
-    char* sa = sa0 + (kt % NSA) * ASLOT;
-#pragma unroll
-    for (int j = 0; j < AI; ++j)
-      dma16(src.a, sa + (wave * AI + j) * 1024, (wave * AI + j) * ROWS_PER_LD < a_rows ? a_off[j] : a_off[0], ko);
-  };
-  auto issue_b = [&](int kt) __attribute__((always_inline)) {
-    const int ko = (kt < nk ? kt : nk - 1) * b_stage;
-    char* sb = sb0 + (kt % NSB) * BSLOT;
-#pragma unroll
-    for (int j = 0; j < BI; ++j) {
-      const int g = wave * BI + j;
-      dma16((NB == 2 && g * ROWS_PER_LD >= BN) ? src.b1 : src.b0, sb + g * 1024, b_off[j], ko);
-    }
-  };
   using frag_a_t = i32x4_t[FML > 0 ? FML : 1];
   using frag_b_t = i32x4_t[NB][FN];
   auto read_frags = [&](int kt, int step, frag_a_t& af, frag_b_t& bfr) __attribute__((always_inline)) {
@@ -137,12 +167,8 @@ __device__ __forceinline__ void k_loop_i8(char* smem, const I8Src& src, const ui
   constexpr int VM_FIRST = VM_AFTER + (NSA - 1) * (AI + BI);
   constexpr int VM_STAGE = VM_AFTER + (NSA - 2) * (AI + BI);
   static_assert(VM_FIRST < 64, "vmcnt range");
-#pragma unroll
-  for (int v = -NSB; v < 0; ++v) {
-    if (v + NSA >= 0) issue_a(v + NSA);
-    issue_b(v + NSB);
-  }
-  asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(VM_FIRST, 15)) : "memory");  // A(0), B(0) landed
+  // A(0), B(0) and the tables in LDS have landed
+  wait_behind<VM_FIRST, STORES>(stores);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   frag_a_t af[2];
@@ -159,18 +185,23 @@ __device__ __forceinline__ void k_loop_i8(char* smem, const I8Src& src, const ui
       }
     }
     // A(kt+1) and B(kt+1) have landed and this wave's reads of stage kt are
-    // done, before any wave refills a slot (in the tail by draining the counter)
-    if constexpr (kLoads)
-      asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(VM_STAGE, 0)) : "memory");
-    else
+    // done, before any wave refills a slot (in the tail by draining the counter;
+    // the stages of the prologue landed before the stores behind them)
+    if constexpr (kLoads) {
+      if (kt == 0)
+        wait_behind<VM_STAGE, STORES>(stores);
+      else
+        asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(VM_STAGE, 0)) : "memory");
+    } else {
       asm volatile("s_waitcnt %0" ::"n"(waitcnt_imm(0, 0)) : "memory");
+    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if constexpr (kLoads) {
-      issue_a(kt + NSA);
-      issue_b(kt + NSB);
+      issue_a<BM, NSA>(smem, src, wave, kt + NSA);
+      issue_b<BM, BN, NB, NSA, NSB>(smem, src, wave, kt + NSB);
     } else if constexpr (NSB > NSA) {
-      if (kt + NSA < nk) issue_a(kt + NSA);  // a stage still to come (uniform branch)
+      if (kt + NSA < nk) issue_a<BM, NSA>(smem, src, wave, kt + NSA);  // a stage still to come (uniform branch)
     }
     if constexpr (FML > 0) {
       // past the last stage this reads a slot whose data is not used
@@ -182,14 +213,24 @@ __device__ __forceinline__ void k_loop_i8(char* smem, const I8Src& src, const ui
   int kt = 0;
   for (; kt < nk - NSB; ++kt) step(kt, std::true_type{});
   for (; kt < nk; ++kt) step(kt, std::false_type{});
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still target LDS when the workgroup ends
 }
 
-// One work item (row tile, N block): its K loop and its epilogue.  The
-// workgroup's LDS is free on entry and on return.
+// What the epilogue needs of an item beside its sums: the scales of its rows
+// and columns and the output rows, kept in LDS past the rings, twice (the next
+// item's are filled in before this one's epilogue).
+template <int BM, int BROWS>
+struct I8Tables {
+  float row_scale[BM];
+  int row_out[BM];  // output row, or -1
+  float col_scale[BROWS];
+};
+
+// Resident workgroups walk items.  An item's first loads are issued before the
+// previous item's epilogue, which needs nothing of the rings: fp32 rows go
+// straight from the registers (32 lanes hold 128 consecutive bytes), bf16 rows
+// through 8-row pieces that each wave stages for itself.
 template <int BM, int BN, int WM, int WN, int NSA, int NSB, int EPI>
-__device__ __forceinline__ void gemm_i8_item(const I8GemmArgs& args, int w, int n_blocks, int dense_tiles, char* smem,
-                                             int wave0) {
+__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs args, int dense_tiles) {
   constexpr int NB = (EPI == kEpiSwiGLU) ? 2 : 1;
   constexpr int BROWS = NB * BN;
   constexpr int WTN = BN / WN, NW = WM * WN;
@@ -197,202 +238,23 @@ __device__ __forceinline__ void gemm_i8_item(const I8GemmArgs& args, int w, int 
   constexpr int ROWS_PER_LD = 1024 / kRB;
   constexpr int AI = BM / (NW * ROWS_PER_LD), BI = BROWS / (NW * ROWS_PER_LD);
   static_assert(FM >= 1 && FM <= 5 && FN >= 1, "tile shape");
+  static_assert(AI * ROWS_PER_LD * NW == BM && BI * ROWS_PER_LD * NW == BROWS, "loads per wave per stage");
+  static_assert(BM <= 64 * NW && BROWS <= 64 * NW, "one table entry per thread");
+  // bf16 pieces: 8 rows of the wave's WTN columns, padded against bank conflicts
+  constexpr int PS = WTN * 2 + 16, PIECE = EPI == kEpiBF16 ? 8 * PS : 0;
+  constexpr int CPR = WTN * 2 / 16;                // 16-byte chunks per bf16 row
+  constexpr int PIECE_STORES = EPI == kEpiBF16 ? (8 * CPR + 63) / 64 : 4 * FN;  // stores per 8-row piece
+  constexpr int STORES = FM * 4 * PIECE_STORES;    // of a whole tile
+  constexpr int RING = ring_bytes(BM, BROWS, NSA, NSB);
+  using Tables = I8Tables<BM, BROWS>;
+  __shared__ __attribute__((aligned(1024))) char smem[RING + 2 * sizeof(Tables) + NW * PIECE];
+  Tables* const tables = reinterpret_cast<Tables*>(smem + RING);
 
-  constexpr bool kItemLoop = EPI == kEpiBF16;  // resident workgroups walk several items
-  const int tid = kItemLoop ? item_thread_index(wave0) : static_cast<int>(threadIdx.x);
-  const int lane = tid & (kWave - 1), wave = kItemLoop ? wave0 : __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave / WN, wn = wave % WN;
-
-  int e = 0, nb, lt, nrows;
-  int64_t p0;
-  if (args.tiles) {
-    const int4 g = load_uniform(args.tiles + w / n_blocks);
-    const int nt = g.x >> 10, first = g.w;
-    grouped_item(w - first * n_blocks, nt, n_blocks, nb, lt);
-    const int4 t = load_uniform(args.tiles + first + lt);
-    e = t.x & 1023;
-    p0 = t.y;
-    nrows = t.z;
-  } else {  // rows 0 .. dense_rows - 1 in tiles of equal height, a multiple of 32
-    grouped_item(w, dense_tiles, n_blocks, nb, lt);
-    const int h = ((args.dense_rows + dense_tiles - 1) / dense_tiles + 31) / 32 * 32;
-    p0 = static_cast<int64_t>(lt) * h;
-    nrows = args.dense_rows - static_cast<int>(p0) < h ? args.dense_rows - static_cast<int>(p0) : h;
-    if (nrows <= 0) return;  // rounding the height up may leave the last tiles empty
-  }
-  const int n0 = nb * BN;
-  const int K = args.K;
-
-  // the scale of tile row tid, kept through the K loop
-  static_assert(BM <= 64 * NW, "one row scale per thread");
-  const float my_scale = tid < BM ? args.As[i8_a_row(args, p0 + (tid < nrows ? tid : nrows - 1))] : 0.f;
-  // ---- byte offsets of the 16-byte chunks this lane fetches ----
-  constexpr int CH = kRB / 16;
-  uint32_t a_off[AI];
-#pragma unroll
-  for (int j = 0; j < AI; ++j) {
-    const int row = ROWS_PER_LD * (wave * AI + j) + lane / CH;
-    const int c = (lane % CH) ^ ((row / (256 / kRB)) & (CH - 1));
-    a_off[j] = static_cast<uint32_t>(i8_a_row(args, p0 + (row < nrows ? row : nrows - 1)) * K + c * 16);
-  }
-  const bool b_tiled = args.b_plane > 0;
-  const int b_stage = b_tiled ? static_cast<int>(args.b_plane * kRB) : kRB;
-  uint32_t b_off[BI];
-#pragma unroll
-  for (int j = 0; j < BI; ++j) {
-    const int row = ROWS_PER_LD * (wave * BI + j) + lane / CH;
-    const int c = (lane % CH) ^ ((row / (256 / kRB)) & (CH - 1));
-    const int half = row / BN;
-    int n = n0 + (row - half * BN);
-    n = n < args.N ? n : args.N - 1;
-    b_off[j] = static_cast<uint32_t>(b_tiled ? n * kRB + c * 16 : n * K + c * 16);
-  }
-  constexpr int kRsrcWord3 = 0x00020000;
-  I8Src src;
-  src.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(args.A), 0, static_cast<int>(args.a_rows * K),
-                                            kRsrcWord3);
-  const int b_bytes = args.N * K;
-  src.b0 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(args.B0 + static_cast<int64_t>(e) * b_bytes), 0,
-                                             b_bytes, kRsrcWord3);
-  if constexpr (NB == 2)
-    src.b1 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(args.B1 + static_cast<int64_t>(e) * b_bytes), 0,
-                                               b_bytes, kRsrcWord3);
-  else
-    src.b1 = src.b0;
-  i32x16_t acc[NB][FM][FN];
-#pragma unroll
-  for (int h = 0; h < NB; ++h)
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm)
-#pragma unroll
-      for (int fn = 0; fn < FN; ++fn) acc[h][fm][fn] = i32x16_t{};
-
-  // 32-row blocks of this wave that hold tile rows (wave-uniform)
-  int fm_live = ((nrows + 31) / 32 - wm + WM - 1) / WM;
-  fm_live = fm_live < 0 ? 0 : (fm_live > FM ? FM : fm_live);
-  const int nk = K / kRB;
-  switch (fm_live) {
-#define MOE_CASE(n)                                                                                                \
-  case n:                                                                                                          \
-    if constexpr (n <= FM)                                                                                         \
-      k_loop_i8<BM, BN, WM, WN, NSA, NSB, NB, n, FM, FN, AI, BI>(smem, src, a_off, b_off, b_stage, nk, nrows, tid,   \
-                                                                 wm, wn, acc);                                     \
-    break;
-    MOE_CASE(0)
-    MOE_CASE(1)
-    MOE_CASE(2)
-    MOE_CASE(3)
-    MOE_CASE(4)
-    MOE_CASE(5)
-#undef MOE_CASE
-    default:
-      break;
-  }
-
-  // ---- epilogue: scales, then rows leave through LDS in 16-byte pieces ----
-  // The MFMA layout gives lane l column l % 32 of rows 8*(r/4) + 4*(l/32) +
-  // r%4 of each 32 x 32 block.  The tile (or a band of it) is written to LDS
-  // row by row, then copied out by all threads.
-  constexpr int ESZ = EPI == kEpiBF16 ? 2 : 4;
-  constexpr int CS = BN * ESZ + 16;                  // LDS row stride (padded against bank conflicts)
-  constexpr int SCALE_AT = ring_bytes(BM, BROWS, NSA, NSB) - BM * 4;  // row scales, past the staged band
-  constexpr int FMP_FIT = SCALE_AT / CS / (WM * 32);
-  constexpr int FMP = FMP_FIT < FM ? FMP_FIT : FM;   // 32-row blocks per row group and band
-  constexpr int NBANDS = (FM + FMP - 1) / FMP;
-  static_assert(FMP >= 1, "epilogue bands");
-  constexpr int BAND = FMP * WM * 32;
-  constexpr int CPR = BN * ESZ / 16, EPC = 16 / ESZ;  // chunks per row, elements per chunk
-  // In pass `it` of a band, wave w stores rows it * RSTEP + w * RPI + lane /
-  // CPR.  Each row's output row is found once, before any store, and passed
-  // on by a cross-lane read (a table load among the stores waits for them).
-  constexpr int RPI = 64 / CPR, RSTEP = RPI * NW;
-  static_assert(64 % CPR == 0 && BAND % RSTEP == 0, "copy-out mapping");
-  int row_entry = -1;
-  {
-    const int r = (lane / RPI) * RSTEP + wave * RPI + lane % RPI;
-    if (r < nrows) row_entry = static_cast<int>(i8_c_row(args, p0 + r));
-  }
-  float sb[NB][FN];
-#pragma unroll
-  for (int h = 0; h < NB; ++h)
-#pragma unroll
-    for (int fn = 0; fn < FN; ++fn) {
-      int n = n0 + wn * WTN + fn * 32 + (lane & 31);
-      n = n < args.N ? n : args.N - 1;
-      sb[h][fn] = (h ? args.Bs1 : args.Bs0)[static_cast<int64_t>(e) * args.N + n];
-    }
-  __syncthreads();  // every wave is done with the K loop's LDS
-  float* row_s = reinterpret_cast<float*>(smem + SCALE_AT);
-  if (tid < BM) row_s[tid] = my_scale;
-  __syncthreads();
-  const bool whole = args.N % EPC == 0 && args.ldc % EPC == 0;
-#pragma unroll
-  for (int band = 0; band < NBANDS; ++band) {
-    if (band > 0 && band * BAND >= nrows) break;  // workgroup-uniform
-#pragma unroll
-    for (int fm = band * FMP; fm < (band + 1) * FMP && fm < FM; ++fm) {
-      if (fm >= fm_live) continue;  // wave-uniform
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const int row0 = tile_row<WM>(wm, fm) + r4 * 8 + (lane >> 5) * 4;
-        const f32x4_t s = *reinterpret_cast<const f32x4_t*>(row_s + row0);
-        char* to = smem + (row0 - band * BAND) * CS;
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn) {
-          const int col_l = wn * WTN + fn * 32 + (lane & 31);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = static_cast<float>(acc[0][fm][fn][r4 * 4 + i]) * s[i] * sb[0][fn];
-            if constexpr (EPI == kEpiSwiGLU)
-              v = silu_mul(v, static_cast<float>(acc[NB - 1][fm][fn][r4 * 4 + i]) * s[i] * sb[NB - 1][fn]);
-            if constexpr (ESZ == 4)
-              *reinterpret_cast<float*>(to + i * CS + col_l * 4) = v;
-            else
-              *reinterpret_cast<uint16_t*>(to + i * CS + col_l * 2) = f32_to_bf16(v);
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const int band_rows = min(BAND, nrows - band * BAND);
-    for (int it = 0; it * RSTEP < band_rows; ++it) {
-      const int row_b = it * RSTEP + wave * RPI + lane / CPR, ch = lane % CPR;
-      const int crow = __shfl(row_entry, (band * BAND / RSTEP + it) * RPI + lane / CPR);
-      const int col = n0 + ch * EPC;
-      if (row_b >= band_rows || col >= args.N || crow < 0) continue;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(smem + row_b * CS + ch * 16);
-      char* dst = static_cast<char*>(args.C) + (static_cast<int64_t>(crow) * args.ldc + col) * ESZ;
-      if (whole) {
-        // bf16 rows are next read long after they leave the caches
-        if constexpr (ESZ == 2)
-          __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst));
-        else
-          *reinterpret_cast<u32x4_t*>(dst) = v;
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-          if (col + i >= args.N) continue;
-          if constexpr (ESZ == 4)
-            reinterpret_cast<uint32_t*>(dst)[i] = v[i];
-          else
-            reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i % 2)));
-        }
-      }
-    }
-    if (band + 1 < NBANDS) __syncthreads();  // the next band reuses the LDS
-  }
-}
-
-// Work items are cut into 8 contiguous runs, one per XCD, as in the bf16 and
-// MXFP8 kernels: workgroup b takes item b / 8 of the run of XCD b mod 8, and
-// the bf16 epilogue's resident workgroups walk their run side by side, so that
-// one item's output stores drain under the next one's first loads.
-template <int BM, int BN, int WM, int WN, int NSA, int NSB, int EPI>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs args, int dense_tiles) {
-  constexpr int NB = (EPI == kEpiSwiGLU) ? 2 : 1;
-  __shared__ __attribute__((aligned(1024))) char smem[ring_bytes(BM, NB * BN, NSA, NSB)];
   const int n_blocks = (args.N + BN - 1) / BN;
   const int xcd = static_cast<int>(blockIdx.x) % kXcds;
+  // work items are cut into 8 contiguous runs, one per XCD, as in the bf16 and
+  // MXFP8 kernels; workgroup b walks items b / 8, b / 8 + G, ... of the run of
+  // XCD b mod 8 (G workgroups per XCD), so an XCD's workgroups move side by side
   int run0, len;
   if (args.tiles) {  // positions in 1/kTileRunFrac of a tile
     run0 = static_cast<int>(static_cast<int64_t>(__builtin_amdgcn_readfirstlane(args.tile_runs[xcd])) * n_blocks /
@@ -405,18 +267,200 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
     run0 = xcd * chunk;
     len = W - run0 < chunk ? W - run0 : chunk;
   }
-  const int first = static_cast<int>(blockIdx.x) / kXcds;
   const int per_xcd = static_cast<int>(gridDim.x) / kXcds;  // the grid is a multiple of kXcds
-  const int wave0 = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
-  if constexpr (EPI != kEpiBF16) {
-    if (first < len) gemm_i8_item<BM, BN, WM, WN, NSA, NSB, EPI>(args, run0 + first, n_blocks, dense_tiles, smem, wave0);
-  } else {
-    for (int local = first; local < len; local += per_xcd) {
-      if (local > first) __syncthreads();  // the previous item's copy-out has read the LDS
-      gemm_i8_item<BM, BN, WM, WN, NSA, NSB, EPI>(args, __builtin_amdgcn_readfirstlane(run0 + local), n_blocks, dense_tiles,
-                                        smem, wave0);
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  int local = static_cast<int>(blockIdx.x) / kXcds;
+  if (local >= len) return;
+
+  I8Stream<AI, BI> src;
+  src.nk = args.K / kRB;
+  src.b_stage = args.b_plane ? static_cast<int>(args.b_plane * kRB) : kRB;
+  constexpr int kRsrcWord3 = 0x00020000;
+  src.a = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(args.A), 0, static_cast<int>(args.a_rows * args.K),
+                                            kRsrcWord3);
+
+  // Item `w`: its place, its tables into buffer `buf`, its addresses, and the
+  // loads of its first stages.
+  int nrows, n0;
+  auto begin = [&](int w, int buf) __attribute__((always_inline)) {
+    const int tid = item_thread_index(wave), lane = tid & (kWave - 1);
+    const int K = args.K;
+    int e = 0, nb, lt;
+    int64_t p0;
+    if (args.tiles) {
+      const int4 g = load_uniform(args.tiles + w / n_blocks);
+      const int nt = g.x >> 10, first = g.w;
+      grouped_item(w - first * n_blocks, nt, n_blocks, nb, lt);
+      const int4 t = load_uniform(args.tiles + first + lt);
+      e = t.x & 1023;
+      p0 = t.y;
+      nrows = t.z;
+    } else {  // rows 0 .. dense_rows - 1 in tiles of equal height, a multiple of 32
+      grouped_item(w, dense_tiles, n_blocks, nb, lt);
+      const int h = ((args.dense_rows + dense_tiles - 1) / dense_tiles + 31) / 32 * 32;
+      p0 = static_cast<int64_t>(lt) * h;
+      const int left = args.dense_rows - static_cast<int>(p0);
+      nrows = left < h ? left : h;  // at least 1: (dense_tiles - 1) h < dense_rows
     }
+    n0 = nb * BN;
+    // ---- byte offsets of the 16-byte chunks this lane fetches; rows past the
+    // tile are clamped onto its last row and rows past N onto row N - 1: their
+    // products only reach outputs that are dropped ----
+    constexpr int CH = kRB / 16;
+#pragma unroll
+    for (int j = 0; j < AI; ++j) {
+      const int row = ROWS_PER_LD * (wave * AI + j) + lane / CH;
+      const int c = (lane % CH) ^ ((row / (256 / kRB)) & (CH - 1));
+      src.a_off[j] = static_cast<uint32_t>(i8_a_row(args, p0 + (row < nrows ? row : nrows - 1)) * K + c * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < BI; ++j) {
+      const int row = ROWS_PER_LD * (wave * BI + j) + lane / CH;
+      const int c = (lane % CH) ^ ((row / (256 / kRB)) & (CH - 1));
+      const int half = row / BN;
+      int n = n0 + (row - half * BN);
+      n = n < args.N ? n : args.N - 1;
+      src.b_off[j] = static_cast<uint32_t>(args.b_plane ? n * kRB + c * 16 : n * K + c * 16);
+    }
+    src.a_rows = nrows;
+    const int b_bytes = args.N * K;
+    src.b0 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(args.B0 + static_cast<int64_t>(e) * b_bytes), 0,
+                                               b_bytes, kRsrcWord3);
+    src.b1 = NB == 2 ? __builtin_amdgcn_make_buffer_rsrc(
+                           const_cast<int8_t*>(args.B1 + static_cast<int64_t>(e) * b_bytes), 0, b_bytes, kRsrcWord3)
+                     : src.b0;
+    // the tables: read before the stage loads, so that these stay in flight
+    float rs = 0.f, cs = 0.f;
+    int ro = -1;
+    if (tid < BM) {
+      rs = args.As[i8_a_row(args, p0 + (tid < nrows ? tid : nrows - 1))];
+      if (tid < nrows) ro = static_cast<int>(i8_c_row(args, p0 + tid));
+    }
+    if (tid < BROWS) {
+      const int half = tid / BN;
+      int n = n0 + tid - half * BN;
+      n = n < args.N ? n : args.N - 1;
+      cs = (half ? args.Bs1 : args.Bs0)[static_cast<int64_t>(e) * args.N + n];
+    }
+#pragma unroll
+    for (int v = -NSB; v < 0; ++v) {
+      if (v + NSA >= 0) issue_a<BM, NSA>(smem, src, wave, v + NSA);
+      issue_b<BM, BN, NB, NSA, NSB>(smem, src, wave, v + NSB);
+    }
+    if (tid < BM) {
+      tables[buf].row_scale[tid] = rs;
+      tables[buf].row_out[tid] = ro;
+    }
+    if (tid < BROWS) tables[buf].col_scale[tid] = cs;
+  };
+
+  begin(run0 + local, 0);
+  int stores = 0;  // of the last epilogue, at least
+  for (int turn = 0;; ++turn) {
+    // 32-row blocks of this wave that hold tile rows (wave-uniform)
+    int fm_live = ((nrows + 31) / 32 - wm + WM - 1) / WM;
+    fm_live = fm_live < 0 ? 0 : (fm_live > FM ? FM : fm_live);
+    i32x16_t acc[NB][FM][FN];
+#pragma unroll
+    for (int h = 0; h < NB; ++h)
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) acc[h][fm][fn] = i32x16_t{};
+    {
+      const int lane = item_thread_index(wave) & (kWave - 1);
+      switch (fm_live) {
+#define MOE_CASE(n)                                                                                                \
+  case n:                                                                                                          \
+    if constexpr (n <= FM)                                                                                         \
+      k_loop_i8<BM, BN, WM, WN, NSA, NSB, NB, n, FM, FN, STORES, AI, BI>(smem, src, stores, wave, lane, wm, wn, acc); \
+    break;
+        MOE_CASE(0)
+        MOE_CASE(1)
+        MOE_CASE(2)
+        MOE_CASE(3)
+        MOE_CASE(4)
+        MOE_CASE(5)
+#undef MOE_CASE
+        default:
+          break;
+      }
+    }
+    const int col0 = n0 + wn * WTN, buf = turn & 1, rows = nrows;
+    local += per_xcd;
+    const bool more = local < len;
+    if (more) begin(__builtin_amdgcn_readfirstlane(run0 + local), buf ^ 1);
+
+    // ---- epilogue.  The MFMA layout gives lane l column l % 32 of rows 8*(r/4)
+    // + 4*(l/32) + r%4 of each 32 x 32 block. ----
+    const int lane = item_thread_index(wave) & (kWave - 1);
+    const Tables& t = tables[buf];
+    const bool whole = EPI != kEpiBF16 || (args.N % 8 == 0 && args.ldc % 8 == 0);
+    stores = 0;
+    float sb[NB][FN];
+#pragma unroll
+    for (int h = 0; h < NB; ++h)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) sb[h][fn] = t.col_scale[h * BN + wn * WTN + fn * 32 + (lane & 31)];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      if (fm >= fm_live) continue;  // wave-uniform
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const int row0 = tile_row<WM>(wm, fm) + r4 * 8;
+        if (row0 >= rows) continue;  // wave-uniform
+        // every store of the piece has a lane to issue it for: its first row is in the tile
+        if (whole && col0 + WTN <= args.N) stores += PIECE_STORES;
+        const f32x4_t s = *reinterpret_cast<const f32x4_t*>(&t.row_scale[row0 + (lane >> 5) * 4]);
+        if constexpr (EPI == kEpiBF16) {
+          char* piece = smem + RING + 2 * sizeof(Tables) + wave * PIECE;
+#pragma unroll
+          for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint16_t*>(piece + ((lane >> 5) * 4 + i) * PS + (fn * 32 + (lane & 31)) * 2) =
+                  f32_to_bf16(static_cast<float>(acc[0][fm][fn][r4 * 4 + i]) * s[i] * sb[0][fn]);
+          // the wave's LDS instructions run in order; the compiler must keep them so
+          asm volatile("" ::: "memory");
+#pragma unroll
+          for (int it = 0; it < PIECE_STORES; ++it) {
+            const int q = it * 64 + lane, row = q / CPR % 8, ch = q % CPR;
+            const int col = col0 + ch * 8, out = t.row_out[row0 + row];
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(piece + row * PS + ch * 16);
+            if (q >= 8 * CPR || out < 0 || col >= args.N) continue;
+            uint16_t* c = static_cast<uint16_t*>(args.C) + static_cast<int64_t>(out) * args.ldc + col;
+            if (whole) {
+              // next read long after they leave the caches
+              __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(c));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (col + i < args.N) c[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i % 2)));
+            }
+          }
+          asm volatile("" ::: "memory");
+        } else {
+          const int4 out = *reinterpret_cast<const int4*>(&t.row_out[row0 + (lane >> 5) * 4]);
+          const int outs[4] = {out.x, out.y, out.z, out.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (outs[i] < 0) continue;
+            float* c = static_cast<float*>(args.C) + static_cast<int64_t>(outs[i]) * args.ldc + col0 + (lane & 31);
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn) {
+              float v = static_cast<float>(acc[0][fm][fn][r4 * 4 + i]) * s[i] * sb[0][fn];
+              if constexpr (EPI == kEpiSwiGLU)
+                v = silu_mul(v, static_cast<float>(acc[NB - 1][fm][fn][r4 * 4 + i]) * s[i] * sb[NB - 1][fn]);
+              if (col0 + fn * 32 + (lane & 31) < args.N) c[fn * 32] = v;
+            }
+          }
+        }
+      }
+    }
+    if (!more) break;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still target LDS when the workgroup ends
 }
 
 template <int BM, int BN, int WM, int WN, int NSA, int NSB, int EPI>
@@ -427,26 +471,23 @@ hipError_t run_i8(const I8GemmArgs& a, hipStream_t stream) {
   if (work <= 0) return hipSuccess;
   if (work > 0x7ffffff0) return hipErrorInvalidValue;
   auto kernel = gemm_i8_kernel<BM, BN, WM, WN, NSA, NSB, EPI>;
-  // with room for balanced runs of up to tile_run_cap tiles on every XCD
-  int64_t cap = a.tiles ? int64_t(kXcds) * tile_run_cap(a.max_tiles) * n_blocks : work;
-  if (EPI == kEpiBF16) {
-    static std::atomic<int64_t> resident_cache{0};
-    int64_t resident = resident_cache.load(std::memory_order_relaxed);
-    if (resident <= 0) {
-      resident = resident_workgroups(reinterpret_cast<const void*>(kernel), 64 * WM * WN);
-      if (resident <= 0) return hipErrorInvalidValue;
-      resident_cache.store(resident, std::memory_order_relaxed);
-    }
-    cap = std::min(work, resident);
+  static std::atomic<int64_t> resident_cache{0};
+  int64_t resident = resident_cache.load(std::memory_order_relaxed);
+  if (resident <= 0) {
+    resident = resident_workgroups(reinterpret_cast<const void*>(kernel), 64 * WM * WN);
+    if (resident <= 0) return hipErrorInvalidValue;
+    resident_cache.store(resident, std::memory_order_relaxed);
   }
+  const int64_t cap = std::min(work, resident);
   const int64_t grid = (cap + kXcds - 1) / kXcds * kXcds;
   kernel<<<static_cast<unsigned>(grid), 64 * WM * WN, 0, stream>>>(a, static_cast<int>(dense_tiles));
   return hipGetLastError();
 }
 
-// 320- and 256-row tiles: 8 waves, two per SIMD, 64 x 128 or 160 x 64 outputs
-// a wave.  128- and 64-row tiles: fewer outputs a workgroup, two workgroups or
-// more per CU.
+// 192- to 320-row tiles: 8 waves, two per SIMD, one workgroup on a CU; three
+// slots of weight rows where LDS holds them beside the tables (256-row tiles
+// lose 4% of a routed layer with two).  128- and 64-row tiles: fewer outputs a
+// workgroup, two workgroups on a CU.  256 rows serve dense products only.
 template <int EPI>
 hipError_t run_height(const I8GemmArgs& a, hipStream_t stream) {
   constexpr int kHalf = EPI == kEpiSwiGLU ? 2 : 1;  // SwiGLU: gate and up share the columns of a tile
@@ -454,9 +495,11 @@ hipError_t run_height(const I8GemmArgs& a, hipStream_t stream) {
     case 320:
       return run_i8<320, 256 / kHalf, 2, 4, 2, 2, EPI>(a, stream);
     case 256:
-      return run_i8<256, 256 / kHalf, 4, 2, 2, 3, EPI>(a, stream);
+      return run_i8<256, 256 / kHalf, 4, 2, 2, 2, EPI>(a, stream);
+    case 192:
+      return run_i8<192, 256 / kHalf, 2, 4, 2, 3, EPI>(a, stream);
     case 128:
-      return run_i8<128, 128 / kHalf, 4, 2, 2, 3, EPI>(a, stream);
+      return run_i8<128, 128 / kHalf, 4, 2, 2, 2, EPI>(a, stream);
     case 64:
       // dense tiles half as wide while they still get a CU each: a CU's load
       // path is the bound, and more CUs take part (777 x 1001 x 1536: 10.2 us
@@ -474,33 +517,33 @@ hipError_t run_height(const I8GemmArgs& a, hipStream_t stream) {
 
 // Heights for `rows` rows spread over `groups` weight matrices of N rows.
 //
-// Routed, measured for whole layers (D x I, experts): up to 4 rows an expert
-// the few-rows kernel (7168 x 2048, 256 experts, 64 tokens: 1.68 ms against
-// 1.66 with 64-row tiles; 4 tokens: 0.30 against 0.34), up to 48 rows 64-row
-// tiles (512 tokens: 2.04 ms against 2.07 with 128 and 2.41 with the few-rows
-// kernel).  From 192 rows on 320-row tiles, whose waves read the fewest bytes
-// per product, where their items make two rounds over the chip (8192 tokens:
-// 4.23 ms against 4.68 with 256 and 5.18 with 128; 1024 x 1024, 32 experts, 512
-// rows each: 187 us against 206 and 196); between, 256-row tiles if their items
-// make five rounds (2048 tokens: 2.40 ms against 2.47 with 128 and 2.63 with
-// 320), else 128-row tiles, which fill the last round better (2048 x 768, 128
-// experts, 128 rows each: 307 us against 332 with 256; 1024 x 1024, 32 experts,
-// 256 rows each: 134 us against 145 with 320).
+// Routed, measured for whole layers: up to 4 rows an expert the few-rows kernel
+// (7168 x 2048, 256 experts, 4 tokens: 0.27 ms against 0.34 with 64-row tiles).
+// Where 192-row items make five rounds over the chip, the weights' stream is
+// the bound and a third slot of it is what counts: 192 rows (7168 x 2048, 256
+// experts, 512 tokens: 2.03 ms against 2.12 with 64 and 2.28 with 320; 4096
+// tokens: 2.81 against 3.26 with 128 and 3.02 with 320), and 320 rows from 192
+// an expert on, where segments would often need two (8192 tokens: 4.07 ms
+// against 4.54 with 256 and 5.00 with 128).  With fewer rounds small tiles fill
+// the last one better: 64 rows up to 48 an expert, then 128 (2048 x 768, 128
+// experts, 128 rows each: 302 us against 307 with 192; 1024 x 1024, 32 experts,
+// 512 rows each: 185 us against 208 with 320), and 320 from 192 rows and three
+// rounds on (2048 x 768, 256 rows each: 422 us against 437 with 128).
 //
 // Dense: the few-rows kernel while its workgroups fit the chip at once (256 x
-// 2048 x 7168: 24 us against 32 with 64-row tiles), else the least rounds times
-// the measured cost of a round (us per 128-byte stage: 64-row tiles 0.94 with
-// two workgroups on every CU and 0.57 with one, 128-row tiles 1.49 and 0.80,
-// 256-row 1.85, 320-row 2.2).
+// 2048 x 7168: 24.7 us against 26.2 with 64-row tiles), else the least rounds
+// times the measured cost of a round (us per 128-byte stage: 64-row tiles 0.85
+// with two workgroups on every CU and 0.56 with one, 128-row tiles 1.35 and
+// 0.87, 256-row 1.95, 320-row 2.4).
 int i8_tile_rows(int64_t rows, int64_t groups, int64_t N) {
   const int64_t known = device_compute_units(), cus = known > 0 ? known : 256;
   auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   if (groups > 1) {
     if (rows <= 4 * groups) return kI8RowsBM;
-    if (rows <= 48 * groups) return 64;
     const auto items = [&](int bm) { return groups * ceil_div(rows, bm * groups) * ceil_div(N, 128); };
-    if (rows >= 192 * groups) return items(320) >= 2 * cus ? 320 : 128;
-    return items(256) >= 5 * cus ? 256 : 128;
+    if (rows >= 192 * groups) return items(320) >= 3 * cus ? 320 : 128;
+    if (items(192) >= 5 * cus) return 192;
+    return rows <= 48 * groups ? 64 : 128;
   }
   if (ceil_div(rows, kI8RowsBM) * ceil_div(N, 64) <= cus) return kI8RowsBM;
   int best = 0;
@@ -513,10 +556,10 @@ int i8_tile_rows(int64_t rows, int64_t groups, int64_t N) {
       least = cost;
     }
   };
-  consider(64, 128, 2, 0.57, 0.94);
-  consider(128, 128, 2, 0.80, 1.49);
-  consider(256, 256, 1, 1.85, 1.85);
-  consider(320, 256, 1, 2.2, 2.2);
+  consider(64, 128, 2, 0.56, 0.85);
+  consider(128, 128, 2, 0.87, 1.35);
+  consider(256, 256, 1, 1.95, 1.95);
+  consider(320, 256, 1, 2.4, 2.4);
   return best;
 }
 

@@ -77,7 +77,7 @@ MATS = [(1, 1, 128), (1, 2048, 7168), (2, 17, 256), (15, 33, 384), (16, 64, 128)
         (33, 257, 640), (64, 512, 1024), (100, 96, 128), (255, 300, 256), (257, 511, 384), (777, 1001, 1536),
         (1024, 768, 2048), (513, 8, 65536),
         # sizes for which the product takes tiles of 64, 128, 256 and 320 rows
-        (777, 2048, 128), (2047, 2048, 256), (2050, 7168, 128), (2400, 8190, 128)]
+        (777, 2048, 128), (777, 7168, 256), (2050, 7168, 128), (2400, 8190, 128)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -177,11 +177,19 @@ LAYERS = [  # workload, minibatch, ring
     (synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian"), None, None),
     (synth.Workload("ragged", T=300, D=256, I=384, E=16, k=4, I_shared=128, seed=7, routing="gaussian"), 256, 512),
     (synth.Workload("skewed", T=1100, D=384, I=128, E=24, k=6, I_shared=256, seed=8, routing="zipf"), None, None),
-    # 25, 64 and 200 rows an expert: tiles of 64, 256 and 320 rows (those above take 32 and 128)
+    # 25, 64 and 200 rows an expert: tiles of 64, 192 and 320 rows (those above take 32 and 128)
     (synth.Workload("rows25", T=100, D=256, I=256, E=16, k=4, I_shared=128, seed=10, routing="gaussian"), None, None),
     (synth.Workload("rows64", T=1024, D=128, I=1280, E=128, k=8, I_shared=128, seed=11, routing="gaussian"), None,
      None),
-    (synth.Workload("rows200", T=3200, D=128, I=1024, E=64, k=4, I_shared=128, seed=12, routing="zipf"), None, None),
+    (synth.Workload("rows200", T=4800, D=128, I=1024, E=96, k=4, I_shared=128, seed=12, routing="zipf"), None, None),
+    # shared experts whose up/gate takes tiles of 64, 128, 256 and 320 rows
+    (synth.Workload("shared64", T=777, D=128, I=128, E=4, k=1, I_shared=2048, seed=15, routing="gaussian"), None, None),
+    (synth.Workload("shared128", T=777, D=128, I=128, E=4, k=1, I_shared=7168, seed=16, routing="gaussian"), None,
+     None),
+    (synth.Workload("shared256", T=2050, D=128, I=128, E=4, k=1, I_shared=7168, seed=17, routing="gaussian"), None,
+     None),
+    (synth.Workload("shared320", T=2400, D=128, I=128, E=4, k=1, I_shared=8192, seed=18, routing="gaussian"), None,
+     None),
     (synth.Workload("single", T=700, D=128, I=128, E=1, k=1, I_shared=128, seed=9, routing="gaussian"), None, None),
 ]
 
@@ -222,6 +230,57 @@ def test_int8_layer_is_the_same_for_every_minibatch():
     for b, C in ((1, 1), (7, 7), (64, 128), (1000, 2000)):
         got = make(w, dev, b, C)(x, None, wd, logits=lg)["out32"]
         assert torch.equal(got, want), (b, C)
+
+
+def random_layer(dev, T, D, I, E, k, seed):
+    """Weights drawn as int8 (no quantiser), routes and gates, all on the GPU."""
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    w = {}
+    for n, (a, b) in (("gate", (I, D)), ("up", (I, D)), ("down", (D, I))):
+        w["q_" + n] = torch.randint(-60, 61, (E, a, b), dtype=torch.int8, device=dev, generator=gen)
+        w["qs_" + n] = torch.randint(-60, 61, (a, b), dtype=torch.int8, device=dev, generator=gen)
+        w["s_" + n] = 1e-3 * torch.rand((E, a), device=dev, generator=gen)
+        w["ss_" + n] = 1e-3 * torch.rand(a, device=dev, generator=gen)
+    x = torch.randn((T, D), device=dev, generator=gen).to(torch.bfloat16)
+    idx = torch.rand((T, E), device=dev, generator=gen).topk(k, dim=1).indices.to(torch.int32).contiguous()
+    return w, x, idx, torch.rand((T, k), device=dev, generator=gen)
+
+
+def test_int8_mid_layer_is_the_same_for_every_tile_height_and_on_every_run():
+    # 256 rows an expert (320-row tiles, a resident workgroup walks several items), 64 and 8 of
+    # them in a minibatch (128-row tiles, and 64-row ones): the integer sums give the same bits
+    dev = need_gpu()
+    T, D, I, E, k = 4096, 2048, 768, 128, 8
+    w, x, idx, gate = random_layer(dev, T, D, I, E, k, 5)
+    want = None
+    for b in (None, None, 8192, 1024, 512, None):
+        say("int8 mid, minibatch", b)
+        m = MoELayer(shape_for(T, D, I, E, k, minibatch_rows=b, precision="int8", shared_precision="int8"), device=dev)
+        _, got = m.forward(w, x, x, gate, m.schedule(idx))
+        torch.cuda.synchronize()
+        want = got if want is None else want
+        assert torch.equal(got, want), b
+
+
+def test_int8_layers_on_two_streams_at_once():
+    dev = need_gpu()
+    T, D, I, E, k = 200, 512, 256, 32, 4
+    layers, streams, inputs, want = [], [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    for i in range(2):
+        inputs.append(random_layer(dev, T, D, I, E, k, 30 + i))
+        layers.append(MoELayer(shape_for(T, D, I, E, k, precision="int8", shared_precision="int8"), device=dev))
+        w, x, idx, gate = inputs[i]
+        want.append(layers[i].forward(w, x, x, gate, layers[i].schedule(idx))[1].clone())
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i in range(2):
+            w, x, idx, gate = inputs[i]
+            with torch.cuda.stream(streams[i]):
+                got[i] = layers[i].forward(w, x, x, gate, layers[i].schedule(idx))[1]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(got[i], want[i])
 
 
 @pytest.mark.parametrize("routed,shared", [(True, False), (False, True)])
