@@ -41,26 +41,42 @@ __device__ __forceinline__ int i8_exact_quotient(float v, float m) {
   return static_cast<int>(q);
 }
 
-// Eight quotients as bytes.  In fp32 the quotient v r with r = 127 / m is off by
-// at most 127 2^-23 (r's rounding and the product's), so it is right unless it
-// lies within 2^-15 of a half; adding 1.5 2^23 rounds it to an integer in the
-// sum's low bits.  The exact form then redoes the chunks that hold such a
-// value, one in a thousand or so, and rows whose r would leave fp32's range.
-// (fp64 throughout took 59 us for 8192 x 7168 bf16, bound by arithmetic.)
+// Eight quotients as bytes.  In fp32 the quotient v r, with r the float above
+// 127 / m rounded, is off by at most 127 1.5 2^-23, so it is right unless it lies
+// within 2^-14 of a half; adding 1.5 2^23 rounds it to an integer in the sum's
+// low bits.  The one exact half there is among bf16 values, |v| = m / 2 (127 has
+// to divide the other factor), comes out as 64, the even side, since r is not
+// below 127 / m.  A chunk that holds another value so close is settled by the
+// remainder d = 127 v - q m: 127 v = hi + lo exactly, hi - q m is exact (a
+// multiple of half m's last place, at most about m / 2), and 2 |d| against m,
+// with lo, says on which side of the half it lies.  (Settling m / 2 there as
+// well took 42 us for 8192 x 7168 bf16, without any check 34.)
+// `exact`: rows whose r would leave fp32's range.
 __device__ __forceinline__ uint2 i8_quotients(const float (&v)[kI8Chunk], float m, float r, bool exact) {
   constexpr float kMagic = 12582912.f;
   uint32_t b[kI8Chunk];
   float near = 1.f;
+  const float half = 0.5f * m;
 #pragma unroll
   for (int e = 0; e < kI8Chunk; ++e) {
     const float y = fmaf(v[e], r, kMagic);
     b[e] = __float_as_uint(y);
     const float f = fmaf(v[e], r, kMagic - y);  // the fraction, in [-0.5, 0.5]
-    near = fminf(near, 0.5f - fabsf(f));
+    near = fminf(near, fabsf(v[e]) == half ? 1.f : 0.5f - fabsf(f));
   }
-  if (exact || near < 0x1p-15f) {
+  if (exact) {
 #pragma unroll
     for (int e = 0; e < kI8Chunk; ++e) b[e] = static_cast<uint32_t>(i8_exact_quotient(v[e], m));
+  } else if (near < 0x1p-14f) {
+#pragma unroll
+    for (int e = 0; e < kI8Chunk; ++e) {
+      const float q = __uint_as_float(b[e]) - kMagic;
+      const float hi = 127.f * v[e], lo = fmaf(127.f, v[e], -hi);
+      const float d = fmaf(-q, m, hi);
+      const float over = fmaf(2.f, fabsf(d), -m) + 2.f * (d < 0.f ? -lo : lo);  // 2 |127 v - q m| - m
+      const bool step = over > 0.f || (over == 0.f && (b[e] & 1u));
+      b[e] += step ? (d < 0.f ? 0xffffffffu : 1u) : 0u;
+    }
   }
   auto pack = [&](int i) {
     const uint32_t lo = __builtin_amdgcn_perm(b[i + 1], b[i], 0x0c0c0400u);
@@ -89,7 +105,7 @@ struct I8RowScale {
     some = bits && finite;  // neither all zero nor not finite
     m = __uint_as_float(bits);
     scale = finite ? m / 127.f : __uint_as_float(0x7fc00000u);
-    r = some ? 127.f / m : 0.f;
+    r = some ? __uint_as_float(__float_as_uint(127.f / m) + 1u) : 0.f;
     exact = some && m < 0x1p-100f;  // r past fp32's range, or close
   }
   __device__ __forceinline__ uint2 operator()(const float (&v)[kI8Chunk]) const {
