@@ -207,8 +207,10 @@ moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router
  *   g_s = scale * s_s                    renorm = 0
  * The bias only chooses; it never enters a gate.  Scores are formed in 64
  * bits, and two c are told apart down to 2^-42 of their value: closer ones tie,
- * to the lower expert id.  A logit of -inf or NaN scores 0, and an expert whose
- * c is -inf or NaN ranks below every other; a non-finite logit or bias sets
+ * to the lower expert id.  (Without a bias, and unless groups rank by two
+ * scores, s orders as l does, and the logits themselves are compared.)  A logit
+ * of -inf or NaN scores 0, and an expert whose c is -inf or NaN ranks below
+ * every other; a non-finite logit or bias sets
  * MOE_DEVERR_NONFINITE.
  */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;

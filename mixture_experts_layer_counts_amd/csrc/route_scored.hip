@@ -210,6 +210,7 @@ __device__ __forceinline__ void lanes_best(double (&v)[K]) {
 
 // Candidate of expert e, and the id back from it.
 __device__ __forceinline__ double candidate(double c, int e) {
+  c += 0.0;  // -0 as +0
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(c)) & ~uint64_t(1023);
   return __longlong_as_double(static_cast<long long>(b | (c < 0.0 ? e : 1023 - e)));
 }
@@ -283,18 +284,23 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
         f32x4_t{l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]};
   if (live && bad) raise_error(err, kErrNonFinite);
 
-  // scores, then choosing values
+  // choosing values.  Without a bias, and with groups that rank by their
+  // largest, scores order as their logits do, and only a sum needs the row's
+  // exponentials.
   double c[EPL];
   float m = 0.f;
-  double inv = 1.0;  // softmax: 1 / sum
-  if (r.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = sigmoid64(l[i]);
-  } else {
+  double inv = 1.0;  // softmax: 1 / sum (renormalised gates do not need it)
+  const bool by_logit = !bias && (r.kept_groups == r.groups || !r.top2 || r.group_size == 1);
+  if (!r.sigmoid) {
     m = l[0];
 #pragma unroll
     for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
     m = lanes_max<LPT>(m);
+  }
+  if (r.sigmoid && !by_logit) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c[i] = sigmoid64(l[i]);
+  } else if (!r.sigmoid && !(by_logit && r.renorm)) {
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -303,12 +309,10 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     }
     sum = lanes_sum<LPT>(sum);
     inv = sum > 0.0 ? recip64(sum) : 0.0;  // at least 1, or 0 for a token whose logits are all -inf
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] *= inv;
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const double v = c[i] + static_cast<double>(b[i]);
+    const double v = by_logit ? static_cast<double>(l[i]) : c[i] * inv + static_cast<double>(b[i]);
     c[i] = v > kLast ? (v < -kLast ? v : -kLast) : kLast;
     if (expert_of<LPT, EPL>(j, i) >= E) c[i] = -INFINITY;
   }
@@ -555,7 +559,7 @@ hipError_t launch_route_scored(const RouterArgs& args, const float* planes, int 
   const int lanes = wave ? 64 : lanes_for(E);
   const RouterArgs r = with_groups(args, E, lanes);
   const bool vec = E % 4 == 0 && part_stride % 4 == 0 && aligned16(planes) && aligned16(bias) && aligned16(logits);
-  const int blocks = (T + 256 / lanes - 1) / (256 / lanes);
+  const int blocks = (T - 1) / (256 / lanes) + 1;
 #define MOE_RUN(K, LPT, EPL)                                                                                        \
   (vec ? route_scored_kernel<K, LPT, EPL, true> : route_scored_kernel<K, LPT, EPL, false>)                          \
       <<<blocks, 256, r.group_lanes ? sizeof(double) * 256 * EPL : 0, stream>>>(                                    \
@@ -592,7 +596,7 @@ hipError_t launch_route_backward(const RouterArgs& r, const float* logits, const
   if (E > 1024 || ld < E || ld > 1024 || k > 16 || !out32 == !out16) return hipErrorInvalidValue;
   if (out16 && (ld % 4 || reinterpret_cast<uintptr_t>(out16) % 8)) return hipErrorInvalidValue;
   const bool vec = E % 4 == 0 && aligned16(logits) && aligned16(out32);
-  const int lanes = lanes_for(ld), blocks = (T + 256 / lanes - 1) / (256 / lanes);
+  const int lanes = lanes_for(ld), blocks = (T - 1) / (256 / lanes) + 1;
 #define MOE_RUN(LPT, EPL)                                                                                         \
   (out16 ? (vec ? route_backward_kernel<LPT, EPL, true, true> : route_backward_kernel<LPT, EPL, true, false>)     \
          : (vec ? route_backward_kernel<LPT, EPL, false, true> : route_backward_kernel<LPT, EPL, false, false>))  \
