@@ -51,7 +51,7 @@ __device__ __forceinline__ int i8_exact_quotient(float v, float m) {
 // multiple of half m's last place, at most about m / 2), and 2 |d| against m,
 // with lo, says on which side of the half it lies.  (Settling m / 2 there as
 // well took 42 us for 8192 x 7168 bf16, without any check 34.)
-// `exact`: rows whose r would leave fp32's range.
+// `exact`: rows whose r or 127 m would leave fp32's range.
 __device__ __forceinline__ uint2 i8_quotients(const float (&v)[kI8Chunk], float m, float r, bool exact) {
   constexpr float kMagic = 12582912.f;
   uint32_t b[kI8Chunk];
@@ -106,7 +106,7 @@ struct I8RowScale {
     m = __uint_as_float(bits);
     scale = finite ? m / 127.f : __uint_as_float(0x7fc00000u);
     r = some ? __uint_as_float(__float_as_uint(127.f / m) + 1u) : 0.f;
-    exact = some && m < 0x1p-100f;  // r past fp32's range, or close
+    exact = some && (m < 0x1p-100f || m > 0x1p119f);  // r or 127 m past fp32's range, or close
   }
   __device__ __forceinline__ uint2 operator()(const float (&v)[kI8Chunk]) const {
     return some ? i8_quotients(v, m, r, exact) : make_uint2(0, 0);

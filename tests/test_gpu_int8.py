@@ -58,6 +58,14 @@ def test_quantize_int8_special_rows():
     v[5, 0], v[5, 1] = 1e-45, -1e-45  # the smallest numbers
     v[6, 0], v[6, 1] = 1.0, 2.0 ** -120
     v[7, ::2] = -0.0
+    # near the largest floats, values on either side of a half, and the half itself
+    top = torch.finfo(torch.float32).max
+    big = torch.zeros((1, 200))
+    big[0, 0] = top
+    big[0, 1:9] = torch.tensor([top / 2, top / 254, 3 * (top / 254), -5 * (top / 254), top / 127, -top / 2,
+                                7 * (top / 254), 0.0])
+    qb, _ = quantize_int8(big.to(dev))
+    assert np.array_equal(qb.cpu().numpy()[:, :200], int8.quantize(big.double().numpy())[0])
     q, s = (t.cpu() for t in quantize_int8(v.to(dev)))
     assert torch.isnan(s[1:4]).all() and (q[1:4] == 0).all()
     assert (q[0] == 0).all() and s[0] == 0 and (q[7] == 0).all() and s[7] == 0
@@ -385,6 +393,43 @@ def test_int8_layer_with_a_scored_router_in_a_graph():
     # and the eager step is the oracle's
     want, tol = oracle(w, {**inp, "x": x.cpu()}, got["idx"].cpu().numpy(), got["gate"].cpu().numpy())
     assert np.all(np.abs(got["out32"].cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("T", [2, 40, 400])
+def test_int8_layer_keeps_a_bad_token_to_itself(T):
+    # a token with an infinity comes out NaN; every other one has the bits it has without it
+    dev = need_gpu()
+    w = synth.Workload("bad", T=T, D=256, I=128, E=8, k=2, I_shared=128, seed=13, routing="gaussian")
+    say("int8 bad token", T)
+    inp = synth.make_inputs(w)
+    wd = quantised(inp, dev)
+    lg, x = inp["logits"].to(dev), inp["x"].to(dev)
+    want = make(w, dev)(x, None, wd, logits=lg)["out32"]
+    bad = x.clone()
+    bad[1, 17] = float("inf")
+    got = make(w, dev)(bad, None, wd, logits=lg)["out32"]
+    assert torch.isnan(got[1]).all()
+    keep = torch.arange(T) != 1
+    assert torch.equal(got[keep.to(dev)], want[keep.to(dev)])
+
+
+def test_int8_wide_experts_with_one_token():
+    # widths around what the down product of one or two tokens holds in LDS
+    dev = need_gpu()
+    for T in (1, 2):
+        for I in (20352, 20480, 40704, 41088):
+            say("int8 wide", T, I)
+            w, x, idx, gate = random_layer(dev, T, 128, I, 2, 1, 9)
+            m = MoELayer(shape_for(T, 128, I, 2, 1, precision="int8", shared_precision="int8"), device=dev)
+            _, got = m.forward(w, x, x, gate, m.schedule(idx))
+            # the same tokens among others take the products that read quantised rows
+            pad = 6
+            xs = torch.cat([x] + [x[:1]] * pad)
+            ids, gs = torch.cat([idx] + [idx[:1]] * pad), torch.cat([gate] + [gate[:1]] * pad)
+            m8 = MoELayer(shape_for(T + pad, 128, I, 2, 1, precision="int8", shared_precision="int8"), device=dev)
+            _, want = m8.forward(w, xs, xs, gs, m8.schedule(ids))
+            torch.cuda.synchronize()
+            assert m.device_error() == 0 and torch.equal(got, want[:T])
 
 
 @pytest.mark.parametrize("T", [1, 2, 5, 40])
