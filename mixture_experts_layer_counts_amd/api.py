@@ -2,7 +2,8 @@
 
 Torch supplies device memory and the current HIP stream; the C calls do all
 of the work.  Names follow include/moe.h: ``route``, ``schedule``,
-``forward``, ``quantize_mxfp8`` and ``pack_mxfp8_scales``.
+``forward``, ``quantize_mxfp8``, ``pack_mxfp8_scales``, ``quantize_int8``,
+``matmul_int8`` and ``linear_int8``.
 """
 
 from __future__ import annotations
@@ -173,14 +174,15 @@ class MoELayer:
             logits = torch.empty((s.T, s.E_total), dtype=torch.float32, device=dev)
         idx = torch.empty((s.T, s.k), dtype=torch.int32, device=dev)
         gate = torch.empty((s.T, s.k), dtype=torch.float32, device=dev)
-        if router is None:
-            _lib.check("moe_route", self.lib.moe_route(ctypes.byref(s), _ptr(x), _ptr(w_router), _ptr(logits),
-                                                       _ptr(idx), _ptr(gate), _ptr(self.ws), self.ws_bytes,
-                                                       _stream()))
-        else:
-            _lib.check("moe_route_scored", self.lib.moe_route_scored(
-                ctypes.byref(s), ctypes.byref(router), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(logits), _ptr(idx),
-                _ptr(gate), _ptr(self.ws), self.ws_bytes, _stream()))
+        with _on(dev):
+            if router is None:
+                _lib.check("moe_route", self.lib.moe_route(ctypes.byref(s), _ptr(x), _ptr(w_router), _ptr(logits),
+                                                           _ptr(idx), _ptr(gate), _ptr(self.ws), self.ws_bytes,
+                                                           _stream()))
+            else:
+                _lib.check("moe_route_scored", self.lib.moe_route_scored(
+                    ctypes.byref(s), ctypes.byref(router), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(logits),
+                    _ptr(idx), _ptr(gate), _ptr(self.ws), self.ws_bytes, _stream()))
         return logits, idx, gate
 
     def route_backward(self, logits: torch.Tensor, idx: torch.Tensor, dgate: torch.Tensor,
@@ -192,9 +194,10 @@ class MoELayer:
         _need(idx, "idx", torch.int32, (s.T, s.k), dev)
         _need(dgate, "dgate", torch.float32, (s.T, s.k), dev)
         dlogits = torch.empty((s.T, s.E_total), dtype=torch.float32, device=dev)
-        _lib.check("moe_route_backward", self.lib.moe_route_backward(
-            ctypes.byref(s), ctypes.byref(router), _ptr(logits), _ptr(idx), _ptr(dgate), _ptr(dlogits),
-            _ptr(self.ws), self.ws_bytes, _stream()))
+        with _on(dev):
+            _lib.check("moe_route_backward", self.lib.moe_route_backward(
+                ctypes.byref(s), ctypes.byref(router), _ptr(logits), _ptr(idx), _ptr(dgate), _ptr(dlogits),
+                _ptr(self.ws), self.ws_bytes, _stream()))
         return dlogits
 
     # -- moe_schedule ------------------------------------------------------
@@ -210,9 +213,10 @@ class MoELayer:
             "sched": torch.empty((max(s.max_rows, 1),), dtype=torch.int32, device=dev),
             "route_dst": torch.empty(s.num_src_ranks * NK, dtype=torch.int32, device=dev),
         }
-        _lib.check("moe_schedule", self.lib.moe_schedule(
-            ctypes.byref(s), _ptr(routes), _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["sched"]),
-            _ptr(out["route_dst"]), _ptr(self.ws), self.ws_bytes, _stream()))
+        with _on(dev):
+            _lib.check("moe_schedule", self.lib.moe_schedule(
+                ctypes.byref(s), _ptr(routes), _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["sched"]),
+                _ptr(out["route_dst"]), _ptr(self.ws), self.ws_bytes, _stream()))
         return out
 
     # -- moe_forward -------------------------------------------------------
@@ -235,10 +239,11 @@ class MoELayer:
             out_f32 = torch.empty((s.T, D), dtype=torch.float32, device=dev)
         if out_f32 is not None:
             _need(out_f32, "out32", torch.float32, (s.T, D), dev)
-        _lib.check("moe_forward", self.lib.moe_forward(
-            ctypes.byref(s), ctypes.byref(w), _ptr(x_src), _ptr(x_local), _ptr(gate), _ptr(sched["offsets"]),
-            _ptr(sched["sched"]), _ptr(sched["route_dst"]), _ptr(out), _ptr(out_f32), _ptr(self.ws), self.ws_bytes,
-            _stream()))
+        with _on(dev):
+            _lib.check("moe_forward", self.lib.moe_forward(
+                ctypes.byref(s), ctypes.byref(w), _ptr(x_src), _ptr(x_local), _ptr(gate), _ptr(sched["offsets"]),
+                _ptr(sched["sched"]), _ptr(sched["route_dst"]), _ptr(out), _ptr(out_f32), _ptr(self.ws),
+                self.ws_bytes, _stream()))
         return out, out_f32
 
     # -- whole layer -------------------------------------------------------
@@ -362,13 +367,15 @@ class MoEBackward:
             _need(grads[n], n, dt, shp, dev)
         g = _lib.MoeGrads(*[_ptr(grads[n]) for n, _ in _lib.MoeGrads._fields_])
         b = _lib.MoeBwdWeights(*[_ptr(bw[n]) for n, _ in _lib.MoeBwdWeights._fields_])
-        rest = (_ptr(idx), _ptr(gate), _ptr(sched["offsets"]), _ptr(sched["sched"]), _ptr(sched["route_dst"]),
-                _ptr(y_routes), _ptr(dout), ctypes.byref(g), _ptr(self.err), _ptr(self.ws), self.ws_bytes, _stream())
-        if router is None:
-            _lib.check("moe_backward", self.lib.moe_backward(ctypes.byref(s), ctypes.byref(b), _ptr(x), *rest))
-        else:
-            _lib.check("moe_backward_scored", self.lib.moe_backward_scored(
-                ctypes.byref(s), ctypes.byref(router), ctypes.byref(b), _ptr(x), _ptr(logits), *rest))
+        with _on(dev):
+            rest = (_ptr(idx), _ptr(gate), _ptr(sched["offsets"]), _ptr(sched["sched"]), _ptr(sched["route_dst"]),
+                    _ptr(y_routes), _ptr(dout), ctypes.byref(g), _ptr(self.err), _ptr(self.ws), self.ws_bytes,
+                    _stream())
+            if router is None:
+                _lib.check("moe_backward", self.lib.moe_backward(ctypes.byref(s), ctypes.byref(b), _ptr(x), *rest))
+            else:
+                _lib.check("moe_backward_scored", self.lib.moe_backward_scored(
+                    ctypes.byref(s), ctypes.byref(router), ctypes.byref(b), _ptr(x), _ptr(logits), *rest))
         return grads
 
     def device_error(self) -> int:
