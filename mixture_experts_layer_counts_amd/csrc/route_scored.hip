@@ -15,7 +15,7 @@
 // 16) largest of both by one bitonic merge, with the partner's list coming by
 // DPP inside the 16-lane row.  Rounds of a wave-wide arg-max (a token a wave,
 // k rounds of six crossbar steps) took 26 us for 8192 tokens where this takes
-// 10.6, and 10.0 for one where this takes 4.8.
+// 9.9, and 10.0 for one where this takes 4.7 (sigmoid, 256 experts in 8 groups).
 
 #include "common.h"
 #include "kernels.h"
@@ -26,21 +26,27 @@ namespace {
 
 constexpr double kLast = -1e300;  // choosing value of an expert whose c is NaN or -inf
 
+// A constant that stays in scalar registers: a plain one is copied into vector
+// registers before every step of a polynomial, two moves each.
+__device__ __forceinline__ double scalar(double c) {
+  asm("" : "+s"(c));
+  return c;
+}
+
 // exp(x) for |x| <= 750, relative error about 1e-14: x = n ln 2 + r with
 // |r| <= ln(2) / 2, and the Taylor polynomial of degree 11 (the next term is
 // below 7e-15 of the result).
 __device__ __forceinline__ double exp64(double x) {
   const double n = rint(x * 1.4426950408889634);
   const double r = fma(n, -0.6931471805599453, x);
-  double p = 1.0 / 39916800.0;
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
+  double p = fma(r, scalar(1.0 / 39916800.0), scalar(1.0 / 3628800.0));
+  p = fma(p, r, scalar(1.0 / 362880.0));
+  p = fma(p, r, scalar(1.0 / 40320.0));
+  p = fma(p, r, scalar(1.0 / 5040.0));
+  p = fma(p, r, scalar(1.0 / 720.0));
+  p = fma(p, r, scalar(1.0 / 120.0));
+  p = fma(p, r, scalar(1.0 / 24.0));
+  p = fma(p, r, scalar(1.0 / 6.0));
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
@@ -71,7 +77,8 @@ __device__ __forceinline__ double sigmoid64(float l) {
 // exp(l - m) for l <= m; 0 where it is below exp(-700).
 __device__ __forceinline__ double exp_below(float l, float m) {
   const double d = static_cast<double>(l) - static_cast<double>(m);
-  return d > -700.0 ? exp64(d) : 0.0;
+  const double e = exp64(d > -700.0 ? d : -700.0);  // no branch: neighbours' chains interleave
+  return d > -700.0 ? e : 0.0;
 }
 
 // Maximum and minimum of two candidates (never NaN).  As instructions of their
@@ -146,17 +153,21 @@ __device__ __forceinline__ uint32_t lanes_or(uint32_t v) {
   return v;
 }
 
-// The two largest of `lanes` (a power of two) neighbouring lanes' pairs.
-template <int LPT, int STEP = 0>
-__device__ __forceinline__ void lanes_two(double& best, double& next, int lanes) {
+// The two largest of `lanes` (a power of two) neighbouring lanes' pairs, for N
+// pairs side by side.
+template <int LPT, int N, int STEP = 0>
+__device__ __forceinline__ void lanes_two(double (&best)[N], double (&next)[N], int lanes) {
   if constexpr ((1 << STEP) < LPT) {
     if ((1 << STEP) >= lanes) return;  // uniform
-    double a, b, c, d;
-    partner64<STEP>(best, a, b);
-    partner64<STEP>(next, c, d);
-    best = max64(a, b);
-    next = max64(min64(a, b), max64(c, d));
-    lanes_two<LPT, STEP + 1>(best, next, lanes);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      double a, b, c, d;
+      partner64<STEP>(best[i], a, b);
+      partner64<STEP>(next[i], c, d);
+      best[i] = max64(a, b);
+      next[i] = max64(min64(a, b), max64(c, d));
+    }
+    lanes_two<LPT, N, STEP + 1>(best, next, lanes);
   }
 }
 
@@ -268,11 +279,23 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
   }
   float b[EPL];
   if (bias) load_row<LPT, EPL, VEC>(bias, j, E, 0.f, b);
+  if (planes != logits && live) {
+#pragma unroll
+    for (int q = 0; q < EPL / 4; ++q) {
+      const int e = expert_of<LPT, EPL>(j, 4 * q);
+      if constexpr (VEC) {
+        if (e < E) *reinterpret_cast<f32x4_t*>(logits + row + e) = f32x4_t{l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e + i < E) logits[row + e + i] = l[4 * q + i];
+      }
+    }
+  }
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = expert_of<LPT, EPL>(j, i);
-    if (planes != logits && live && e < E) logits[row + e] = l[i];
     bad |= !__builtin_isfinite(l[i]);
     if (!bias) b[i] = 0.f;
     bad |= !__builtin_isfinite(b[i]);
@@ -304,7 +327,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      c[i] = l[i] == -INFINITY ? 0.0 : exp_below(l[i], m);
+      c[i] = exp_below(l[i], m);
       sum += c[i];
     }
     sum = lanes_sum<LPT>(sum);
@@ -317,6 +340,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     if (expert_of<LPT, EPL>(j, i) >= E) c[i] = -INFINITY;
   }
 
+  // e / size
+  auto group_of = [&](int e) { return __umul24(static_cast<uint32_t>(e), r.group_magic) >> 20; };
   // groups: their scores into g_s, then each is ranked by counting the better ones
   uint64_t kept = ~uint64_t(0);
   if (r.kept_groups < r.groups) {
@@ -324,14 +349,21 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     if (r.group_lanes == 0) {
       // a group is 1, 2, 4, ... neighbouring lanes' quads: the two largest by
       // the first steps of the butterfly, in registers
+      double best[EPL / 4], next[EPL / 4];
 #pragma unroll
       for (int q = 0; q < EPL / 4; ++q) {
         const double h0 = max64(c[4 * q], c[4 * q + 1]), l0 = min64(c[4 * q], c[4 * q + 1]);
         const double h1 = max64(c[4 * q + 2], c[4 * q + 3]), l1 = min64(c[4 * q + 2], c[4 * q + 3]);
-        double best = max64(h0, h1), next = max64(min64(h0, h1), max64(l0, l1));
-        lanes_two<LPT>(best, next, size / 4);
-        const int e = expert_of<LPT, EPL>(j, 4 * q);
-        if (e < E && e % size == 0) g_s[tok_b][e / size] = r.top2 ? best + next : best;
+        best[q] = max64(h0, h1);
+        next[q] = max64(min64(h0, h1), max64(l0, l1));
+      }
+      lanes_two<LPT>(best, next, size / 4);
+      if ((j & (size / 4 - 1)) == 0) {  // a group's first lane
+#pragma unroll
+        for (int q = 0; q < EPL / 4; ++q) {
+          const int e = expert_of<LPT, EPL>(j, 4 * q);
+          if (e < E) g_s[tok_b][group_of(e)] = r.top2 ? best[q] + next[q] : best[q];
+        }
       }
     } else {
       // any other size: group_lanes lanes read one together
@@ -376,8 +408,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     hi = r.groups > 32 ? lanes_or<LPT>(hi) : 0u;
     kept = static_cast<uint64_t>(hi) << 32 | lo;
   }
-  // e / size as (e * group_magic) >> 20
-  auto in = [&](int e) { return (kept >> ((static_cast<uint32_t>(e) * r.group_magic) >> 20)) & 1; };
+  auto in = [&](int e) { return (kept >> group_of(e)) & 1; };
 #pragma unroll
   for (int q = 0; q < EPL / 4; ++q) {
     const int e = expert_of<LPT, EPL>(j, 4 * q);
@@ -475,7 +506,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      z[i] = l[i] == -INFINITY ? 0.0 : exp_below(l[i], m);
+      z[i] = exp_below(l[i], m);
       sum += z[i];
     }
     sum = lanes_sum<LPT>(sum);
@@ -540,12 +571,13 @@ RouterArgs with_groups(RouterArgs r, int E, int lanes) {
 
 // Experts a lane holds at most, and the lanes of a token for them.
 int lanes_for(int E) { return E <= 256 ? 16 : (E <= 512 ? 32 : 64); }
-// Up to this many tokens, with at most 512 experts, a whole wave takes a token,
-// four or eight experts a lane: with two waves or less for every SIMD its
-// shorter chain of fp64 instructions is what counts (256 experts in 8 groups:
-// one token 4.8 us against 7.3 with 16 lanes, 2048 tokens 6.2 against 7.8; 4096
-// tokens 8.9 against 8.0).
-constexpr int kWaveTokens = 2048;
+// For few tokens a whole wave takes one, four or eight experts a lane: its chain
+// of fp64 instructions is shorter, and that counts while SIMDs have one wave or
+// none (1024 tokens), for 129 to 256 experts while they have two.  256 experts in
+// 8 groups: one token 4.7 us against 6.8 with 16 lanes, 2048 tokens 6.0 against
+// 7.1, 4096 tokens 8.6 against 7.3; 128 experts: 1024 tokens 3.7 against 3.9,
+// 1536 4.5 against 3.9; 384 in 12 groups: 6.2 against 6.7 and 7.4 against 6.8.
+bool wave_a_token(int T, int E) { return E <= 512 && T <= (E > 128 && E <= 256 ? 2048 : 1024); }
 
 }  // namespace
 
@@ -555,7 +587,7 @@ hipError_t launch_route_scored(const RouterArgs& args, const float* planes, int 
   if (T <= 0) return hipSuccess;
   if (parts < 1 || parts > kMaxRouterParts || E > 1024 || k > 16 || args.groups > kMaxGroups || E % args.groups)
     return hipErrorInvalidValue;
-  const bool wave = E <= 512 && T <= kWaveTokens;
+  const bool wave = wave_a_token(T, E);
   const int lanes = wave ? 64 : lanes_for(E);
   const RouterArgs r = with_groups(args, E, lanes);
   const bool vec = E % 4 == 0 && part_stride % 4 == 0 && aligned16(planes) && aligned16(bias) && aligned16(logits);
