@@ -203,9 +203,10 @@ __device__ __forceinline__ int64_t i8_c_row(const I8GemmArgs& a, int64_t p) {
   return r >= 0 && r < a.c_rows ? r : -1;
 }
 constexpr int kI8RowsBM = 32;  // tile rows of the few-rows kernel (gemm_i8_rows.hip)
-// Tile height for `rows` rows spread over `groups` weight matrices: that of the
-// few-rows kernel, or 64, 128, 256 or 320 (gemm_i8.hip).
-int i8_tile_rows(int64_t rows, int64_t groups, int64_t N);
+// Tile height for `rows` rows spread over `groups` weight matrices of N rows
+// (`pair`: N of each of SwiGLU's two): that of the few-rows kernel, or 64, 128,
+// 192, 256 or 320 (gemm_i8.hip).
+int i8_tile_rows(int64_t rows, int64_t groups, int64_t N, bool pair);
 hipError_t launch_gemm_i8_tiles(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stream);
 // A dense product of M bf16 or fp32 rows [M][K] that quantises them itself, where

@@ -116,7 +116,7 @@ Layout layout_of(const moe_shape* s) {
   const moe::RoutedTiling tiling = s->precision == MOE_MXFP8
                                        ? moe::RoutedTiling{moe::gemm_mx_routed_bm(), 0, 0}
                                    : s->precision == MOE_INT8
-                                       ? moe::RoutedTiling{moe::i8_tile_rows(mb_rows, Lx, s->I), 0, 0}
+                                       ? moe::RoutedTiling{moe::i8_tile_rows(mb_rows, Lx, s->I, true), 0, 0}
                                        : moe::gemm_routed_tiling(mb_rows, s->max_rows, Lx, s->I, s->D,
                                                                  s->pipeline != 0);
   const int bm = tiling.bm;
@@ -473,9 +473,9 @@ moe::QuantI8Args quant_args(const void* src, int64_t K, int8_t* q, float* scale,
   return a;
 }
 
-// C = A B^T of quantised rows, dense.
+// C = A B^T of quantised rows, dense; with B1 SwiGLU of two products.
 moe::I8GemmArgs dense_i8(const int8_t* A, const float* As, int64_t M, const void* B, const void* Bs, int64_t N,
-                         int64_t K, void* C) {
+                         int64_t K, void* C, const void* B1 = nullptr, const void* Bs1 = nullptr) {
   moe::I8GemmArgs g{};
   g.A = A;
   g.As = As;
@@ -483,12 +483,14 @@ moe::I8GemmArgs dense_i8(const int8_t* A, const float* As, int64_t M, const void
   g.a_mod = INT64_MAX;
   g.B0 = static_cast<const int8_t*>(B);
   g.Bs0 = static_cast<const float*>(Bs);
+  g.B1 = static_cast<const int8_t*>(B1);
+  g.Bs1 = static_cast<const float*>(Bs1);
   g.N = static_cast<int>(N);
   g.K = static_cast<int>(K);
   g.C = C;
   g.ldc = N;
   g.c_rows = M;
-  g.tile_rows = moe::i8_tile_rows(M, 1, N);
+  g.tile_rows = moe::i8_tile_rows(M, 1, N, B1 != nullptr);
   g.dense_rows = static_cast<int>(M);
   return g;
 }
@@ -509,9 +511,7 @@ I8Ffn shared_ffn_i8(const moe_shape* shape, const moe_weights* w, const int8_t* 
   const int64_t T = shape->T, D = shape->D, Is = shape->I_shared;
   I8Ffn f{};
   float* h32 = at<float>(ws, L.hs32);
-  f.up = dense_i8(xq, xs, T, w->ws_gate, w->ss_gate, Is, D, h32);
-  f.up.B1 = static_cast<const int8_t*>(w->ws_up);
-  f.up.Bs1 = reinterpret_cast<const float*>(w->ss_up);
+  f.up = dense_i8(xq, xs, T, w->ws_gate, w->ss_gate, Is, D, h32, w->ws_up, w->ss_up);
   f.h = quant_args(h32, Is, at<int8_t>(ws, L.h_shared), at<float>(ws, L.hs_s));
   f.h_rows = T;
   f.down = dense_i8(f.h.q, f.h.scale, T, w->ws_down, w->ss_down, D, Is, at<float>(ws, L.shared_out));
@@ -594,8 +594,8 @@ hipError_t run_ffn_i8(const I8Ffn& f, int up_id, int down_id, hipStream_t s) {
 bool few_tokens_i8(const moe_shape* s, const Layout& L, const void* x_src, const void* x_local) {
   return s->precision == MOE_INT8 && s->shared_precision == MOE_INT8 && s->num_src_ranks == 1 && s->T > 0 &&
          x_src == x_local && reinterpret_cast<uintptr_t>(x_src) % 16 == 0 && L.n_minibatches == 1 &&
-         L.routed_bm == moe::kI8RowsBM && moe::i8_tile_rows(s->T, 1, s->I_shared) == moe::kI8RowsBM &&
-         moe::i8_tile_rows(s->T, 1, s->D) == moe::kI8RowsBM;
+         L.routed_bm == moe::kI8RowsBM && moe::i8_tile_rows(s->T, 1, s->I_shared, true) == moe::kI8RowsBM &&
+         moe::i8_tile_rows(s->T, 1, s->D, false) == moe::kI8RowsBM;
 }
 
 // Its launches: tokens quantised beside the tile list, up/gate of both, h's rows
