@@ -137,9 +137,9 @@ class MoELayer:
         self.ws_bytes = nbytes.value
         # the caching allocator hands out 512-byte aligned blocks
         self.ws = torch.empty(max(self.ws_bytes, 1), dtype=torch.uint8, device=self.device)
-        _lib.check("moe_workspace_init",
-                   self.lib.moe_workspace_init(ctypes.byref(shape), _ptr(self.ws), self.ws_bytes, _stream()))
-
+        with _on(self.device):
+            _lib.check("moe_workspace_init",
+                       self.lib.moe_workspace_init(ctypes.byref(shape), _ptr(self.ws), self.ws_bytes, _stream()))
         self._weight_specs = _weight_specs(shape)
 
     # -- sizes -------------------------------------------------------------
@@ -267,8 +267,9 @@ class MoELayer:
 
     def device_error(self) -> int:
         code = ctypes.c_int32(0)
-        _lib.check("moe_get_device_error", self.lib.moe_get_device_error(
-            ctypes.byref(self.shape), _ptr(self.ws), self.ws_bytes, _stream(), ctypes.byref(code)))
+        with _on(self.device):
+            _lib.check("moe_get_device_error", self.lib.moe_get_device_error(
+                ctypes.byref(self.shape), _ptr(self.ws), self.ws_bytes, _stream(), ctypes.byref(code)))
         return code.value
 
 
@@ -289,9 +290,10 @@ def schedule_static(shape: _lib.MoeShape, routes: torch.Tensor, dev_error: torch
         "sched": torch.empty((max(shape.max_rows, 1),), dtype=torch.int32, device=dev),
         "route_dst": torch.empty(shape.num_src_ranks * NK, dtype=torch.int32, device=dev),
     }
-    _lib.check("moe_schedule_static", lib.moe_schedule_static(
-        ctypes.byref(shape), _ptr(routes), _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["sched"]),
-        _ptr(out["route_dst"]), _ptr(dev_error), _stream()))
+    with _on(dev):
+        _lib.check("moe_schedule_static", lib.moe_schedule_static(
+            ctypes.byref(shape), _ptr(routes), _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["sched"]),
+            _ptr(out["route_dst"]), _ptr(dev_error), _stream()))
     return out
 
 
@@ -319,8 +321,9 @@ def prepare_backward(shape: _lib.MoeShape, weights: Dict[str, torch.Tensor], w_r
            "ws_gu_t": (D, 2 * Is), "ws_down_t": (Is, D), "w_router_t": (D, Ep)}
     out = {n: torch.empty(shp, dtype=torch.bfloat16, device=dev) for n, shp in out.items()}
     bw = _lib.MoeBwdWeights(*[_ptr(out[n]) for n, _ in _lib.MoeBwdWeights._fields_])
-    _lib.check("moe_backward_prepare", lib.moe_backward_prepare(ctypes.byref(shape), ctypes.byref(w), _ptr(w_router),
-                                                                ctypes.byref(bw), _stream()))
+    with _on(dev):
+        _lib.check("moe_backward_prepare", lib.moe_backward_prepare(
+            ctypes.byref(shape), ctypes.byref(w), _ptr(w_router), ctypes.byref(bw), _stream()))
     return out
 
 
@@ -379,7 +382,7 @@ class MoEBackward:
         return grads
 
     def device_error(self) -> int:
-        torch.cuda.current_stream().synchronize()
+        torch.cuda.current_stream(self.device).synchronize()
         return int(self.err.item())
 
 
@@ -392,7 +395,8 @@ def quantize_mxfp8(src: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     rows = src.numel() // max(K, 1)
     q = torch.empty(src.shape, dtype=torch.uint8, device=src.device)
     sc = torch.empty(src.shape[:-1] + (K // 32,), dtype=torch.uint8, device=src.device)
-    _lib.check("moe_quantize_mxfp8", lib.moe_quantize_mxfp8(_ptr(src), rows, K, _ptr(q), _ptr(sc), _stream()))
+    with _on(src.device):
+        _lib.check("moe_quantize_mxfp8", lib.moe_quantize_mxfp8(_ptr(src), rows, K, _ptr(q), _ptr(sc), _stream()))
     return q, sc
 
 
@@ -406,7 +410,8 @@ def tile_bf16(w: torch.Tensor) -> torch.Tensor:
     if K % 64:
         raise ValueError("K must be a multiple of 64")
     out = torch.empty((G, K // 64, N, 64), dtype=torch.bfloat16, device=w.device)
-    _lib.check("moe_tile_bf16", lib.moe_tile_bf16(_ptr(w), G, N, K, _ptr(out), _stream()))
+    with _on(w.device):
+        _lib.check("moe_tile_bf16", lib.moe_tile_bf16(_ptr(w), G, N, K, _ptr(out), _stream()))
     return out
 
 
@@ -430,8 +435,9 @@ def pack_mxfp8_scales(scale: torch.Tensor) -> torch.Tensor:
     if KS % 4:
         raise ValueError("K must be a multiple of 128")
     packed = torch.empty((G, KS // 4, N, 4), dtype=torch.uint8, device=scale.device)
-    _lib.check("moe_mxfp8_pack_scales", lib.moe_mxfp8_pack_scales(_ptr(scale), G, N, KS * 32, _ptr(packed),
-                                                                  _stream()))
+    with _on(scale.device):
+        _lib.check("moe_mxfp8_pack_scales", lib.moe_mxfp8_pack_scales(_ptr(scale), G, N, KS * 32, _ptr(packed),
+                                                                      _stream()))
     return packed
 
 

@@ -216,11 +216,12 @@ __global__ __launch_bounds__(WAVES* kWave) void gemm_i8_rows_kernel(const I8Gemm
     rows_block<NBL, WAVES, EPI1>(b, block - blocks0, red);
 }
 
-// ---- products that quantise their own activations, one or two rows at a time: every workgroup reads its rows x [.][K] (out of L2) and keeps their
-// quotients in LDS, which costs less than a launch before it (1 x 2048 x 7168:
-// 10.4 us against 15.2, 2 rows 12.3 against 14.9; three rows already 15.3
-// against 14.7).  a: as for the other products, without A and As. ----
-// (LDS: the rows beside up to 16 KB of partial sums, within the 64 KB of a plain launch)
+// ---- products that quantise their own activations, one or two rows at a time:
+// every workgroup reads its rows x [.][K] (out of L2) and keeps their quotients
+// in LDS, which costs less than a launch before it (1 x 2048 x 7168: 10.4 us
+// against 15.2, 2 rows 12.3 against 14.9; three rows already 15.3 against
+// 14.7).  a: as for the other products, without A and As.  (LDS: the rows beside
+// up to 16 KB of partial sums, within the 64 KB of a plain launch.) ----
 constexpr int kFusedRows = 2, kFusedLds = 40 * 1024;
 
 template <int NBL, int WAVES, int EPI, bool VEC, typename T>

@@ -16,6 +16,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWaveRow = kWave * kI8Held * kI8Chunk;  // longest row that a wave holds
+constexpr int64_t kLaunchRows = int64_t(1) << 23;     // a launch's threads stay below 2^32
 
 template <int TH, bool VEC, typename T>
 __global__ __launch_bounds__(kThreads) void quantize_rows_i8_kernel(const QuantI8Args a, int rows) {
@@ -35,7 +37,7 @@ __global__ __launch_bounds__(kThreads) void quantize_two_i8_kernel(const QuantI8
 
 template <bool VEC, typename T>
 hipError_t run_rows(const QuantI8Args& a, int rows, hipStream_t stream) {
-  if (a.Kp <= kWave * kI8Held * kI8Chunk) {
+  if (a.Kp <= kWaveRow) {
     constexpr int per = kThreads / kWave;
     quantize_rows_i8_kernel<kWave, VEC, T><<<(rows - 1) / per + 1, kThreads, 0, stream>>>(a, rows);
   } else {
@@ -65,9 +67,21 @@ hipError_t launch_quantize_rows_i8(const QuantI8Args& a, bool src_f32, int64_t r
   if (rows > 0x7fffffff || !valid(a)) return hipErrorInvalidValue;
   const int64_t per16 = src_f32 ? 4 : 8;  // elements in 16 bytes
   const bool vec = a.K % per16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
-  const int n = static_cast<int>(rows);
-  if (src_f32) return vec ? run_rows<true, float>(a, n, stream) : run_rows<false, float>(a, n, stream);
-  return vec ? run_rows<true, uint16_t>(a, n, stream) : run_rows<false, uint16_t>(a, n, stream);
+  for (int64_t at = 0; at < rows; at += kLaunchRows) {
+    QuantI8Args part = a;
+    part.p_begin += at;
+    if (!a.sched) {
+      part.src = static_cast<const char*>(a.src) + at * a.K * (src_f32 ? 4 : 2);
+      part.q += at * a.Kp;
+      part.scale += at;
+    }
+    const int n = static_cast<int>(rows - at < kLaunchRows ? rows - at : kLaunchRows);
+    const hipError_t e = src_f32 ? (vec ? run_rows<true, float>(part, n, stream) : run_rows<false, float>(part, n, stream))
+                                 : (vec ? run_rows<true, uint16_t>(part, n, stream)
+                                        : run_rows<false, uint16_t>(part, n, stream));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

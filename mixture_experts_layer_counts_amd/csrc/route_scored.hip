@@ -408,7 +408,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     hi = r.groups > 32 ? lanes_or<LPT>(hi) : 0u;
     kept = static_cast<uint64_t>(hi) << 32 | lo;
   }
-  auto in = [&](int e) { return (kept >> group_of(e)) & 1; };
+  auto in = [&](int e) { return (kept >> (group_of(e) & 63)) & 1; };  // past E: any bit
 #pragma unroll
   for (int q = 0; q < EPL / 4; ++q) {
     const int e = expert_of<LPT, EPL>(j, 4 * q);

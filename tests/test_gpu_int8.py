@@ -460,3 +460,20 @@ def test_int8_layer_without_tokens():
     r = m(torch.empty((0, 128), dtype=torch.bfloat16, device=dev), None, quantised(inp, dev),
           logits=torch.empty((0, 4), device=dev))
     assert r["out"].shape == (0, 128) and m.device_error() == 0
+
+
+@pytest.mark.parametrize("K", [1, 2056])
+def test_quantize_more_rows_than_one_launch(K):
+    # the rows either side of 2^23 and the last ones, of K = 1 (2^23 + 37 rows) and of rows a workgroup each
+    dev = need_gpu()
+    rows = (1 << 23) + 37
+    say("int8 many rows", rows, K)
+    x = torch.zeros((rows, K), dtype=torch.bfloat16, device=dev)
+    ids = torch.tensor([0, 1, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, rows - 1], device=dev)
+    g = torch.Generator().manual_seed(3)
+    x[ids] = torch.randn((6, K), generator=g).to(torch.bfloat16).to(dev)
+    q, s = quantize_int8(x)
+    want_q, want_s = int8.quantize(x[ids].double().cpu().numpy())
+    assert np.array_equal(q[ids][:, :K].cpu().numpy(), want_q)
+    assert np.allclose(s[ids].double().cpu().numpy(), want_s, rtol=2.0**-24, atol=0)  # one rounding to fp32
+    assert not q[ids][:, K:].any() and int((s != 0).sum()) == 6 and int((q != 0).any(1).sum()) == 6
