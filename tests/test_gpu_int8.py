@@ -18,7 +18,7 @@ import synth
 from mixture_experts_layer_counts_amd import (MoELayer, linear_int8, matmul_int8, quantize_int8, router_for, shape_for,
                                               tile_int8)
 from oracle import int8
-from tests._gpu import need_gpu, say, to_dev
+from tests._gpu import mx_shared_weights_dev, mx_weights_dev, need_gpu, say, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -318,6 +318,91 @@ def test_int8_for_one_kind_of_expert(routed, shared):
     other = shared_part(rb if shared else rp, yb if shared else plain.routed_rows())
     scale = r["out32"].abs().max().double()
     assert (shared_part(r, y) - other).abs().max() <= 2.0 ** -20 * scale
+
+
+@pytest.mark.parametrize("T", [1, 130])
+@pytest.mark.parametrize("routed", [True, False])
+def test_int8_beside_mxfp8(routed, T):
+    # int8 and MXFP8 experts in one layer: each part has the bits it has beside its own kind
+    dev = need_gpu()
+    w = synth.Workload("int8-mx", T=T, D=256, I=128, E=8, k=2, I_shared=128, seed=6, routing="gaussian")
+    say("int8 beside mxfp8", routed, T)
+    inp = synth.make_inputs(w)
+    d = to_dev(inp, dev)
+    x, lg = d["x"], d["logits"]
+    weights = quantised(inp, dev, routed=routed, shared=not routed)
+    mx = {**mx_weights_dev(d), **mx_shared_weights_dev(d)}
+    weights = {n: v for n, v in weights.items() if not n.startswith("w")}
+    weights.update({n: v for n, v in mx.items() if n not in weights})
+    kinds = ("int8", "mxfp8") if routed else ("mxfp8", "int8")
+    m = make(w, dev, precision=kinds[0], shared=kinds[1])
+    r = m(x, None, weights, logits=lg)
+    y = m.routed_rows().clone()
+    ref_i8, ref_mx = make(w, dev), make(w, dev, precision="mxfp8", shared="mxfp8")
+    ri, rm = ref_i8(x, None, quantised(inp, dev), logits=lg), ref_mx(x, None, mx, logits=lg)
+    torch.cuda.synchronize()
+    assert m.device_error() == 0
+    yi, ym = ref_i8.routed_rows().clone(), ref_mx.routed_rows().clone()
+    assert torch.equal(y, yi if routed else ym)
+    g = r["gate"].double()
+
+    def shared_part(res, rows):
+        return res["out32"].double() - (g[:, :, None] * rows.double().view(w.T, w.k, w.D)).sum(1)
+    other = shared_part(rm, ym) if routed else shared_part(ri, yi)
+    assert (shared_part(r, y) - other).abs().max() <= 2.0 ** -20 * r["out32"].abs().max().double()
+
+
+@pytest.mark.parametrize("M", [1, 2, 40])
+def test_linear_int8_in_a_graph(M):
+    # captured, replayed on new rows between eager calls on two streams
+    dev = need_gpu()
+    K, N = 1500, 776
+    say("linear graph", M)
+    gen = torch.Generator().manual_seed(M)
+    wq, ws = quantize_int8(torch.randn((N, K), generator=gen).to(dev))
+    x = torch.randn((M, K), generator=gen).to(torch.bfloat16).to(dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        linear_int8(x, wq, ws, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = linear_int8(x, wq, ws, out_dtype=torch.float32)
+    for rep in range(3):
+        x.copy_(torch.randn((M, K), generator=gen).to(torch.bfloat16))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            want = linear_int8(x, wq, ws, out_dtype=torch.float32)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), rep
+    q, s = int8.quantize(x.double().cpu().numpy())
+    exact = int8.product(q, s, wq.cpu().numpy()[:, :K], ws.cpu().numpy())
+    assert np.all(np.abs(got.cpu().numpy() - exact) <= 2.0 ** -21 * np.abs(exact))
+
+
+def test_int8_one_token_in_a_graph():
+    dev = need_gpu()
+    D, I, E, k = 512, 256, 16, 4
+    say("int8 one token graph")
+    w, x, idx, gate = random_layer(dev, 1, D, I, E, k, 8)
+    m, eager = (MoELayer(shape_for(1, D, I, E, k, precision="int8", shared_precision="int8"), device=dev)
+                for _ in range(2))
+    m.forward(w, x, x, gate, m.schedule(idx))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = m.forward(w, x, x, gate, m.schedule(idx))[1]
+    for rep in range(3):
+        x.copy_(torch.randn((1, D), device=dev).to(torch.bfloat16))
+        idx.copy_(torch.randperm(E, device=dev)[:k].view(1, k))
+        want = eager.forward(w, x, x, gate, eager.schedule(idx))[1]
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), rep
+    assert m.device_error() == 0
 
 
 def test_int8_expert_parallel_share():

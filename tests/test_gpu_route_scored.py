@@ -65,6 +65,18 @@ CASES = [  # T, E, k, bias, router
     (2051, 500, 16, True, dict(score="sigmoid", groups=20, kept_groups=3)),
     (2050, 128, 9, False, dict(score="sigmoid", groups=4, kept_groups=1)),
     (2053, 201, 3, True, dict(score="softmax", renorm=False)),
+    # every count of lanes and experts a lane with up to 8 and up to 16 choices
+    (31, 500, 16, False, dict(score="softmax", groups=4, kept_groups=2, group_score="max")),
+    (2055, 256, 11, False, dict(score="sigmoid", groups=16, kept_groups=5)),
+    (1030, 120, 8, True, dict(score="sigmoid", groups=15, kept_groups=4)),
+    (1031, 300, 10, False, dict(score="sigmoid", groups=3, kept_groups=1, group_score="max")),
+    (1033, 512, 7, True, dict(score="softmax", groups=32, kept_groups=4)),
+    (41, 640, 8, True, dict(score="sigmoid", groups=5, kept_groups=2)),
+    # either side of where a wave takes a token
+    (1024, 128, 4, True, dict(score="sigmoid", groups=8, kept_groups=2)),
+    (1025, 128, 4, True, dict(score="sigmoid", groups=8, kept_groups=2)),
+    (2048, 160, 4, False, dict(score="softmax", groups=10, kept_groups=3)),
+    (1025, 260, 6, False, dict(score="softmax")),
 ]
 
 
