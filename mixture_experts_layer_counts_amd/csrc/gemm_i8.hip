@@ -215,6 +215,49 @@ __device__ __forceinline__ void k_loop_i8(char* smem, const I8Stream<AI, BI>& sr
   for (; kt < nk; ++kt) step(kt, std::false_type{});
 }
 
+// Who walks which item of a tile list.  The items are cut into 8 contiguous runs,
+// one per XCD (neighbours share operands in its L2).  Tiles of about equal rows
+// give equal runs, walked in fixed strides: runs balanced by cost there differ by
+// a few items, and one that is two items longer than a whole number of rounds
+// costs the chip a round (2048 x 768, 128 experts, 4096 tokens: 438 us against
+// 404; 7168 x 2048, 256 experts, 4096 tokens: 2.82 ms against 2.68).  Under skewed
+// routing the runs balance cost, and the items past the first round are handed
+// out as the workgroups get to them: from the XCD's own queue, and when that run
+// is used up from the longest rest of another's (Zipf(1.2) routes, 7168 x 2048,
+// 256 experts: 4.65 -> 4.38 ms at 8192 tokens and 1.66 -> 1.56 at 2048; 4096 x
+// 1408, 96 experts: 1.61 -> 1.52 at 8192).  A draw is made an item ahead, so its
+// trip to memory is hidden; drawn when needed, small layers took 10 us more.
+__device__ __forceinline__ int draw(int32_t* queue, int xcd) {
+  return __hip_atomic_fetch_add(queue + xcd * kQueueStride, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Item at which the run of XCD j (at most kXcds: the end) starts, balanced by
+// the tiles' cost.
+__device__ __forceinline__ int run_start(const int32_t* __restrict__ runs, int n_blocks, int j) {
+  return static_cast<int>(static_cast<int64_t>(runs[j]) * n_blocks / kTileRunFrac);
+}
+
+// An item of another XCD's run, or -1 if all are handed out.  Queues only grow,
+// so a draw that fails shows its run to be used up: at most 8 passes.
+__device__ __forceinline__ int steal(int32_t* queue, const int32_t* __restrict__ runs, int n_blocks, int per_xcd) {
+  const int lane = lane_id(), j = lane < kXcds ? lane : 0;
+  const int first = run_start(runs, n_blocks, j), len = run_start(runs, n_blocks, j + 1) - first;
+  for (;;) {
+    const int left =
+        len - per_xcd - __hip_atomic_load(queue + j * kQueueStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    int best = left > 0 ? left * kXcds + j : -1;
+#pragma unroll
+    for (int d = 1; d < kXcds; d *= 2) best = max(best, __shfl_xor(best, d));
+    best = __builtin_amdgcn_readfirstlane(best);
+    if (best < 0) return -1;
+    const int from = best % kXcds;
+    int drawn = 0;
+    if (lane == 0) drawn = draw(queue, from);
+    drawn = __builtin_amdgcn_readfirstlane(drawn);
+    if (drawn < __builtin_amdgcn_readlane(len, from) - per_xcd)
+      return __builtin_amdgcn_readlane(first, from) + per_xcd + drawn;
+  }
+}
+
 // What the epilogue needs of an item beside its sums: the scales of its rows
 // and columns and the output rows, kept in LDS past the rings, twice (the next
 // item's are filled in before this one's epilogue).
@@ -247,31 +290,52 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
   constexpr int STORES = FM * 4 * PIECE_STORES;    // of a whole tile
   constexpr int RING = ring_bytes(BM, BROWS, NSA, NSB);
   using Tables = I8Tables<BM, BROWS>;
-  __shared__ __attribute__((aligned(1024))) char smem[RING + 2 * sizeof(Tables) + NW * PIECE];
+  // the next item goes into the padding behind the last piece's last row
+  constexpr int NEXT = RING + 2 * sizeof(Tables) + (PIECE ? NW * PIECE - 16 : 0);
+  __shared__ __attribute__((aligned(1024))) char smem[NEXT + 16];
   Tables* const tables = reinterpret_cast<Tables*>(smem + RING);
+  int* const next_s = reinterpret_cast<int*>(smem + NEXT);
 
   const int n_blocks = (args.N + BN - 1) / BN;
   const int xcd = static_cast<int>(blockIdx.x) % kXcds;
-  // work items are cut into 8 contiguous runs, one per XCD, as in the bf16 and
-  // MXFP8 kernels; workgroup b walks items b / 8, b / 8 + G, ... of the run of
-  // XCD b mod 8 (G workgroups per XCD), so an XCD's workgroups move side by side
+  // the run of XCD b mod 8, where workgroup b starts with item b / 8.  Walked in
+  // strides of the XCD's workgroups, or with `queued` drawn, when the runs
+  // balanced by cost start further than half a round or a sixteenth of a run from
+  // equal ones.
+  const int per_xcd = static_cast<int>(gridDim.x) / kXcds;  // the grid is a multiple of kXcds
+  bool queued = false;
   int run0, len;
-  if (args.tiles) {  // positions in 1/kTileRunFrac of a tile
-    run0 = static_cast<int>(static_cast<int64_t>(__builtin_amdgcn_readfirstlane(args.tile_runs[xcd])) * n_blocks /
-                            kTileRunFrac);
-    len = static_cast<int>(static_cast<int64_t>(__builtin_amdgcn_readfirstlane(args.tile_runs[xcd + 1])) * n_blocks /
-                           kTileRunFrac) -
-          run0;
+  if (args.tiles) {
+    const int lane = lane_id(), j = lane < kXcds ? lane : kXcds;
+    const int start = run_start(args.tile_runs, n_blocks, j);
+    const int items = __builtin_amdgcn_readlane(start, kXcds), share = (items + kXcds - 1) / kXcds;
+    const int equal = j * share < items ? j * share : items;
+    queued = __any(abs(start - equal) > max(per_xcd / 2, share / 16));
+    run0 = __builtin_amdgcn_readlane(queued ? start : equal, xcd);
+    len = __builtin_amdgcn_readlane(queued ? start : equal, xcd + 1) - run0;
   } else {
     const int W = dense_tiles * n_blocks, chunk = (W + kXcds - 1) / kXcds;
     run0 = xcd * chunk;
     len = W - run0 < chunk ? W - run0 : chunk;
   }
-  const int per_xcd = static_cast<int>(gridDim.x) / kXcds;  // the grid is a multiple of kXcds
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int wm = wave / WN, wn = wave % WN;
   int local = static_cast<int>(blockIdx.x) / kXcds;
-  if (local >= len) return;
+  // wave 0 draws, the others read it from LDS: an item, or -1
+  auto publish = [&](int drawn) __attribute__((always_inline)) {  // drawn: from its own queue
+    if (wave == 0) {
+      const int ticket = per_xcd + __builtin_amdgcn_readfirstlane(drawn);
+      *next_s = ticket < len ? run0 + ticket : steal(args.queue, args.tile_runs, n_blocks, per_xcd);
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*next_s);
+  };
+  int item = run0 + local, drawn = 0;
+  if (local >= len) {
+    if (!queued) return;
+    item = publish(len);
+    if (item < 0) return;
+  }
 
   I8Stream<AI, BI> src;
   src.nk = args.K / kRB;
@@ -355,7 +419,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
     if (tid < BROWS) tables[buf].col_scale[tid] = cs;
   };
 
-  begin(run0 + local, 0);
+  // (the draw for the item after this one is on its way ahead of the loads)
+  if (queued && threadIdx.x == 0) drawn = draw(args.queue, xcd);
+  begin(item, 0);
   int stores = 0;  // of the last epilogue, at least
   for (int turn = 0;; ++turn) {
     // 32-row blocks of this wave that hold tile rows (wave-uniform)
@@ -388,9 +454,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
       }
     }
     const int col0 = n0 + wn * WTN, buf = turn & 1, rows = nrows;
-    local += per_xcd;
-    const bool more = local < len;
-    if (more) begin(__builtin_amdgcn_readfirstlane(run0 + local), buf ^ 1);
+    bool more;
+    if (queued) {
+      item = publish(drawn);
+      more = item >= 0;
+      if (more && threadIdx.x == 0) drawn = draw(args.queue, xcd);
+    } else {
+      local += per_xcd;
+      more = local < len;
+      item = __builtin_amdgcn_readfirstlane(run0 + local);
+    }
+    if (more) begin(item, buf ^ 1);
 
     // ---- epilogue.  The MFMA layout gives lane l column l % 32 of rows 8*(r/4)
     // + 4*(l/32) + r%4 of each 32 x 32 block. ----
@@ -568,7 +642,7 @@ int i8_tile_rows(int64_t rows, int64_t groups, int64_t N, bool pair) {
 }
 
 hipError_t launch_gemm_i8_tiles(const I8GemmArgs& a, int epilogue, hipStream_t stream) {
-  if (a.tiles && !a.tile_runs) return hipErrorInvalidValue;
+  if (a.tiles && (!a.tile_runs || !a.queue)) return hipErrorInvalidValue;
   switch (epilogue) {
     case kEpiSwiGLU:
       return run_height<kEpiSwiGLU>(a, stream);

@@ -63,8 +63,12 @@ __host__ __device__ inline int tile_run_cap(int max_tiles) { return (max_tiles +
 // `runs` (kTileRunBounds words per minibatch, each run spanning at most
 // tile_run_cap(max_tiles) tiles) may be NULL: the kernels then cut the items
 // into runs of equal count.
+// `queues` (or NULL): kTileQueues queues per minibatch, cleared for the GEMMs
+// that hand out their items at run time (gemm_i8.hip).
+constexpr int kQueueStride = 16, kQueueInts = 8 * kQueueStride, kTileQueues = 2;
 hipError_t launch_build_tiles(const int32_t* offsets, int L, int64_t b, int64_t max_rows, int BM, int n_minibatches,
-                              int max_tiles, int4* tiles, int32_t* tile_count, int32_t* runs, hipStream_t stream);
+                              int max_tiles, int4* tiles, int32_t* tile_count, int32_t* runs, int32_t* queues,
+                              hipStream_t stream);
 
 // Tile list of a dense GEMM run through the routed kernels: rows 0 .. rows-1 as
 // one segment of expert 0, cut into ceil(rows / BM) tiles of equal height
@@ -188,6 +192,7 @@ struct I8GemmArgs {
   const int4* tiles;
   const int32_t* tile_count;
   const int32_t* tile_runs;
+  int32_t* queue;  // kQueueInts, cleared: items of each XCD's run that were handed out
   int max_tiles;
   int tile_rows;  // height of the tile lists, which picks the kernel (i8_tile_rows)
   int dense_rows;

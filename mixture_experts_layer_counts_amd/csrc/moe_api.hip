@@ -27,7 +27,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  size_t err, ord_local, chunk_cnt, M, tiles, tile_count, tile_runs, ring, ring_s, h, h_s, Y, h_shared, shared_out, router_parts,
+  size_t err, ord_local, chunk_cnt, M, tiles, tile_count, tile_runs, queues, ring, ring_s, h, h_s, Y, h_shared, shared_out, router_parts,
       xs_q, xs_s, hs_s, h32, hs32, shared_tiles, shared_tile_count, total;
   int router_splits;
   int64_t n_minibatches;
@@ -139,6 +139,8 @@ Layout layout_of(const moe_shape* s) {
   L.tiles = take(sizeof(int4) * L.n_minibatches * L.max_tiles);
   L.tile_count = take(sizeof(int32_t) * std::max<int64_t>(L.n_minibatches, 1));
   L.tile_runs = take(sizeof(int32_t) * moe::kTileRunBounds * std::max<int64_t>(L.n_minibatches, 1));
+  if (s->precision == MOE_INT8)
+    L.queues = take(sizeof(int32_t) * moe::kTileQueues * moe::kQueueInts * std::max<int64_t>(L.n_minibatches, 1));
   if (s->precision == MOE_MXFP8) {  // E4M3 bytes + one E8M0 byte per 32 along K
     L.ring = take(s->ring_rows * s->D);
     L.ring_s = take(s->ring_rows * (s->D / 32));
@@ -549,6 +551,7 @@ I8Ffn routed_ffn_i8(const moe_shape* shape, const moe_weights* w, const int32_t*
   u.tiles = at<int4>(ws, L.tiles) + m * L.max_tiles;
   u.tile_count = at<int32_t>(ws, L.tile_count) + m;
   u.tile_runs = at<int32_t>(ws, L.tile_runs) + m * moe::kTileRunBounds;
+  u.queue = at<int32_t>(ws, L.queues) + m * moe::kTileQueues * moe::kQueueInts;
   u.max_tiles = L.max_tiles;
   u.tile_rows = L.routed_bm;
   f.h = quant_args(h32, I, at<int8_t>(ws, L.h), at<float>(ws, L.h_s), expert_offsets + shape->experts_per_rank, p_begin);
@@ -561,6 +564,7 @@ I8Ffn routed_ffn_i8(const moe_shape* shape, const moe_weights* w, const int32_t*
   d.a_idx = nullptr;
   d.a_sub = p_begin;
   d.a_mod = INT64_MAX;
+  d.queue += moe::kQueueInts;
   d.B0 = static_cast<const int8_t*>(w->w_down);
   d.B1 = nullptr;
   d.Bs0 = reinterpret_cast<const float*>(w->s_down);
@@ -860,7 +864,7 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
     ProbeScope probe(MOE_K_TILES, s);
     MOE_TRY_HIP(moe::launch_build_tiles(expert_offsets, Lx, b, shape->max_rows, bm,
                                         static_cast<int>(L.n_minibatches), L.max_tiles,
-                                        tiles, tile_count, tile_runs, s));
+                                        tiles, tile_count, tile_runs, i8 ? at<int32_t>(ws, L.queues) : nullptr, s));
   }
 
   // 2. shared expert on this rank's tokens (MoK paper §3.4, "Shared Expert":
@@ -1415,7 +1419,7 @@ static moe_status backward_impl(const moe_shape* shape, const moe_router* router
 
   // ---- routed experts: the forward's rows again, in schedule order ----
   MOE_TRY_HIP(moe::launch_build_tiles(expert_offsets, Lx, P, P, L.tiling.bm, 1, L.max_tiles, tiles, tile_count,
-                                      tile_runs, s));
+                                      tile_runs, nullptr, s));
   MOE_TRY_HIP(moe::launch_gather_src(xb, T, D, k, route_dst, P, P, ring, dev_error, s));
   MOE_TRY_HIP(moe::launch_dy_gather(dob, topk_gate, sched_src, P, T, D, k, dy, dev_error, s));
   auto routed = [&](const void* A, int64_t lda, const void* B, int64_t b_stride, int N, int K, void* C, int64_t ldc) {

@@ -395,7 +395,11 @@ __device__ __forceinline__ void build_tiles(int m, const int32_t* __restrict__ o
 __global__ __launch_bounds__(1024) void build_tiles_kernel(const int32_t* __restrict__ offsets, int L, int64_t b,
                                                            int64_t max_rows, int BM, int max_tiles,
                                                            int4* __restrict__ tiles, int32_t* __restrict__ tile_count,
-                                                           int32_t* __restrict__ runs) {
+                                                           int32_t* __restrict__ runs,
+                                                           int32_t* __restrict__ queues) {
+  constexpr int kClear = kTileQueues * kQueueInts;
+  static_assert(kClear <= 1024, "one thread per word");
+  if (queues && threadIdx.x < kClear) queues[static_cast<int64_t>(blockIdx.x) * kClear + threadIdx.x] = 0;
   build_tiles(blockIdx.x, offsets, L, b, max_rows, BM, max_tiles, tiles, tile_count, runs);
 }
 
@@ -450,13 +454,14 @@ hipError_t launch_dense_tiles(int64_t rows, int BM, int4* tiles, int32_t* tile_c
 }
 
 hipError_t launch_build_tiles(const int32_t* offsets, int L, int64_t b, int64_t max_rows, int BM, int n_minibatches,
-                              int max_tiles, int4* tiles, int32_t* tile_count, int32_t* runs, hipStream_t stream) {
+                              int max_tiles, int4* tiles, int32_t* tile_count, int32_t* runs, int32_t* queues,
+                              hipStream_t stream) {
   static_assert(kTileRunBounds == kXcds + 1, "one run per XCD");
   if (n_minibatches <= 0) return hipSuccess;
   // run positions (kTileRunFrac per tile) are int32
   if (runs && static_cast<int64_t>(max_tiles) * kTileRunFrac >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   build_tiles_kernel<<<n_minibatches, 1024, 0, stream>>>(offsets, L, b, max_rows, BM, max_tiles, tiles, tile_count,
-                                                         runs);
+                                                         runs, queues);
   return hipGetLastError();
 }
 

@@ -198,6 +198,10 @@ LAYERS = [  # workload, minibatch, ring
      None),
     (synth.Workload("shared320", T=2400, D=128, I=128, E=4, k=1, I_shared=8192, seed=18, routing="gaussian"), None,
      None),
+    # a few large experts: items drawn from the queues, at tiles of 64, 128 and 320 rows
+    (synth.Workload("zipf64", T=600, D=128, I=512, E=64, k=4, I_shared=128, seed=19, routing="zipf"), None, None),
+    (synth.Workload("zipf128", T=1700, D=256, I=384, E=64, k=4, I_shared=128, seed=20, routing="zipf"), None, None),
+    (synth.Workload("zipf320", T=6100, D=128, I=1152, E=96, k=4, I_shared=128, seed=22, routing="zipf"), None, None),
     (synth.Workload("single", T=700, D=128, I=128, E=1, k=1, I_shared=128, seed=9, routing="gaussian"), None, None),
 ]
 
@@ -268,6 +272,39 @@ def test_int8_mid_layer_is_the_same_for_every_tile_height_and_on_every_run():
         torch.cuda.synchronize()
         want = got if want is None else want
         assert torch.equal(got, want), b
+
+
+@pytest.mark.parametrize("hot", ["one", "two", "most"])
+def test_int8_hot_experts(hot):
+    # routes that leave most experts, and most XCDs' shares, without rows: the bits of small minibatches, on every
+    # run, and in a graph
+    dev = need_gpu()
+    T, D, I, E, k = 3000, 256, 640, 40, 2
+    say("int8 hot experts", hot)
+    w, x, idx, gate = random_layer(dev, T, D, I, E, k, 17)
+    if hot == "one":
+        idx[:] = torch.tensor([7, 8], dtype=torch.int32, device=dev)  # two experts in all
+    elif hot == "two":
+        idx[:, 0], idx[:, 1] = 0, (torch.arange(T, device=dev) % 2 + E - 2).to(torch.int32)
+    else:
+        idx[: T - 200] = torch.tensor([20, 3], dtype=torch.int32, device=dev)
+    kw = dict(precision="int8", shared_precision="int8")
+    small = MoELayer(shape_for(T, D, I, E, k, minibatch_rows=96, ring_rows=192, **kw), device=dev)
+    want = small.forward(w, x, x, gate, small.schedule(idx))[1]
+    m = MoELayer(shape_for(T, D, I, E, k, **kw), device=dev)
+    for _ in range(3):
+        assert torch.equal(m.forward(w, x, x, gate, m.schedule(idx))[1], want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = m.forward(w, x, x, gate, m.schedule(idx))[1]
+    for _ in range(3):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert torch.equal(m.forward(w, x, x, gate, m.schedule(idx))[1], want)
+    assert m.device_error() == 0 and small.device_error() == 0
 
 
 def test_int8_layers_on_two_streams_at_once():
