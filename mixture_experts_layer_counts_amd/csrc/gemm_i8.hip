@@ -596,14 +596,15 @@ hipError_t run_height(const I8GemmArgs& a, hipStream_t stream) {
 // (7168 x 2048, 256 experts, 4 tokens: 0.27 ms against 0.34 with 64-row tiles).
 // Where 192-row items make five rounds over the chip, the weights' stream is
 // the bound and a third slot of it is what counts: 192 rows (7168 x 2048, 256
-// experts, 512 tokens: 2.03 ms against 2.12 with 64 and 2.28 with 320; 4096
-// tokens: 2.81 against 3.26 with 128 and 3.02 with 320), and 320 rows from 192
-// an expert on, where segments would often need two (8192 tokens: 4.07 ms
-// against 4.54 with 256 and 5.00 with 128).  With fewer rounds small tiles fill
-// the last one better: 64 rows up to 48 an expert, then 128 (2048 x 768, 128
-// experts, 128 rows each: 302 us against 307 with 192; 1024 x 1024, 32 experts,
-// 512 rows each: 185 us against 208 with 320), and 320 from 192 rows and three
-// rounds on (2048 x 768, 256 rows each: 422 us against 437 with 128).
+// experts, 512 tokens: 1.98 ms against 2.07 with 64 and 2.24 with 320; 4096
+// tokens: 2.68 against 3.25 with 128 and 2.93 with 320), from 96 rows an expert on
+// with three rounds too (2048 x 768, 128 experts, 128 rows each: 288 us against
+// 300 with 128; 64 rows each 240 against 231).  320 rows from 192 an expert on,
+// where segments would often need two (7168 x 2048, 8192 tokens: 4.10 ms against
+// 5.12 with 192), given three rounds (2048 x 768, 256 rows each: 405 us against
+// 430 with 192).  With fewer rounds small tiles fill the last one better: 64
+// rows up to 48 an expert, then 128 (1024 x 1024, 32 experts, 375 rows each: 155
+// us against 164 with 320 and 177 with 192).
 //
 // Dense: the few-rows kernel while its workgroups fit the chip at once (256 x
 // 2048 x 7168: 24.7 us against 26.2 with 64-row tiles), else the least rounds
@@ -617,7 +618,7 @@ int i8_tile_rows(int64_t rows, int64_t groups, int64_t N, bool pair) {
     if (rows <= 4 * groups) return kI8RowsBM;
     const auto items = [&](int bm) { return groups * ceil_div(rows, bm * groups) * ceil_div(N, 128); };
     if (rows >= 192 * groups) return items(320) >= 3 * cus ? 320 : 128;
-    if (items(192) >= 5 * cus) return 192;
+    if (items(192) >= (rows >= 96 * groups ? 3 : 5) * cus) return 192;
     return rows <= 48 * groups ? 64 : 128;
   }
   if (ceil_div(rows, kI8RowsBM) * ceil_div(N, 64) <= cus) return kI8RowsBM;
