@@ -216,68 +216,14 @@ __global__ __launch_bounds__(WAVES* kWave) void gemm_i8_rows_kernel(const I8Gemm
     rows_block<NBL, WAVES, EPI1>(b, block - blocks0, red);
 }
 
-// ---- products that quantise their own activations, one or two rows at a time:
-// every workgroup reads its rows x [.][K] (out of L2) and keeps their quotients
-// in LDS, which costs less than a launch before it (1 x 2048 x 7168: 10.4 us
-// against 15.2, 2 rows 12.3 against 14.9; three rows already 15.3 against
-// 14.7).  a: as for the other products, without A and As.  (LDS: the rows beside
-// up to 16 KB of partial sums, within the 64 KB of a plain launch.) ----
-constexpr int kFusedRows = 2, kFusedLds = 40 * 1024;
-
-template <int NBL, int WAVES, int EPI, bool VEC, typename T>
-__device__ __forceinline__ void fused_block(const I8GemmArgs& a, const T* __restrict__ x, int K, int per, int block,
-                                            char* xq, i32x4_t* red, uint32_t (&part)[kFusedRows][WAVES]) {
-  int e, tile_rows, n0;
-  int64_t p0;
-  if (!find_block<16 * NBL>(a, block, e, p0, tile_rows, n0)) return;
-  const int tid = threadIdx.x, lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int chunks = a.K / kI8Chunk;
-  const int stride = a.K + 16;  // rows at one K position fall on distinct banks
-  // `per` rows at a time: all of a tile's, unless a token names its expert twice
-  for (int base = 0; base < tile_rows; base += per) {
-    const int nrows = tile_rows - base < per ? tile_rows - base : per;
-    if (base > 0) __syncthreads();  // the rows before are done with the LDS
-    for (int m = 0; m < nrows; ++m) {
-      const T* __restrict__ row = x + i8_a_row(a, p0 + base + m) * K;
-      uint32_t bits = 0;
-      for (int c = tid; c < chunks; c += WAVES * kWave) {
-        float v[kI8Chunk];
-        i8_load_chunk<VEC>(row, c, K, v);
-        bits = i8_max_bits(v, bits);
-      }
-#pragma unroll
-      for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t o = __shfl_xor(bits, d);
-        bits = o > bits ? o : bits;
-      }
-      if (lane == 0) part[m][wave] = bits;
-    }
-    __syncthreads();
-    auto row_bits = [&](int m) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) bits = part[m][w] > bits ? part[m][w] : bits;
-      return bits;
-    };
-    for (int m = 0; m < nrows; ++m) {
-      const T* __restrict__ row = x + i8_a_row(a, p0 + base + m) * K;
-      const I8RowScale quant(row_bits(m));
-      for (int c = tid; c < chunks; c += WAVES * kWave) {
-        float v[kI8Chunk];
-        i8_load_chunk<VEC>(row, c, K, v);
-        *reinterpret_cast<uint2*>(xq + m * stride + c * kI8Chunk) = quant(v);
-      }
-    }
-    __syncthreads();
-    const int row = (lane & 15) < nrows ? lane & 15 : nrows - 1;
-    const LdsRows rows{xq + row * stride + (lane >> 4) * 16};
-    i32x4_t acc[1][NBL][1];
-    rows_sums<1, NBL, 1, WAVES>(a, e, n0, rows, wave, lane, acc);
-    rows_finish<1, NBL, 1, WAVES, EPI>(a, e, p0 + base, nrows, n0, red, wave, lane, acc,
-                                       [&](int) { return I8RowScale(row_bits(row)).scale; });
-  }
-}
+// ---- a dense product of up to three rows that quantises them itself: every
+// workgroup reads the rows x [.][K] (out of L2) and keeps their quotients in LDS,
+// which saves a launch (1 x 2048 x 7168: 9.8 us in a graph against 13.2, called
+// from Python 10.1 against 13.6; three rows 12.9 against 13.2 and 10.6 against
+// 13.6; four rows 14.4 against 13.5).  In a layer, where the next launch waits on
+// the GPU, it gains nothing.  a: as for the other products, without A and As.
+// (LDS: the rows beside the partial sums, within the 64 KB of a plain launch.) ----
+constexpr int kFusedRows = 3, kFusedLds = 40 * 1024;
 
 template <int WAVES, int EPI, bool VEC, typename T>
 __global__ __launch_bounds__(WAVES* kWave) void linear_i8_rows_kernel(const I8GemmArgs a, const T* __restrict__ x,
@@ -285,22 +231,49 @@ __global__ __launch_bounds__(WAVES* kWave) void linear_i8_rows_kernel(const I8Ge
   extern __shared__ __attribute__((aligned(16))) char xq[];
   __shared__ i32x4_t red[WAVES * kWave];
   __shared__ uint32_t part[kFusedRows][WAVES];
-  fused_block<1, WAVES, EPI, VEC>(a, x, K, a.dense_rows, blockIdx.x, xq, red, part);
-}
-
-// Two products over fp32 rows of their K (both a multiple of 128).
-template <int NBL, int WAVES, int EPI0, int EPI1>
-__global__ __launch_bounds__(WAVES* kWave) void fused_pair_i8_kernel(const I8GemmArgs a, const float* __restrict__ xa,
-                                                                     const I8GemmArgs b, const float* __restrict__ xb,
-                                                                     int per, int blocks0) {
-  extern __shared__ __attribute__((aligned(16))) char xq[];
-  __shared__ i32x4_t red[WAVES * NBL * kWave];
-  __shared__ uint32_t part[kFusedRows][WAVES];
-  const int block = blockIdx.x;
-  if (block < blocks0)
-    fused_block<NBL, WAVES, EPI0, true>(a, xa, a.K, per, block, xq, red, part);
-  else
-    fused_block<NBL, WAVES, EPI1, true>(b, xb, b.K, per, block - blocks0, xq, red, part);
+  const int n0 = blockIdx.x * 16, nrows = a.dense_rows;
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int chunks = a.K / kI8Chunk;
+  const int stride = a.K + 16;  // rows at one K position fall on distinct banks
+  for (int m = 0; m < nrows; ++m) {
+    const T* __restrict__ row = x + static_cast<int64_t>(m) * K;
+    uint32_t bits = 0;
+    for (int c = tid; c < chunks; c += WAVES * kWave) {
+      float v[kI8Chunk];
+      i8_load_chunk<VEC>(row, c, K, v);
+      bits = i8_max_bits(v, bits);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const uint32_t o = __shfl_xor(bits, d);
+      bits = o > bits ? o : bits;
+    }
+    if (lane == 0) part[m][wave] = bits;
+  }
+  __syncthreads();
+  auto row_bits = [&](int m) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) bits = part[m][w] > bits ? part[m][w] : bits;
+    return bits;
+  };
+  for (int m = 0; m < nrows; ++m) {
+    const T* __restrict__ row = x + static_cast<int64_t>(m) * K;
+    const I8RowScale quant(row_bits(m));
+    for (int c = tid; c < chunks; c += WAVES * kWave) {
+      float v[kI8Chunk];
+      i8_load_chunk<VEC>(row, c, K, v);
+      *reinterpret_cast<uint2*>(xq + m * stride + c * kI8Chunk) = quant(v);
+    }
+  }
+  __syncthreads();
+  const int row = (lane & 15) < nrows ? lane & 15 : nrows - 1;
+  const LdsRows rows{xq + row * stride + (lane >> 4) * 16};
+  i32x4_t acc[1][1][1];
+  rows_sums<1, 1, 1, WAVES>(a, 0, n0, rows, wave, lane, acc);
+  rows_finish<1, 1, 1, WAVES, EPI>(a, 0, 0, nrows, n0, red, wave, lane, acc,
+                                   [&](int) { return I8RowScale(row_bits(row)).scale; });
 }
 
 template <int EPI, typename T>
@@ -338,8 +311,8 @@ hipError_t run_rows(const I8GemmArgs& a, const I8GemmArgs* b, hipStream_t stream
 // with four waves, 13.8 with 32 columns); past that wider blocks read the
 // activations less often (64 x 7168 x 2048: 11.4 us with 64 columns, 15.3 with
 // 16).  SwiGLU blocks hold gate and up columns and stay at 16 (the layer of
-// 7168 x 2048 and 256 experts at one token: 114 us, 121 with 32; at 64 tokens
-// 1.70 ms and 1.68); four waves do there once the blocks fill the chip (122 us
+// 7168 x 2048 and 256 experts at one token: 96 us, 103 with 32; at 64 tokens
+// 1.63 ms and 1.64); four waves do there once the blocks fill the chip (99 us
 // with eight).
 template <int EPI0, int EPI1>
 hipError_t pick_rows(const I8GemmArgs& a, const I8GemmArgs* b, hipStream_t stream) {
@@ -394,22 +367,6 @@ hipError_t launch_linear_i8_fused(const I8GemmArgs& a, const void* x, bool x_f32
   if (epilogue == kEpiF32)
     return x_f32 ? run_linear<kEpiF32, float>(a, x, K, stream) : run_linear<kEpiF32, uint16_t>(a, x, K, stream);
   return hipErrorInvalidValue;
-}
-
-hipError_t launch_fused_pair_i8(const I8GemmArgs& a, const float* xa, const I8GemmArgs& b, const float* xb,
-                                int64_t rows, hipStream_t stream) {
-  for (const I8GemmArgs* x : {&a, &b})
-    if (x->K % kStage || x->N <= 0 || !linear_i8_fused(rows, x->K)) return hipErrorInvalidValue;
-  if (!xa || !xb || reinterpret_cast<uintptr_t>(xa) % 16 || reinterpret_cast<uintptr_t>(xb) % 16)
-    return hipErrorInvalidValue;
-  constexpr int kBlocks = 4, kWaves = 4;  // 64 columns and four waves, as for products of this size elsewhere
-  const int64_t first = rows_blocks(a, 16 * kBlocks), work = first + rows_blocks(b, 16 * kBlocks);
-  if (work > 0x7fffffff) return hipErrorInvalidValue;
-  const size_t lds = static_cast<size_t>(rows) * ((a.K > b.K ? a.K : b.K) + 16);
-  fused_pair_i8_kernel<kBlocks, kWaves, kEpiBF16, kEpiF32>
-      <<<static_cast<unsigned>(work), kWaves * kWave, lds, stream>>>(a, xa, b, xb, static_cast<int>(rows),
-                                                                           static_cast<int>(first));
-  return hipGetLastError();
 }
 
 hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream) {

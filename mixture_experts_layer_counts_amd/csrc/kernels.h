@@ -219,11 +219,6 @@ hipError_t launch_gemm_i8(const I8GemmArgs& args, int epilogue, hipStream_t stre
 bool linear_i8_fused(int64_t M, int64_t K);
 hipError_t launch_linear_i8_fused(const I8GemmArgs& a, const void* x, bool x_f32, int64_t K, int epilogue,
                                   hipStream_t stream);
-// Two products (bf16 and fp32) over fp32 rows [.][K] that quantise them
-// themselves, `rows` rows of a tile at a time; linear_i8_fused(rows, K) holds for
-// both.
-hipError_t launch_fused_pair_i8(const I8GemmArgs& a, const float* xa, const I8GemmArgs& b, const float* xb,
-                                int64_t rows, hipStream_t stream);
 // Two few-rows products in one launch: both SwiGLU, or bf16 and fp32.
 hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream);
 

@@ -603,7 +603,7 @@ bool few_tokens_i8(const moe_shape* s, const Layout& L, const void* x_src, const
 }
 
 // Its launches: tokens quantised beside the tile list, up/gate of both, h's rows
-// (within the down product for one or two tokens), down of both.
+// of both, down of both.
 hipError_t few_tokens_experts_i8(const moe_shape* shape, const moe_weights* w, const void* x,
                                  const int32_t* sched_src, const int32_t* expert_offsets, const Layout& L, void* ws,
                                  hipStream_t s) {
@@ -627,9 +627,6 @@ hipError_t few_tokens_experts_i8(const moe_shape* shape, const moe_weights* w, c
     if (e != hipSuccess) return e;
   }
   ProbeScope probe(MOE_K_DOWN, s);
-  if (moe::linear_i8_fused(T, shape->I) && moe::linear_i8_fused(T, shape->I_shared))
-    return moe::launch_fused_pair_i8(f.down, static_cast<const float*>(f.h.src), sh.down,
-                                     static_cast<const float*>(sh.h.src), T, s);
   e = moe::launch_quantize_two_i8(f.h, f.h_rows, sh.h, sh.h_rows, s);
   return e == hipSuccess ? moe::launch_gemm_i8_pair(f.down, f.down_epi, sh.down, sh.down_epi, s) : e;
 }

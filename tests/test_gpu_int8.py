@@ -389,6 +389,24 @@ def test_int8_beside_mxfp8(routed, T):
     assert (shared_part(r, y) - other).abs().max() <= 2.0 ** -20 * r["out32"].abs().max().double()
 
 
+@pytest.mark.parametrize("K,N", [(100, 33), (1500, 301), (7168, 256), (20480, 48), (40960, 16), (65536, 16)])
+def test_linear_int8_of_few_rows_is_the_same_as_of_many(K, N):
+    # up to three rows that fit in LDS are quantised inside the product, more or longer ones before it
+    dev = need_gpu()
+    say("linear few rows", K, N)
+    gen = torch.Generator().manual_seed(K)
+    wq, ws = quantize_int8(torch.randn((N, K), generator=gen).to(dev))
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn((6, K), generator=gen).to(dtype).to(dev)
+        x[4, 3] = float("nan")
+        want = linear_int8(x, wq, ws, torch.float32)
+        assert torch.isnan(want[4]).all()
+        for M in (1, 2, 3, 4):
+            for first in (0, 6 - M):
+                got = linear_int8(x[first:first + M].clone(), wq, ws, torch.float32)
+                assert torch.equal(got.view(torch.int32), want[first:first + M].view(torch.int32)), (dtype, M, first)
+
+
 @pytest.mark.parametrize("M", [1, 2, 40])
 def test_linear_int8_in_a_graph(M):
     # captured, replayed on new rows between eager calls on two streams
@@ -536,7 +554,7 @@ def test_int8_layer_keeps_a_bad_token_to_itself(T):
 
 
 def test_int8_wide_experts_with_one_token():
-    # widths around what the down product of one or two tokens holds in LDS
+    # wide h rows, of one and two tokens and beside others
     dev = need_gpu()
     for T in (1, 2):
         for I in (20352, 20480, 40704, 41088):
