@@ -200,7 +200,12 @@ struct I8GemmArgs {
 // Rows outside the operand (a table not built by the schedule kernels) read
 // row 0 and write nothing.
 __device__ __forceinline__ int64_t i8_a_row(const I8GemmArgs& a, int64_t p) {
-  const int64_t r = a.a_idx ? a.a_idx[p] / a.a_div : (p - a.a_sub) % a.a_mod;
+  if (a.a_idx) {
+    const int r = a.a_idx[p] / a.a_div;
+    return r >= 0 && r < a.a_rows ? r : 0;
+  }
+  int64_t r = p - a.a_sub;
+  if (r >= a.a_mod) r %= a.a_mod;  // a ring that wraps: a 64-bit division costs a microsecond an item
   return r >= 0 && r < a.a_rows ? r : 0;
 }
 __device__ __forceinline__ int64_t i8_c_row(const I8GemmArgs& a, int64_t p) {
