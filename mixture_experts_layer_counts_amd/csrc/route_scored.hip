@@ -522,7 +522,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const
   if (r.renorm) {
     const double W = lanes_sum<LPT>(s);
     const double mean = W > 0.0 ? lanes_sum<LPT>(dw * s) / W : 0.0;
-    dw = W > 0.0 ? (dw - mean) / W : 0.0;
+    // (a single expert's gate is `scale` whatever its score: no rounding left over)
+    dw = W > 0.0 && k > 1 ? (dw - mean) / W : 0.0;
   }
   // the softmax's own mean, sum_s s_s dw_s: zero for renormalised gates
   const double mean = dense ? lanes_sum<LPT>(s * dw) : 0.0;

@@ -195,6 +195,19 @@ def test_route_backward_refuses_ids_out_of_range():
     assert close(got, scored.backward(logits, good, drop, "softmax", False, 1.0), np.ones((4, 3)))
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_gradient_of_a_single_renormalised_gate_is_zero(kind):
+    # the gate is `scale` whatever the logit
+    dev = need_gpu()
+    say("one expert a token", kind)
+    for T, E in ((1, 6), (17, 36), (3000, 300)):
+        rng = np.random.default_rng(E)
+        m, r, lg, idx, gate = run(dev, rng.standard_normal((T, E)), 1, score=kind, scale=2.5)
+        dg = torch.from_numpy(rng.standard_normal((T, 1)).astype(np.float32)).to(dev)
+        assert torch.all(gate == 2.5)
+        assert not m.route_backward(lg, idx, dg, router=r).any()
+
+
 def test_routing_from_x_scores_the_same_logits():
     # the router projection with K ranges: the choice equals the oracle's of the logits that come back
     dev = need_gpu()
