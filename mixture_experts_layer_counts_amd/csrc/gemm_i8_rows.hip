@@ -14,8 +14,6 @@
 // One launch can hold two products (the routed experts' and the shared one's,
 // which at a few tokens would each leave most of the chip idle).
 
-#include <utility>
-
 #include "common.h"
 #include "i8.h"
 #include "kernels.h"
@@ -370,11 +368,10 @@ hipError_t launch_linear_i8_fused(const I8GemmArgs& a, const void* x, bool x_f32
 }
 
 hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs& b, int epi_b, hipStream_t stream) {
-  for (const auto& [x, e] : {std::pair<const I8GemmArgs&, int>(a, epi_a), std::pair<const I8GemmArgs&, int>(b, epi_b)}) {
-    const hipError_t bad = check_i8(x, e);
-    if (bad != hipSuccess) return bad;
-    if (x.tile_rows != kI8RowsBM) return hipErrorInvalidValue;
-  }
+  const hipError_t bad_a = check_i8(a, epi_a), bad_b = check_i8(b, epi_b);
+  if (bad_a != hipSuccess) return bad_a;
+  if (bad_b != hipSuccess) return bad_b;
+  if (a.tile_rows != kI8RowsBM || b.tile_rows != kI8RowsBM) return hipErrorInvalidValue;
   if (epi_a == kEpiSwiGLU && epi_b == kEpiSwiGLU) return pick_rows<kEpiSwiGLU, kEpiSwiGLU>(a, &b, stream);
   if (epi_a == kEpiBF16 && epi_b == kEpiF32) return pick_rows<kEpiBF16, kEpiF32>(a, &b, stream);
   return hipErrorInvalidValue;

@@ -554,7 +554,8 @@ I8Ffn routed_ffn_i8(const moe_shape* shape, const moe_weights* w, const int32_t*
   u.queue = at<int32_t>(ws, L.queues) + m * moe::kTileQueues * moe::kQueueInts;
   u.max_tiles = L.max_tiles;
   u.tile_rows = L.routed_bm;
-  f.h = quant_args(h32, I, at<int8_t>(ws, L.h), at<float>(ws, L.h_s), expert_offsets + shape->experts_per_rank, p_begin);
+  f.h = quant_args(h32, I, at<int8_t>(ws, L.h), at<float>(ws, L.h_s), expert_offsets + shape->experts_per_rank,
+                   p_begin);
   f.h_rows = rows;
   moe::I8GemmArgs& d = f.down;
   d = u;

@@ -76,9 +76,11 @@ hipError_t launch_quantize_rows_i8(const QuantI8Args& a, bool src_f32, int64_t r
       part.scale += at;
     }
     const int n = static_cast<int>(rows - at < kLaunchRows ? rows - at : kLaunchRows);
-    const hipError_t e = src_f32 ? (vec ? run_rows<true, float>(part, n, stream) : run_rows<false, float>(part, n, stream))
-                                 : (vec ? run_rows<true, uint16_t>(part, n, stream)
-                                        : run_rows<false, uint16_t>(part, n, stream));
+    hipError_t e;
+    if (src_f32)
+      e = vec ? run_rows<true, float>(part, n, stream) : run_rows<false, float>(part, n, stream);
+    else
+      e = vec ? run_rows<true, uint16_t>(part, n, stream) : run_rows<false, uint16_t>(part, n, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -104,7 +104,8 @@ __device__ __forceinline__ void partner32(uint32_t x, uint32_t& a, uint32_t& b) 
   constexpr int kDpp[4] = {0xB1, 0x4E, 0x141, 0x140};
   if constexpr (STEP < 4) {
     a = x;
-    b = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kDpp[STEP < 4 ? STEP : 0], 0xF, 0xF, false));
+    constexpr int kCtrl = kDpp[STEP < 4 ? STEP : 0];
+    b = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kCtrl, 0xF, 0xF, false));
   } else if constexpr (STEP == 4) {
     const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
     a = r[0];
@@ -284,7 +285,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
     for (int q = 0; q < EPL / 4; ++q) {
       const int e = expert_of<LPT, EPL>(j, 4 * q);
       if constexpr (VEC) {
-        if (e < E) *reinterpret_cast<f32x4_t*>(logits + row + e) = f32x4_t{l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]};
+        const f32x4_t v = {l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]};
+        if (e < E) *reinterpret_cast<f32x4_t*>(logits + row + e) = v;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
