@@ -422,7 +422,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
   // (the draw for the item after this one is on its way ahead of the loads)
   if (queued && threadIdx.x == 0) drawn = draw(args.queue, xcd);
   begin(item, 0);
-  int stores = 0;  // of the last epilogue, at least
+  int stores = 0;  // issued by the last epilogue, at least
   for (int turn = 0;; ++turn) {
     // 32-row blocks of this wave that hold tile rows (wave-uniform)
     int fm_live = ((nrows + 31) / 32 - wm + WM - 1) / WM;
@@ -471,6 +471,10 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
     const int lane = item_thread_index(wave) & (kWave - 1);
     const Tables& t = tables[buf];
     const bool whole = EPI != kEpiBF16 || (args.N % 8 == 0 && args.ldc % 8 == 0);
+    // A store that no lane has a row for (past the tile's last one, or with a
+    // table's row out of range) is branched round, so each is counted where it is
+    // issued: the next item's waits may let this many operations be outstanding
+    // behind its loads, and one too many would pass before a load has landed.
     stores = 0;
     float sb[NB][FN];
 #pragma unroll
@@ -484,8 +488,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
       for (int r4 = 0; r4 < 4; ++r4) {
         const int row0 = tile_row<WM>(wm, fm) + r4 * 8;
         if (row0 >= rows) continue;  // wave-uniform
-        // every store of the piece has a lane to issue it for: its first row is in the tile
-        if (whole && col0 + WTN <= args.N) stores += PIECE_STORES;
         const f32x4_t s = *reinterpret_cast<const f32x4_t*>(&t.row_scale[row0 + (lane >> 5) * 4]);
         if constexpr (EPI == kEpiBF16) {
           char* piece = smem + RING + 2 * sizeof(Tables) + wave * PIECE;
@@ -502,7 +504,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
             const int q = it * 64 + lane, row = q / CPR % 8, ch = q % CPR;
             const int col = col0 + ch * 8, out = t.row_out[row0 + row];
             const u32x4_t v = *reinterpret_cast<const u32x4_t*>(piece + row * PS + ch * 16);
-            if (q >= 8 * CPR || out < 0 || col >= args.N) continue;
+            const bool live = q < 8 * CPR && out >= 0 && col < args.N;
+            stores += __ballot(live) ? 1 : 0;
+            if (!live) continue;
             uint16_t* c = static_cast<uint16_t*>(args.C) + static_cast<int64_t>(out) * args.ldc + col;
             if (whole) {
               // next read long after they leave the caches
@@ -519,7 +523,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
           const int outs[4] = {out.x, out.y, out.z, out.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (outs[i] < 0) continue;
+            const bool live = outs[i] >= 0;
+            stores += __ballot(live) ? FN : 0;
+            if (!live) continue;
             float* c = static_cast<float*>(args.C) + static_cast<int64_t>(outs[i]) * args.ldc + col0 + (lane & 31);
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn) {
@@ -533,6 +539,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_i8_kernel(const I8GemmArgs 
       }
     }
     if (!more) break;
+    if (!whole || col0 + WTN > args.N) stores = 0;  // other stores than those counted
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still target LDS when the workgroup ends
 }

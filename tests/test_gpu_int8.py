@@ -103,6 +103,29 @@ def test_matmul_int8(M, N, K, dtype):
     assert torch.equal(got, reference(q, s, w, ws, dtype))
 
 
+# Resident workgroups that walk on from a tile whose last rows do not fill an 8-row piece of the output: more
+# items than workgroups, in tiles of 256 rows (the first seven) and of 320, last tiles of 1 to 5 rows mod 8.
+HANDOVERS = [(2905, 7168, 128), (2969, 7168, 128), (2970, 7168, 512), (2972, 7168, 128), (3002, 7168, 256),
+             (5276, 4096, 128), (8187, 4096, 128), (4609, 7168, 128), (4610, 7168, 384), (8195, 4096, 256),
+             (4605, 7168, 128)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", HANDOVERS, ids=lambda v: str(v))
+def test_matmul_int8_of_ragged_tiles_between_others(M, N, K, dtype):
+    dev = need_gpu()
+    say("matmul_int8 handover", M, N, K, dtype)
+    gen = torch.Generator().manual_seed(M + K)
+    q = torch.randint(-127, 128, (M, K), generator=gen, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=gen, dtype=torch.int8)
+    s, ws = torch.rand(M, generator=gen), torch.rand(N, generator=gen) - 0.5
+    args = [t.to(dev) for t in (q, s, w, ws)]
+    # sums below 2^24 (K <= 512): an fp32 product of the integers is exact
+    want = ((args[0].float() @ args[2].float().T) * args[1][:, None] * args[3][None, :]).to(dtype)
+    for rep in range(3):
+        assert torch.equal(matmul_int8(*args, out_dtype=dtype), want), rep
+
+
 def test_matmul_int8_writes_only_its_rows():
     # a result inside a larger buffer of the allocator stays inside it: rows past M keep their bytes
     dev = need_gpu()
@@ -272,6 +295,79 @@ def test_int8_mid_layer_is_the_same_for_every_tile_height_and_on_every_run():
         torch.cuda.synchronize()
         want = got if want is None else want
         assert torch.equal(got, want), b
+
+
+@pytest.mark.parametrize("D,I,E,per", [
+    # 320-, 192-, 128- and 64-row tiles of the routed products, several items a workgroup
+    (2048, 1152, 96, 196), (2048, 2048, 64, 145), (2048, 1408, 64, 101), (2048, 1152, 128, 21)])
+def test_int8_layer_of_ragged_experts(D, I, E, per):
+    # experts of per + 1, per + 2, ... per + 8 rows in turn, so that tiles end in every count of rows mod 8: the bits
+    # of minibatches that take the few-rows kernel
+    dev = need_gpu()
+    say("int8 ragged experts", D, I, E, per)
+    ids = torch.repeat_interleave(torch.arange(E), torch.tensor([per + 1 + e % 8 for e in range(E)]))
+    T = len(ids)
+    w, x, _, gate = random_layer(dev, T, D, I, E, 1, 23)
+    ids = ids[torch.randperm(T, generator=torch.Generator().manual_seed(T))]
+    idx = ids.to(torch.int32).view(T, 1).to(dev)
+    kw = dict(precision="int8", shared_precision="int8")
+    small = MoELayer(shape_for(T, D, I, E, 1, minibatch_rows=4 * E, **kw), device=dev)
+    small.forward(w, x, x, gate, small.schedule(idx))
+    want = small.routed_rows().clone()
+    m = MoELayer(shape_for(T, D, I, E, 1, **kw), device=dev)
+    for rep in range(3):
+        m.routed_rows().zero_()
+        m.forward(w, x, x, gate, m.schedule(idx))
+        assert torch.equal(m.routed_rows(), want), rep
+    assert m.device_error() == 0
+
+
+def test_int8_layer_with_rows_that_the_table_drops():
+    # a table of the caller's own, with entries outside the routes: those rows write nothing, the others keep their bits
+    dev = need_gpu()
+    D, I, E, T = 2048, 1152, 96, 19248
+    say("int8 dropped rows", D, I, E)
+    w, x, _, gate = random_layer(dev, T, D, I, E, 1, 37)
+    idx = (torch.arange(T, device=dev) % E).to(torch.int32).view(T, 1)
+    m = MoELayer(shape_for(T, D, I, E, 1, precision="int8", shared_precision="int8"), device=dev)
+    sched = m.schedule(idx)
+    m.forward(w, x, x, gate, sched)
+    want = m.routed_rows().clone()
+    p = torch.arange(T, device=dev)
+    drop = (p % 24 >= 8) | (p % 7 == 3)
+    routes = sched["sched"][drop].long()
+    sched["sched"][drop] = torch.where(p[drop] % 2 == 0, -1, T + 5).to(torch.int32)
+    want[routes] = -3.0
+    for rep in range(3):
+        m.routed_rows().fill_(-3.0)
+        m.forward(w, x, x, gate, sched)
+        assert torch.equal(m.routed_rows(), want), rep
+
+
+@pytest.mark.parametrize("T,I_shared", [(2561, 4096), (2570, 4096), (5123, 2048), (4098, 4096), (4107, 4096)])
+def test_int8_shared_expert_of_ragged_tiles(T, I_shared):
+    # 256- and 320-row SwiGLU tiles, several items a workgroup: the bits of 32 tokens at a time
+    dev = need_gpu()
+    say("int8 shared ragged", T, I_shared)
+    D = 128
+    gen = torch.Generator(device=dev).manual_seed(T)
+    w, x, idx, gate = random_layer(dev, T, D, 128, 2, 1, 29)
+    for n, (a, b) in (("gate", (I_shared, D)), ("up", (I_shared, D)), ("down", (D, I_shared))):
+        w["qs_" + n] = torch.randint(-60, 61, (a, b), dtype=torch.int8, device=dev, generator=gen)
+        w["ss_" + n] = 1e-3 * torch.rand(a, device=dev, generator=gen)
+    gate = torch.zeros_like(gate)  # the routed part adds nothing
+    kw = dict(I_shared=I_shared, precision="int8", shared_precision="int8")
+    few = MoELayer(shape_for(32, D, 128, 2, 1, **kw), device=dev)
+    want = []
+    for t in range(0, T, 32):
+        rows = torch.arange(t, t + 32, device=dev).clamp(max=T - 1)
+        xs, ids, gs = x[rows], idx[rows], gate[rows]
+        want.append(few.forward(w, xs, xs, gs, few.schedule(ids))[1])
+    want = torch.cat(want)[:T]
+    m = MoELayer(shape_for(T, D, 128, 2, 1, **kw), device=dev)
+    for rep in range(3):
+        assert torch.equal(m.forward(w, x, x, gate, m.schedule(idx))[1], want), rep
+    assert m.device_error() == 0
 
 
 @pytest.mark.parametrize("hot", ["one", "two", "most"])
