@@ -530,7 +530,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const
   // the softmax's own mean, sum_s s_s dw_s: zero for renormalised gates
   const double mean = dense ? lanes_sum<LPT>(s * dw) : 0.0;
   __syncthreads();
-  if (id >= 0) atomicAdd(&dw_s[tok_b][id], dense ? dw : r.sigmoid ? s * (1.0 - s) * dw : s * dw);
+  // (1 - s as a score of its own: from l of about 20 the difference is worth less than an fp32 step)
+  if (id >= 0) atomicAdd(&dw_s[tok_b][id], dense ? dw : r.sigmoid ? s * sigmoid64(-lj) * dw : s * dw);
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < EPL / 4; ++q) {

@@ -69,5 +69,5 @@ def backward(logits: np.ndarray, idx: np.ndarray, dgate: np.ndarray, kind: str, 
     ds = np.zeros_like(s)
     np.put_along_axis(ds, idx, dw, axis=1)
     if kind == "sigmoid":
-        return ds * s * (1.0 - s)
+        return ds * s * scores(-np.asarray(logits, dtype=np.float64), kind)  # 1 - s without its cancellation
     return s * (ds - (ds * s).sum(axis=1, keepdims=True))

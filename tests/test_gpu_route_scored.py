@@ -208,6 +208,29 @@ def test_gradient_of_a_single_renormalised_gate_is_zero(kind):
         assert not m.route_backward(lg, idx, dg, router=r).any()
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_saturated_sigmoids(renorm):
+    # 1 - s of a score next to 1 is what the gradient is made of: right relative to itself, out to the fp32 range
+    dev = need_gpu()
+    say("saturated sigmoids", renorm)
+    rng = np.random.default_rng(8)
+    for T, E, k in ((40, 64, 6), (2100, 256, 8)):
+        logits = rng.uniform(20.0, 60.0, (T, E)).astype(np.float32)
+        logits[1::3] *= -1.0
+        logits[2::3, ::2] *= -1.0
+        m, r, lg, idx, _ = run(dev, logits, k, score="sigmoid", renorm=renorm, scale=2.5)
+        dg = rng.standard_normal((T, k)).astype(np.float32)
+        got = m.route_backward(lg, idx, torch.from_numpy(dg).to(dev), router=r).cpu().numpy().astype(np.float64)
+        ids = idx.cpu().numpy()
+        want = scored.backward(logits, ids, dg, "sigmoid", renorm, 2.5)
+        # half an fp32 step, and 1e-12 of the terms that cancel in dg_s - mean, each times scale s (1 - s) / W
+        s = scored.scores(logits, "sigmoid")
+        W = np.take_along_axis(s, ids.astype(np.int64), axis=1).sum(1, keepdims=True) if renorm else 1.0
+        unit = 2.5 * s * scored.scores(-logits, "sigmoid") / W
+        tol = U * np.abs(want) + 1e-12 * unit * np.abs(dg).max(1, keepdims=True)
+        assert np.all(np.abs(got - want) <= tol)
+
+
 def test_routing_from_x_scores_the_same_logits():
     # the router projection with K ranges: the choice equals the oracle's of the logits that come back
     dev = need_gpu()

@@ -3,6 +3,7 @@ on the CPU: the oracle against torch's double autograd and differences, and the
 host-side checks of the entry points."""
 
 import ctypes
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -35,6 +36,20 @@ def test_oracle_gradient(kind, renorm):
         up[t_, e] += h
         dn[t_, e] -= h
         assert abs((loss(up) - loss(dn)) / (2 * h) - got[t_, e]) < 1e-8
+
+
+def test_oracle_gradient_of_saturated_sigmoids():
+    # s (1 - s) = exp(-|l|) / (1 + exp(-|l|))^2 to full precision, against 40 decimal digits
+    l = np.array([[-60.0, -37.5, -8.0, 0.25, 20.0, 30.0, 37.5, 60.0]])
+    idx, dg = np.arange(8, dtype=np.int32)[None], np.linspace(-1.0, 2.0, 8)[None]
+    got = scored.backward(l, idx, dg, "sigmoid", False, 2.5)
+    with localcontext() as c:
+        c.prec = 40
+        for e in range(8):
+            z = (-abs(Decimal(l[0, e]))).exp()
+            want = Decimal(2.5) * Decimal(dg[0, e]) * z / (1 + z) ** 2
+            # two logistic functions and three products, a few 2^-53 each, exp's argument exact
+            assert abs(Decimal(got[0, e]) - want) <= Decimal(1e-15) * 2 * abs(want), e
 
 
 def test_oracle_choice_by_hand():
