@@ -203,8 +203,11 @@ moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router
  * largest (MOE_GROUP_TOP2; a group of one expert by that one), and the
  * kept_groups best stay, ties to the lower group.  Of their experts the k
  * largest c are chosen, in falling order.  The gates are
- *   g_s = scale * s_s / sum_s' s_s'      renorm = 1 (0 where the sum is 0)
+ *   g_s = scale * s_s / sum_s' s_s'      renorm = 1
  *   g_s = scale * s_s                    renorm = 0
+ * Renormalised gates are formed from the chosen logits' differences where the
+ * scores themselves would vanish (finite masks that a bias chose): they are 0
+ * only where every chosen logit is -inf or NaN.
  * The bias only chooses; it never enters a gate.  Scores are formed in 64
  * bits, and two c are told apart down to 2^-42 of their value: closer ones tie,
  * to the lower expert id.  (Without a bias, and unless groups rank by two
@@ -238,7 +241,7 @@ moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, co
  *   dgate     [T, k] fp32: the gradient of the gates
  *   dlogits   [T, E_total] fp32 out, every entry written
  * With W = sum_s s_s over the chosen:
- *   dw_s = scale (dg_s - sum_s' dg_s' s_s' / W) / W    renorm = 1 (0 where W is 0)
+ *   dw_s = scale (dg_s - sum_s' dg_s' s_s' / W) / W    renorm = 1 (as there)
  *   dw_s = scale dg_s                                  renorm = 0
  *   dl_e = s_e (1 - s_e) dw_e                          sigmoid (0 unless chosen)
  *   dl_e = s_e (dw_e - sum_s s_s dw_s)                 softmax (dw_e = 0 unless chosen)

@@ -74,11 +74,19 @@ __device__ __forceinline__ double sigmoid64(float l) {
   return l == -INFINITY ? 0.0 : s;
 }
 
-// exp(l - m) for l <= m; 0 where it is below exp(-700).
+// exp(l - m) for l <= m; 0 where it is below exp(-700), and for l = -inf.
 __device__ __forceinline__ double exp_below(float l, float m) {
   const double d = static_cast<double>(l) - static_cast<double>(m);
   const double e = exp64(d > -700.0 ? d : -700.0);  // no branch: neighbours' chains interleave
   return d > -700.0 ? e : 0.0;
+}
+
+// A chosen expert's score for renormalised gates, which depend on the ratios of
+// the chosen scores alone: `top` is the largest of the chosen logits, and where
+// the scores lie far below fp64's range (masked experts that a bias chose) this
+// is their multiple exp(l - top).  Below -500 a sigmoid is exp(l) to 1e-217.
+__device__ __forceinline__ double chosen_score(bool sigmoid, float l, float top) {
+  return sigmoid && top >= -500.f ? sigmoid64(l) : exp_below(l, top);
 }
 
 // Maximum and minimum of two candidates (never NaN).  As instructions of their
@@ -316,16 +324,14 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
   float m = 0.f;
   double inv = 1.0;  // softmax: 1 / sum (renormalised gates do not need it)
   const bool by_logit = !bias && (r.kept_groups == r.groups || !r.top2 || r.group_size == 1);
-  if (!r.sigmoid) {
-    m = l[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
-    m = lanes_max<LPT>(m);
-  }
   if (r.sigmoid && !by_logit) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) c[i] = sigmoid64(l[i]);
   } else if (!r.sigmoid && !(by_logit && r.renorm)) {
+    m = l[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, l[i]);
+    m = lanes_max<LPT>(m);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -454,12 +460,14 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouterArgs r, const f
   for (int i = 1; i < K; ++i) mine = j == i ? best[i] : mine;
   const int my_id = candidate_id(mine);
   __syncthreads();  // l_s is whole
-  const float my_l = l_s[tok_b][j < k ? my_id : 0];
-  double w = 0.0;
-  if (j < k) w = r.sigmoid ? sigmoid64(my_l) : (my_l == -INFINITY ? 0.0 : exp_below(my_l, m) * inv);
+  const float my_l = j < k ? l_s[tok_b][my_id] : -INFINITY;
+  double w;
   if (r.renorm) {
+    w = chosen_score(r.sigmoid, my_l, lanes_max<LPT>(my_l));
     const double W = lanes_sum<LPT>(w);
     w = W > 0.0 ? w / W : 0.0;
+  } else {
+    w = r.sigmoid ? sigmoid64(my_l) : exp_below(my_l, m) * inv;
   }
   if (live && j < k) {
     idx[static_cast<int64_t>(token) * k + j] = my_id;
@@ -494,11 +502,12 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const
   // the whole row; renormalised ones only their ratios among the chosen
   const bool dense = !r.sigmoid && !r.renorm;
   double z[EPL];
-  float m = lj;
+  float m = 0.f;
   double inv = 1.0;
   if (dense) {
     float l[EPL];
     load_row<LPT, EPL, VEC>(logits + row, j, E, -INFINITY, l);
+    m = lj;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       l[i] = clean_logit(l[i]);
@@ -513,19 +522,19 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouterArgs r, const
     }
     sum = lanes_sum<LPT>(sum);
     inv = sum > 0.0 ? recip64(sum) : 0.0;
-  } else if (!r.sigmoid) {
-    m = lanes_max<LPT>(m);
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) dw_s[tok_b][expert_of<LPT, EPL>(j, i)] = 0.0;
-  double s = 0.0;
-  if (id >= 0) s = r.sigmoid ? sigmoid64(lj) : (lj == -INFINITY ? 0.0 : exp_below(lj, m) * inv);
+  double s;  // 0 for a lane without an expert (lj is -inf there)
   double dw = dg * r.scale;
   if (r.renorm) {
+    s = chosen_score(r.sigmoid, lj, lanes_max<LPT>(lj));
     const double W = lanes_sum<LPT>(s);
     const double mean = W > 0.0 ? lanes_sum<LPT>(dw * s) / W : 0.0;
     // (a single expert's gate is `scale` whatever its score: no rounding left over)
     dw = W > 0.0 && k > 1 ? (dw - mean) / W : 0.0;
+  } else {
+    s = r.sigmoid ? sigmoid64(lj) : exp_below(lj, m) * inv;
   }
   // the softmax's own mean, sum_s s_s dw_s: zero for renormalised gates
   const double mean = dense ? lanes_sum<LPT>(s * dw) : 0.0;

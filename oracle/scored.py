@@ -7,7 +7,7 @@
     g_s = scale s_s / sum s   (renormalised), or scale s_s
 
 The bias only chooses.  A logit of -inf scores 0; a renormalised gate is 0
-where the chosen scores sum to 0.
+where every chosen logit is -inf.
 """
 
 from __future__ import annotations
@@ -55,19 +55,31 @@ def gates(s: np.ndarray, idx: np.ndarray, renorm: bool, scale: float) -> np.ndar
     return scale * w
 
 
+def ratios(logits: np.ndarray, idx: np.ndarray, kind: str) -> np.ndarray:
+    """s_s / sum s over the chosen, from the scores' logarithms: also where the
+    scores themselves are below the range of fp64."""
+    l = np.take_along_axis(np.asarray(logits, dtype=np.float64), idx.astype(np.int64), axis=1)
+    if kind == "sigmoid":
+        l = -np.logaddexp(0.0, -l)
+    m = l.max(axis=1, keepdims=True)
+    z = np.exp(l - np.where(np.isneginf(m), 0.0, m))
+    W = z.sum(axis=1, keepdims=True)
+    return np.divide(z, W, out=np.zeros_like(z), where=W > 0)
+
+
 def backward(logits: np.ndarray, idx: np.ndarray, dgate: np.ndarray, kind: str, renorm: bool,
              scale: float) -> np.ndarray:
     """dlogits [T, E] of sum(gates * dgate), the choice held fixed."""
+    logits = np.asarray(logits, dtype=np.float64)
     s = scores(logits, kind)
     idx = idx.astype(np.int64)
-    w = np.take_along_axis(s, idx, axis=1)
     dw = scale * np.asarray(dgate, dtype=np.float64)
-    if renorm:
-        W = w.sum(axis=1, keepdims=True)
-        inv = np.divide(1.0, W, out=np.zeros_like(W), where=W > 0)
-        dw = (dw - (dw * w).sum(axis=1, keepdims=True) * inv) * inv
     ds = np.zeros_like(s)
+    if renorm:
+        p = ratios(logits, idx, kind)
+        np.put_along_axis(ds, idx, p * (dw - (dw * p).sum(axis=1, keepdims=True)), axis=1)
+        return ds * scores(-logits, kind) if kind == "sigmoid" else ds
     np.put_along_axis(ds, idx, dw, axis=1)
     if kind == "sigmoid":
-        return ds * s * scores(-np.asarray(logits, dtype=np.float64), kind)  # 1 - s without its cancellation
+        return ds * s * scores(-logits, kind)  # 1 - s without its cancellation
     return s * (ds - (ds * s).sum(axis=1, keepdims=True))

@@ -231,6 +231,32 @@ def test_gradient_of_saturated_sigmoids(renorm):
         assert np.all(np.abs(got - want) <= tol)
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", [(40, 64, 5), (2100, 256, 8), (1100, 300, 12)])
+def test_renormalised_gates_of_logits_far_below_the_others(kind, T, E, k):
+    # a bias that chooses masked experts (finite masks, and the type's lowest value): the gates depend on the chosen
+    # logits' differences alone, forward and backward
+    dev = need_gpu()
+    say("far below", kind, T, E, k)
+    rng = np.random.default_rng(E)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    chosen = rng.permutation(E)[:k]
+    bias = np.zeros(E, dtype=np.float32)
+    bias[chosen] = 10.0 + np.arange(k)[::-1]  # in this order, whatever the scores
+    depth = np.array([-1e4, -499.0, -501.0, -650.0, -699.0, -720.0, -3e5, 0.0])
+    logits[:, chosen] += depth[np.arange(T) % 8][:, None].astype(np.float32)
+    logits[::16, chosen] = torch.finfo(torch.float32).min
+    logits[5::16, chosen[1:]] -= 5e3  # one of them far above the rest
+    m, r, lg, idx, gate = run(dev, logits, k, bias, score=kind, scale=2.5)
+    ids = idx.cpu().numpy()
+    assert np.array_equal(ids, np.tile(chosen, (T, 1))) and m.device_error() == 0
+    assert close(gate.cpu().numpy(), 2.5 * scored.ratios(logits, ids, kind))
+    assert np.allclose(gate.double().sum(1).cpu().numpy(), 2.5, rtol=k * U, atol=0)
+    dg = rng.standard_normal((T, k)).astype(np.float32)
+    got = m.route_backward(lg, idx, torch.from_numpy(dg).to(dev), router=r).cpu().numpy()
+    assert close(got, scored.backward(logits, ids, dg, kind, True, 2.5), dg, 2.5)
+
+
 def test_routing_from_x_scores_the_same_logits():
     # the router projection with K ranges: the choice equals the oracle's of the logits that come back
     dev = need_gpu()

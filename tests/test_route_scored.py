@@ -52,6 +52,24 @@ def test_oracle_gradient_of_saturated_sigmoids():
             assert abs(Decimal(got[0, e]) - want) <= Decimal(1e-15) * 2 * abs(want), e
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_oracle_ratios_far_below_the_maximum(kind):
+    # two chosen logits one apart: e / (1 + e) and 1 / (1 + e) wherever they lie below 0
+    l = np.array([[3.0, -1e4, -10001.0], [3.0, -600.0, -601.0], [0.0, -800.0, -np.inf], [0.0, -np.inf, -np.inf]])
+    idx = np.tile(np.array([[1, 2]], dtype=np.int32), (4, 1))
+    a = np.e / (1.0 + np.e)
+    want = np.array([[a, 1 - a], [a, 1 - a], [1, 0], [0, 0]])
+    assert np.abs(scored.ratios(l, idx, kind) - want).max() < 1e-12
+    got = scored.backward(l, idx, np.array([[1.0, 3.0]] * 4), kind, True, 2.0)
+    # scale p (dg - p . dg): the differences of the two are -2 p_1 and 2 p_0
+    dl = 2.0 * a * (1 - a) * 2.0
+    assert np.abs(got - np.array([[0, -dl, dl]] * 2 + [[0, 0, 0]] * 2)).max() < 1e-12
+    near = np.random.default_rng(1).standard_normal((5, 9))
+    ids = scored.choose(scored.scores(near, kind), None, 4)
+    gates = scored.gates(scored.scores(near, kind), ids, True, 1.0)
+    assert np.abs(scored.ratios(near, ids, kind) - gates).max() < 1e-14
+
+
 def test_oracle_choice_by_hand():
     s = np.array([[0.9, 0.1, 0.5, 0.45, 0.8, 0.05]])
     # pairs (0.9 0.1) (0.5 0.45) (0.8 0.05): sums 1.0, 0.95, 0.85; maxima 0.9, 0.5, 0.8
