@@ -37,6 +37,9 @@
  *     C*D*e; h: b*I*e; the shared h: T*I_shared*e; one routed or the shared
  *     weight matrix: I*D*e, I_shared*D*e; e = 2 in bf16, 1 in MXFP8 and int8);
  *     larger shapes return MOE_ERR_UNSUPPORTED.
+ *   - Routing, scheduling and forward calls for no tokens (T == 0) return
+ *     MOE_OK and write no row; the pointers to their rows may then be NULL,
+ *     those to weights and expert tables may not.
  *   - Data errors found on the device (an expert id out of range, more routed
  *     rows than `max_rows`, a non-finite router logit) set bits of a sticky
  *     word in the workspace and never cause an out-of-bounds access; read it

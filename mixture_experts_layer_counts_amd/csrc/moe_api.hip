@@ -722,8 +722,9 @@ moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router
   Layout L;
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
+  if (x && !w_router) return MOE_ERR_INVALID_ARG;
   if (shape->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
-  if (!logits || !topk_idx || !topk_gate || (x && !w_router)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !topk_gate) return MOE_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
   if (x) MOE_TRY_HIP(router_gemm(shape, x, w_router, logits, L, ws, s));
@@ -741,8 +742,9 @@ moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, co
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
   if (!valid_router(shape, router)) return MOE_ERR_INVALID_ARG;
+  if (x && !w_router) return MOE_ERR_INVALID_ARG;
   if (shape->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
-  if (!logits || !topk_idx || !topk_gate || (x && !w_router)) return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !topk_gate) return MOE_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int T = static_cast<int>(shape->T), E = static_cast<int>(shape->E_total), k = static_cast<int>(shape->k);
   if (x) MOE_TRY_HIP(router_gemm(shape, x, w_router, logits, L, ws, s));
@@ -816,7 +818,6 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
   const bool mx = shape->precision == MOE_MXFP8;
-  if (shape->T == 0 && shape->max_rows == 0) return MOE_OK;  // no rows: their pointers may be NULL
   if (!w || !w->w_gate || !w->w_up || !w->w_down || !w->ws_gate || !w->ws_up || !w->ws_down) return MOE_ERR_INVALID_ARG;
   const bool i8 = shape->precision == MOE_INT8;
   if ((mx || i8) && (!w->s_gate || !w->s_up || !w->s_down)) return MOE_ERR_INVALID_ARG;
@@ -827,7 +828,9 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   };
   if (i8 && !aligned16({w->w_gate, w->w_up, w->w_down})) return MOE_ERR_INVALID_ARG;
   if (shared_i8 && !aligned16({w->ws_gate, w->ws_up, w->ws_down})) return MOE_ERR_INVALID_ARG;
-  if (!expert_offsets || !route_dst || !topk_gate || !out) return MOE_ERR_INVALID_ARG;
+  if (!expert_offsets) return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0 && shape->max_rows == 0) return MOE_OK;  // no rows: their pointers may be NULL
+  if (!route_dst || !topk_gate || !out) return MOE_ERR_INVALID_ARG;
   if (shape->T > 0 && !x_local) return MOE_ERR_INVALID_ARG;
   if (shape->max_rows > 0 && (!x_src || !sched_src)) return MOE_ERR_INVALID_ARG;
   const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -129,3 +129,28 @@ def test_binding_refusals():
         tile_int8(torch.zeros((1, 4, 128), dtype=torch.uint8))
     with pytest.raises(KeyError):
         shape_for(T=1, D=128, I=128, E=4, k=1, precision="int4")
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8", "int8"])
+def test_forward_without_tokens_still_checks_its_weights(lib, precision):  # noqa: F811
+    s = shape_for(T=0, D=128, I=128, E=8, k=2, precision=precision, shared_precision=precision)
+    _, n = ws_bytes(lib, s)
+    w = _lib.MoeWeights()
+    names = [f for f, _ in _lib.MoeWeights._fields_]
+    if precision == "bf16":
+        names = [f for f in names if f.startswith("w")]
+
+    def run(weights=ctypes.byref(w), offsets=FAKE):
+        return lib.moe_forward(ctypes.byref(s), weights, None, None, None, offsets, None, None, None, None, FAKE, n,
+                               None)
+    for f in names:
+        setattr(w, f, 4096)
+    assert run() == 0  # no rows: no pointer to them, no launch
+    assert run(weights=None) == -1 and run(offsets=None) == -1
+    for f in names:
+        setattr(w, f, None)
+        assert run() == -1, f
+        setattr(w, f, 4096)
+    if precision == "int8":
+        w.ws_down = 4104
+        assert run() == -1

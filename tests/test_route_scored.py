@@ -121,6 +121,15 @@ def test_missing_arguments_are_refused(lib):  # noqa: F811
     assert call(lib, empty, r) == 0 and call_backward(lib, empty, r) == 0  # nothing to do: no launch
 
 
+def test_routing_without_tokens_still_checks_its_weights(lib):  # noqa: F811
+    s, r = shape_for(T=0, D=128, I=64, E=32, k=4), router_for()
+    n = ws_bytes(lib, s)[1]
+    assert call(lib, s, r, logits=None, idx=None, gate=None) == 0
+    assert call(lib, s, r, x=FAKE) == -1 and call(lib, s, None) == -1  # x without router weights, no router
+    assert lib.moe_route(ctypes.byref(s), None, None, None, None, None, FAKE, n, None) == 0
+    assert lib.moe_route(ctypes.byref(s), FAKE, None, FAKE, FAKE, FAKE, FAKE, n, None) == -1
+
+
 def test_backward_scored_is_refused_like_backward(lib):  # noqa: F811
     s, r = shape_for(T=64, D=128, I=64, E=32, k=4), router_for()
     n = ctypes.c_size_t(0)
