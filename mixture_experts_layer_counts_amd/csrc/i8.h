@@ -121,20 +121,24 @@ template <int TH, bool VEC, typename T>
 __device__ __forceinline__ void i8_quantize_row(const QuantI8Args& a, int64_t i) {
   int64_t from = i, to = i;
   if (a.limit && a.p_begin + i >= *a.limit) return;  // behind the last routed row
+  const int tid = static_cast<int>(threadIdx.x) % TH;
+  if (a.routes && tid == 0) {
+    const int32_t route = a.routes[a.p_begin + i];
+    if (route < 0 || route >= a.n_routes) raise_error(a.err, kErrExpertRange);  // a table of the caller's own
+  }
   if (a.sched) {
     const int64_t p = a.p_begin + i;
     const int32_t route = a.sched[p];
     from = route / a.k;
     to = p % a.ring_rows;
     if (route < 0 || from >= a.src_rows) {  // a table not built by the schedule kernels
-      if (static_cast<int>(threadIdx.x) % TH == 0) raise_error(a.err, kErrExpertRange);
+      if (tid == 0) raise_error(a.err, kErrExpertRange);
       return;
     }
   }
   const T* __restrict__ src = static_cast<const T*>(a.src) + from * a.K;
   int8_t* __restrict__ q = a.q + to * a.Kp;
   const int64_t chunks = a.Kp / kI8Chunk;
-  const int tid = static_cast<int>(threadIdx.x) % TH;
 
   float v[kI8Held][kI8Chunk];
   uint32_t bits = 0;

@@ -230,7 +230,9 @@ hipError_t launch_gemm_i8_pair(const I8GemmArgs& a, int epi_a, const I8GemmArgs&
 // Rows of bf16 or fp32 [.][K] -> int8 [.][Kp] (zeros past K) and one scale per
 // row.  Row i of the launch goes to row i, or with `sched` schedule position p
 // = p_begin + i reads row sched[p] / k and goes to row p mod ring_rows.  With
-// `limit` (device), positions p_begin + i at or past it are left alone.
+// `limit` (device), positions p_begin + i at or past it are left alone.  With
+// `routes`, the schedule table that the products read their rows through, its
+// entry at p_begin + i has to lie in [0, n_routes).
 struct QuantI8Args {
   const void* src;
   int64_t K, Kp;
@@ -241,6 +243,8 @@ struct QuantI8Args {
   const int32_t* sched;
   int k;
   int64_t src_rows, ring_rows;
+  const int32_t* routes;
+  int64_t n_routes;
   int* err;
 };
 hipError_t launch_quantize_rows_i8(const QuantI8Args& args, bool src_f32, int64_t rows, hipStream_t stream);

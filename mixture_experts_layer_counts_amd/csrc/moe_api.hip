@@ -556,6 +556,11 @@ I8Ffn routed_ffn_i8(const moe_shape* shape, const moe_weights* w, const int32_t*
   u.tile_rows = L.routed_bm;
   f.h = quant_args(h32, I, at<int8_t>(ws, L.h), at<float>(ws, L.h_s), expert_offsets + shape->experts_per_rank,
                    p_begin);
+  if (R == 1) {  // (with several ranks the gather checks the table)
+    f.h.routes = sched_src;
+    f.h.n_routes = shape->T * shape->k;
+    f.h.err = at<int>(ws, L.err);
+  }
   f.h_rows = rows;
   moe::I8GemmArgs& d = f.down;
   d = u;

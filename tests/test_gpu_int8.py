@@ -344,6 +344,25 @@ def test_int8_layer_with_rows_that_the_table_drops():
         assert torch.equal(m.routed_rows(), want), rep
 
 
+@pytest.mark.parametrize("T,b", [(2, None), (40, None), (300, None), (300, 128)])
+def test_int8_layer_flags_a_table_with_entries_out_of_range(T, b):
+    # as the bf16 and MXFP8 layers do: no route is dropped without the error bit
+    dev = need_gpu()
+    say("int8 bad table", T, b)
+    w = synth.Workload("table", T=T, D=256, I=128, E=8, k=2, I_shared=128, seed=41, routing="gaussian")
+    inp = synth.make_inputs(w)
+    x, wd = inp["x"].to(dev), quantised(inp, dev)
+    for bad in (-1, T * w.k):
+        m = make(w, dev, b=b)
+        _, idx, gate = m.route(None, None, inp["logits"].to(dev))
+        sched = m.schedule(idx)
+        m.forward(wd, x, x, gate, sched)
+        assert m.device_error() == 0
+        sched["sched"][T * w.k - 1] = bad
+        m.forward(wd, x, x, gate, sched)
+        assert m.device_error() == 0x1, bad
+
+
 @pytest.mark.parametrize("T,I_shared", [(2561, 4096), (2570, 4096), (5123, 2048), (4098, 4096), (4107, 4096)])
 def test_int8_shared_expert_of_ragged_tiles(T, I_shared):
     # 256- and 320-row SwiGLU tiles, several items a workgroup: the bits of 32 tokens at a time
