@@ -21,12 +21,18 @@
 // routes, and fp32.
 //
 // A workgroup's next item begins under its epilogue: the first loads are issued
-// before the stores, so they need not wait for them, and the stores drain under
-// the next K loop's first stages (the waits count them).  That took the down
-// product of the 7168 x 2048 layer at 8192 tokens from 1.36 to 1.30 ms, an 8192
-// x 7168 x 2048 product from 140 to 134 us, and the 2048 x 768 layer of 128
-// experts at 8192 tokens from 737 to 694 us; the one workgroup on a CU
-// otherwise wrote 160 KB with no load in flight.
+// before the stores, and the next K loop's first waits count the stores behind
+// them.  In the bf16 kernels these drain under that loop's first stages, which
+// took the down product of the 7168 x 2048 layer at 8192 tokens from 1.36 to
+// 1.30 ms and an 8192 x 7168 x 2048 product from 140 to 134 us; the one
+// workgroup on a CU otherwise wrote 160 KB with no load in flight.  In the fp32
+// and SwiGLU kernels the loads are only issued early: before each 8-row piece
+// the compiler waits for every memory operation (it takes the LDS that the
+// direct loads write for what the piece reads of row_out), so the loads have
+// landed and the stores have drained before the K loop begins.
+//
+// The 320-row kernels spill 8 to 11 vector registers (36 to 48 bytes of scratch
+// a lane); the others spill none.
 
 #include <algorithm>
 #include <atomic>

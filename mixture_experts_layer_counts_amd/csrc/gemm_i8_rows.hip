@@ -305,9 +305,10 @@ hipError_t run_rows(const I8GemmArgs& a, const I8GemmArgs* b, hipStream_t stream
 
 // Columns per workgroup and waves per workgroup.  A CU streams some 40 GB/s, so
 // while there are at most a CU's worth of 16-column blocks the finest split is
-// the fastest, with the K axis over eight waves (1 x 2048 x 7168: 8.8 us, 12.1
-// with four waves, 13.8 with 32 columns); past that wider blocks read the
-// activations less often (64 x 7168 x 2048: 11.4 us with 64 columns, 15.3 with
+// the fastest, with the K axis over eight waves (the product alone of
+// 1 x 2048 x 7168, as moe_matmul_int8 runs it: 8.4 us, 12.1 with four waves, 13.8
+// with 32 columns); past that wider blocks read the
+// activations less often (64 x 7168 x 2048: 11.1 us with 64 columns, 15.3 with
 // 16).  SwiGLU blocks hold gate and up columns and stay at 16 (the layer of
 // 7168 x 2048 and 256 experts at one token: 96 us, 103 with 32; at 64 tokens
 // 1.63 ms and 1.64); four waves do there once the blocks fill the chip (99 us
