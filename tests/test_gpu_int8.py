@@ -104,7 +104,7 @@ def test_matmul_int8(M, N, K, dtype):
 
 
 # Resident workgroups that walk on from a tile whose last rows do not fill an 8-row piece of the output: more
-# items than workgroups, in tiles of 256 rows (the first seven) and of 320, last tiles of 1 to 5 rows mod 8.
+# items than workgroups, in tiles of 256 rows (the first seven and the last) and of 320, which end in 1 to 5 rows mod 8.
 HANDOVERS = [(2905, 7168, 128), (2969, 7168, 128), (2970, 7168, 512), (2972, 7168, 128), (3002, 7168, 256),
              (5276, 4096, 128), (8187, 4096, 128), (4609, 7168, 128), (4610, 7168, 384), (8195, 4096, 256),
              (4605, 7168, 128)]
