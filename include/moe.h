@@ -59,7 +59,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 9
+#define MOE_ABI_VERSION 10
 
 typedef enum {
   MOE_OK = 0,
@@ -173,7 +173,8 @@ typedef struct {
  * Returns MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED for a bad shape. */
 moe_status moe_workspace_bytes(const moe_shape* shape, size_t* bytes);
 
-/* Clear the workspace's sticky error word (one small kernel on `stream`). */
+/* Clear the workspace's sticky error word and, for shapes moe_few serves, its
+ * counters (small kernels on `stream`). */
 moe_status moe_workspace_init(const moe_shape* shape, void* ws, size_t ws_bytes, void* stream);
 
 /*
@@ -331,6 +332,44 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* weights, const
                        const void* x_local, const float* topk_gate, const int32_t* expert_offsets,
                        const int32_t* sched_src, const int32_t* route_dst, void* out, float* out32,
                        void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The whole layer for a few tokens, T <= MOE_FEW_TOKENS, in one launch: what
+ * moe_route (or, with a router, moe_route_scored), moe_schedule and moe_forward
+ * compute, as a step of serving runs it.
+ *
+ *   router     as in moe_route_scored; NULL: softmax scores, no groups, gates
+ *              renormalised (moe_route's, formed as moe_route_scored forms them)
+ *   bias       [E_total] fp32 or NULL; needs a router
+ *   x          [T, D] bf16
+ *   w_router   [E_total, D] bf16, or NULL: then `logits` is an INPUT
+ *   logits     [T, E_total] fp32 out (or in)
+ *   topk_idx, topk_gate   [T, k] out, as in moe_route_scored
+ *   out        [T, D] bf16 out: RNE of out32
+ *   out32      [T, D] fp32 out, or NULL
+ *   ws         the layer's workspace; moe_workspace_init must have run on it
+ *              once (it clears the counters, which every call leaves cleared)
+ * One GPU (num_src_ranks == 1); MOE_BF16 or MOE_MXFP8 experts, row-major or
+ * K-tiled (MOE_INT8, T > MOE_FEW_TOKENS or num_src_ranks > 1:
+ * MOE_ERR_UNSUPPORTED).  minibatch_rows, ring_rows and pipeline are not used.
+ * x, w_router, out32 and the weights are 16-byte aligned, out 8-byte, scales
+ * and the other outputs 4-byte (MOE_ERR_INVALID_ARG).
+ *
+ * Values: sums are fp32, in a fixed order; routed outputs are not rounded to
+ * bf16 before the combine, and bf16 experts keep 16 bits of h, so results
+ * differ from moe_forward's by that rounding.  MXFP8 quantises x and h as
+ * moe_forward does.  Repeated calls give the same bits.  A token's results do
+ * not depend on the other tokens of the call.
+ * The first call in a process asks the runtime for the current device's
+ * compute-unit count; the call can be captured in a HIP graph.  Its workgroups
+ * wait for each other in an order in which every wait ends, whatever else the
+ * GPU runs (MOE_DEVERR_PIPELINE after about 1 s would mean a workspace that was
+ * never initialised; initialise it before it is used again).
+ */
+#define MOE_FEW_TOKENS 64
+moe_status moe_few(const moe_shape* shape, const moe_weights* weights, const moe_router* router, const void* x,
+                   const void* w_router, const float* bias, float* logits, int32_t* topk_idx, float* topk_gate,
+                   void* out, float* out32, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * ---- Backward pass (one GPU: num_src_ranks == 1; bf16 routed and shared) ----
@@ -532,7 +571,8 @@ typedef enum {
   MOE_K_BWD_REPLAY = 11, /* moe_backward: up/gate replay of the routed rows */
   MOE_K_BWD_DGRAD = 12,  /* moe_backward: the routed data-gradient GEMMs (dh, dx) */
   MOE_K_BWD_WGRAD = 13,  /* moe_backward: the routed weight-gradient GEMMs */
-  MOE_K_COUNT = 14
+  MOE_K_FEW = 14,        /* moe_few: its one launch */
+  MOE_K_COUNT = 15
 } moe_kernel_id;
 
 moe_status moe_probe_begin(int32_t kernel_id, int32_t max_launches);

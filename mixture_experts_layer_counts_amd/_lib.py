@@ -25,7 +25,8 @@ GROUP_SCORES = {"max": 0, "top2": 1}
 DEVERR_EXPERT_RANGE, DEVERR_ROW_OVERFLOW, DEVERR_NONFINITE, DEVERR_PIPELINE = 0x1, 0x2, 0x4, 0x8
 KERNELS = {"router_gemm": 0, "topk": 1, "schedule": 2, "tiles": 3, "shared_up": 4, "shared_down": 5, "gather": 6,
            "up_gate": 7, "down": 8, "combine": 9, "pipeline": 10, "bwd_replay": 11, "bwd_dgrad": 12,
-           "bwd_wgrad": 13}
+           "bwd_wgrad": 13, "few": 14}
+FEW_TOKENS = 64
 
 
 class MoeShape(ctypes.Structure):
@@ -84,6 +85,8 @@ _SIGS = {
     "moe_schedule_static": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, _P]),
     "moe_forward": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights), _P, _P, _P, _P, _P, _P,
                                    _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_few": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights), ctypes.POINTER(MoeRouter), _P, _P,
+                               _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_routed_rows": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.c_size_t, ctypes.POINTER(_P),
                                        ctypes.POINTER(ctypes.c_int64)]),
     "moe_quantize_mxfp8": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]),

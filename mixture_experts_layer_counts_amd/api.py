@@ -219,6 +219,14 @@ class MoELayer:
                 _ptr(out["route_dst"]), _ptr(self.ws), self.ws_bytes, _stream()))
         return out
 
+    def _weights(self, weights: Dict[str, torch.Tensor]) -> _lib.MoeWeights:
+        w = _lib.MoeWeights()
+        for field, name, dtype, shp in self._weight_specs:
+            t = weights[name]
+            _need(t, name, dtype, shp, self.device)
+            setattr(w, field, t.data_ptr())
+        return w
+
     # -- moe_forward -------------------------------------------------------
     def forward(self, weights: Dict[str, torch.Tensor], x_src: torch.Tensor, x_local: torch.Tensor,
                 gate: torch.Tensor, sched: Dict[str, torch.Tensor], out32: bool = True,
@@ -227,11 +235,7 @@ class MoELayer:
         _need(x_local, "x_local", torch.bfloat16, (s.T, D), dev)
         _need(x_src, "x_src", torch.bfloat16, (s.num_src_ranks * s.T, D), dev)
         _need(gate, "gate", torch.float32, (s.T, s.k), dev)
-        w = _lib.MoeWeights()
-        for field, name, dtype, shp in self._weight_specs:
-            t = weights[name]
-            _need(t, name, dtype, shp, dev)
-            setattr(w, field, t.data_ptr())
+        w = self._weights(weights)
         if out is None:
             out = torch.empty((s.T, D), dtype=torch.bfloat16, device=dev)
         _need(out, "out", torch.bfloat16, (s.T, D), dev)
@@ -245,6 +249,39 @@ class MoELayer:
                 _ptr(sched["sched"]), _ptr(sched["route_dst"]), _ptr(out), _ptr(out_f32), _ptr(self.ws),
                 self.ws_bytes, _stream()))
         return out, out_f32
+
+    # -- moe_few -----------------------------------------------------------
+    def few(self, x: torch.Tensor, w_router: Optional[torch.Tensor], weights: Dict[str, torch.Tensor],
+            logits: Optional[torch.Tensor] = None, router: Optional[_lib.MoeRouter] = None,
+            bias: Optional[torch.Tensor] = None, out32: bool = True) -> Dict[str, Optional[torch.Tensor]]:
+        """The whole layer for at most 64 tokens in one launch (moe_few), from x
+        or from given ``logits``: logits, idx, gate, out and out32 (None unless
+        asked for).  bf16 and MXFP8 experts, one GPU."""
+        s, dev = self.shape, self.device
+        T, D, E, k = s.T, s.D, s.E_total, s.k
+        _need(x, "x", torch.bfloat16, (T, D), dev)
+        if bias is not None:
+            if router is None:
+                raise ValueError("a bias needs a router")
+            _need(bias, "bias", torch.float32, (E,), dev)
+        if logits is not None:
+            _need(logits, "logits", torch.float32, (T, E), dev)
+            w_router = None
+        else:
+            _need(w_router, "w_router", torch.bfloat16, (E, D), dev)
+        w = self._weights(weights)
+        with _on(dev):
+            if logits is None:
+                logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+            idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+            gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+            out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+            out_f32 = torch.empty((T, D), dtype=torch.float32, device=dev) if out32 else None
+            _lib.check("moe_few", self.lib.moe_few(
+                ctypes.byref(s), ctypes.byref(w), None if router is None else ctypes.byref(router), _ptr(x),
+                _ptr(w_router), _ptr(bias), _ptr(logits), _ptr(idx), _ptr(gate), _ptr(out), _ptr(out_f32),
+                _ptr(self.ws), self.ws_bytes, _stream()))
+        return {"logits": logits, "idx": idx, "gate": gate, "out": out, "out32": out_f32}
 
     # -- whole layer -------------------------------------------------------
     def __call__(self, x: torch.Tensor, w_router: Optional[torch.Tensor], weights: Dict[str, torch.Tensor],

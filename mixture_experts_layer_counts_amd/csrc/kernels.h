@@ -377,4 +377,38 @@ hipError_t launch_quantize_rows_mx_staged(const uint16_t* src, int64_t rows, int
 hipError_t launch_pack_mx_scales(const uint8_t* scale, int64_t groups, int64_t rows, int64_t K, uint8_t* packed,
                                  hipStream_t stream);
 
+// ---- the layer for a few tokens in one launch (few.hip) ----
+constexpr int kFewTokens = 64;
+struct FewWeights {
+  const void *gate, *up, *down;  // bf16 or E4M3, row-major or K-tiled
+  const uint8_t *s_gate, *s_up, *s_down;  // E4M3: stage-major scales
+  bool tiled;
+};
+struct FewArgs {
+  const uint16_t* x;         // [T][D]
+  const uint16_t* w_router;  // [E][D], or NULL: `logits` is an input
+  const float* bias;         // [E] or NULL
+  float* logits;
+  int32_t* idx;
+  float* gate;
+  uint16_t* out;
+  float* out32;  // or NULL
+  FewWeights routed, shared;
+  RouterArgs router;
+  int T, D, I, Is, E, k;
+  // workspace
+  int32_t* ctl;   // few_ctl_ints words, 0 before the first call
+  int32_t* list;  // few_list_ints words
+  void* h;        // T k I + T Is values of 4 bytes
+  float* y;       // [T k + T][D]
+  uint8_t* xq;    // MXFP8: x and h with their scale words
+  uint32_t* xs;
+  uint8_t* hq;
+  uint32_t* hs;
+  int* err;
+};
+int few_ctl_ints(int E, int D);
+int few_list_ints(int E, int routes);
+hipError_t launch_few(const FewArgs& a, bool mx_routed, bool mx_shared, hipStream_t stream);
+
 }  // namespace moe

@@ -34,6 +34,8 @@ struct Layout {
   int max_tiles;
   int routed_bm;      // tile height of the routed GEMMs' tile lists
   int bn_up, bn_down;  // output columns per work item of the routed bf16 GEMMs
+  // moe_few (shapes it serves)
+  size_t few_ctl, few_list, few_h, few_y, few_xq, few_xs, few_hq, few_hs;
   size_t pipe_counters;  // pipeline == 1: (3 + max_tiles) * n_minibatches ints, then the work queues
   int64_t y_rows;
 };
@@ -106,6 +108,12 @@ int router_splits(const moe_shape* s) {
   int S = 1;
   while (2 * S <= moe::kMaxRouterParts && tiles * S * 2 <= 512 && stages % (2 * S) == 0) S *= 2;
   return S;
+}
+
+// Shapes that moe_few serves; `s` is valid.
+bool few_shape(const moe_shape* s) {
+  return s->num_src_ranks == 1 && s->T <= moe::kFewTokens && s->precision != MOE_INT8 &&
+         s->shared_precision != MOE_INT8;
 }
 
 Layout layout_of(const moe_shape* s) {
@@ -184,6 +192,18 @@ Layout layout_of(const moe_shape* s) {
     L.h_shared = take(sizeof(uint16_t) * s->T * s->I_shared);
   }
   L.router_parts = take(L.router_splits > 1 ? sizeof(float) * L.router_splits * s->T * s->E_total : 0);
+  if (few_shape(s)) {
+    const bool mx = s->precision == MOE_MXFP8 || s->shared_precision == MOE_MXFP8;
+    const int64_t h_elems = NK * s->I + s->T * s->I_shared;
+    L.few_ctl = take(sizeof(int32_t) * moe::few_ctl_ints(static_cast<int>(s->E_total), static_cast<int>(s->D)));
+    L.few_list = take(sizeof(int32_t) * moe::few_list_ints(static_cast<int>(s->E_total), static_cast<int>(NK)));
+    L.few_h = take(sizeof(float) * h_elems);
+    L.few_y = take(sizeof(float) * (NK + s->T) * s->D);
+    L.few_xq = take(mx ? s->T * s->D : 0);
+    L.few_xs = take(mx ? s->T * (s->D / 32) : 0);
+    L.few_hq = take(mx ? h_elems : 0);
+    L.few_hs = take(mx ? 4 * ((h_elems + 127) / 128 + 1) : 0);
+  }
   L.total = off;
   return L;
 }
@@ -719,7 +739,11 @@ moe_status moe_workspace_init(const moe_shape* shape, void* ws, size_t ws_bytes,
   Layout L;
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
-  return hip_status(moe::launch_clear_int(at<int>(ws, L.err), 1, static_cast<hipStream_t>(stream)));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  MOE_TRY_HIP(moe::launch_clear_int(at<int>(ws, L.err), 1, s));
+  if (!few_shape(shape)) return MOE_OK;
+  return hip_status(moe::launch_clear_int(
+      at<int>(ws, L.few_ctl), moe::few_ctl_ints(static_cast<int>(shape->E_total), static_cast<int>(shape->D)), s));
 }
 
 moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router, float* logits, int32_t* topk_idx,
@@ -1045,6 +1069,62 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* w, const void*
   ProbeScope probe(MOE_K_COMBINE, s);
   return hip_status(moe::launch_combine(Y, sh_out, topk_gate, route_dst, shape->rank * T * static_cast<int64_t>(k), T,
                                         D, k, R > 1, static_cast<uint16_t*>(out), out32, s));
+}
+
+moe_status moe_few(const moe_shape* shape, const moe_weights* w, const moe_router* router, const void* x,
+                   const void* w_router, const float* bias, float* logits, int32_t* topk_idx, float* topk_gate,
+                   void* out, float* out32, void* ws, size_t ws_bytes, void* stream) {
+  Layout L;
+  const moe_status st = check_ws(shape, ws, ws_bytes, &L);
+  if (st != MOE_OK) return st;
+  if (!few_shape(shape)) return MOE_ERR_UNSUPPORTED;
+  if (!router && bias) return MOE_ERR_INVALID_ARG;
+  const moe_router plain = {MOE_SCORE_SOFTMAX, 1, 1, MOE_GROUP_MAX, 1, 1.0f};
+  if (!router) router = &plain;
+  if (!valid_router(shape, router) || !w) return MOE_ERR_INVALID_ARG;
+  const bool mxr = shape->precision == MOE_MXFP8, mxs = shape->shared_precision == MOE_MXFP8;
+  const auto fits = [](std::initializer_list<const void*> ps, uintptr_t align) {
+    for (const void* p : ps)
+      if (!p || reinterpret_cast<uintptr_t>(p) % align) return false;
+    return true;
+  };
+  if (!fits({w->w_gate, w->w_up, w->w_down, w->ws_gate, w->ws_up, w->ws_down}, 16)) return MOE_ERR_INVALID_ARG;
+  if (mxr && !fits({w->s_gate, w->s_up, w->s_down}, 4)) return MOE_ERR_INVALID_ARG;
+  if (mxs && !fits({w->ss_gate, w->ss_up, w->ss_down}, 4)) return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
+  if (!fits({x}, 16) || !fits({out}, 8) || !fits({logits, topk_idx, topk_gate}, 4)) return MOE_ERR_INVALID_ARG;
+  if (w_router && reinterpret_cast<uintptr_t>(w_router) % 16) return MOE_ERR_INVALID_ARG;
+  if (out32 && reinterpret_cast<uintptr_t>(out32) % 16) return MOE_ERR_INVALID_ARG;
+  moe::FewArgs a{};
+  a.x = static_cast<const uint16_t*>(x);
+  a.w_router = static_cast<const uint16_t*>(w_router);
+  a.bias = bias;
+  a.logits = logits;
+  a.idx = topk_idx;
+  a.gate = topk_gate;
+  a.out = static_cast<uint16_t*>(out);
+  a.out32 = out32;
+  a.routed = moe::FewWeights{w->w_gate, w->w_up, w->w_down, w->s_gate, w->s_up, w->s_down, shape->weights_tiled != 0};
+  a.shared = moe::FewWeights{w->ws_gate, w->ws_up, w->ws_down, w->ss_gate, w->ss_up, w->ss_down, false};
+  a.router = router_args(router);
+  a.T = static_cast<int>(shape->T);
+  a.D = static_cast<int>(shape->D);
+  a.I = static_cast<int>(shape->I);
+  a.Is = static_cast<int>(shape->I_shared);
+  a.E = static_cast<int>(shape->E_total);
+  a.k = static_cast<int>(shape->k);
+  a.ctl = at<int32_t>(ws, L.few_ctl);
+  a.list = at<int32_t>(ws, L.few_list);
+  a.h = at<void>(ws, L.few_h);
+  a.y = at<float>(ws, L.few_y);
+  a.xq = at<uint8_t>(ws, L.few_xq);
+  a.xs = at<uint32_t>(ws, L.few_xs);
+  a.hq = at<uint8_t>(ws, L.few_hq);
+  a.hs = at<uint32_t>(ws, L.few_hs);
+  a.err = at<int>(ws, L.err);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  ProbeScope probe(MOE_K_FEW, s);
+  return hip_status(moe::launch_few(a, mxr, mxs, s));
 }
 
 moe_status moe_routed_rows(const moe_shape* shape, const void* ws, size_t ws_bytes, const void** rows,
