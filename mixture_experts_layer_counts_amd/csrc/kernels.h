@@ -379,6 +379,7 @@ hipError_t launch_pack_mx_scales(const uint8_t* scale, int64_t groups, int64_t r
 
 // ---- the layer for a few tokens in one launch (few.hip) ----
 constexpr int kFewTokens = 64;
+constexpr int kFewParts = 8;  // K parts of the router's rows, at most
 struct FewWeights {
   const void *gate, *up, *down;  // bf16 or E4M3, row-major or K-tiled
   const uint8_t *s_gate, *s_up, *s_down;  // E4M3: stage-major scales
@@ -405,7 +406,11 @@ struct FewArgs {
   uint32_t* xs;
   uint8_t* hq;
   uint32_t* hs;
+  float* parts;   // [kFewParts][T][E]
   int* err;
+  int32_t* flags;  // in ctl
+  // set by the launcher, with flags: K parts, columns of a combine item, items of a draw
+  int n_parts, comb_cols, up_batch, down_batch;
 };
 int few_ctl_ints(int E, int D);
 int few_list_ints(int E, int routes);

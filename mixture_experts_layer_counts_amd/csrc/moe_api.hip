@@ -35,7 +35,7 @@ struct Layout {
   int routed_bm;      // tile height of the routed GEMMs' tile lists
   int bn_up, bn_down;  // output columns per work item of the routed bf16 GEMMs
   // moe_few (shapes it serves)
-  size_t few_ctl, few_list, few_h, few_y, few_xq, few_xs, few_hq, few_hs;
+  size_t few_ctl, few_list, few_h, few_y, few_xq, few_xs, few_hq, few_hs, few_parts;
   size_t pipe_counters;  // pipeline == 1: (3 + max_tiles) * n_minibatches ints, then the work queues
   int64_t y_rows;
 };
@@ -199,6 +199,7 @@ Layout layout_of(const moe_shape* s) {
     L.few_list = take(sizeof(int32_t) * moe::few_list_ints(static_cast<int>(s->E_total), static_cast<int>(NK)));
     L.few_h = take(sizeof(float) * h_elems);
     L.few_y = take(sizeof(float) * (NK + s->T) * s->D);
+    L.few_parts = take(sizeof(float) * moe::kFewParts * s->T * s->E_total);
     L.few_xq = take(mx ? s->T * s->D : 0);
     L.few_xs = take(mx ? s->T * (s->D / 32) : 0);
     L.few_hq = take(mx ? h_elems : 0);
@@ -1121,6 +1122,7 @@ moe_status moe_few(const moe_shape* shape, const moe_weights* w, const moe_route
   a.xs = at<uint32_t>(ws, L.few_xs);
   a.hq = at<uint8_t>(ws, L.few_hq);
   a.hs = at<uint32_t>(ws, L.few_hs);
+  a.parts = at<float>(ws, L.few_parts);
   a.err = at<int>(ws, L.err);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   ProbeScope probe(MOE_K_FEW, s);
