@@ -542,6 +542,77 @@ moe_status moe_linear_int8(const void* x, int32_t x_dtype, int64_t M, int64_t K,
                            const float* w_scale, int64_t N, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
                            void* stream);
 
+/*
+ * ---- The block around a layer: norms, gate, dropout, residual sum ----
+ *
+ * With x the residual stream [T, D] and y what the layer made of the stream's
+ * norm [T, D]:
+ *   z = x + scale gate drop(N(y) (w_post + weight_offset))     the stream behind the layer
+ *   h = N(z) (w_pre + weight_offset)                           what the next layer reads
+ *   N(v) = v / sqrt(mean_d v^2 + eps), per row
+ * Each of w_post (without it N(y) (...) is y itself), gate and w_pre (without it
+ * there is no h) may be absent, and without y z is x: the norm before a first
+ * layer.  gate [gate_rows, D]: T / gate_rows consecutive rows share one of its rows
+ * (1: a learned gate per channel; the batch size: one per sequence; T: one per token).
+ * drop keeps an element if its 32 random bits are at least round(dropout * 2^32) and
+ * divides what it keeps by 1 - dropout; what it drops adds nothing, an infinity or a
+ * NaN neither.  The bits of element (t, d) are word d % 4 of Philox-4x32 of ten
+ * rounds at the counter (d / 4, t, offset mod 2^32, offset / 2^32) under the key
+ * (seed mod 2^32, seed / 2^32).  The mask is never stored: the backward of a call
+ * takes the same seed and offset.
+ * Sums are fp32, z, h and the row gradients are rounded once; h is formed from
+ * z before it is rounded.  Results are bitwise repeatable.
+ */
+typedef struct {
+  int64_t T;         /* rows, below 2^31 */
+  int64_t D;         /* columns; 8 .. MOE_NORM_MAX_COLUMNS */
+  int64_t gate_rows; /* rows of gate, a divisor of T; 0: no gate */
+  int32_t x_dtype;   /* moe_dtype of x, z, dz and dx */
+  int32_t y_dtype;   /* of y and dy */
+  int32_t w_dtype;   /* of w_post, w_pre and gate */
+  int32_t dh_dtype;  /* of dh (backward) */
+  double scale;      /* finite */
+  double eps;        /* finite, >= 0 */
+  double weight_offset; /* finite; 1 for weights stored as their difference to 1 */
+  double dropout;    /* 0 <= dropout < 1 */
+} moe_norm;
+#define MOE_NORM_MAX_COLUMNS 16384
+
+/*
+ *   x, y        [T, D]; y or NULL
+ *   w_post, w_pre  [D] or NULL; gate [gate_rows, D], NULL where gate_rows is 0
+ *   rng         device uint64 [2]: seed and offset (so that a captured graph can be
+ *               given new ones); NULL where dropout is 0
+ *   z           [T, D] out, or NULL (only without y: z is x)
+ *   h           [T, D] bf16 out, with w_pre; else NULL
+ * w_post, gate and dropout need y; y or w_pre must be there.  Pointers are aligned to
+ * their elements; outputs overlap no input.  MOE_ERR_INVALID_ARG otherwise;
+ * MOE_ERR_UNSUPPORTED for other column counts.  One launch on `stream`.
+ */
+moe_status moe_block_norm(const moe_norm* norm, const void* x, const void* y, const void* w_post, const void* gate,
+                          const void* w_pre, const uint64_t* rng, void* z, void* h, void* stream);
+
+/*
+ * The gradients of moe_block_norm for gradients dz of z and dh of h (those of z
+ * that came through h are not part of dz).
+ *   z           [T, D], as the forward wrote it (without y: x); needed with w_pre
+ *   dz          [T, D] or NULL for zero;  dh [T, D], with w_pre; else NULL
+ *   dx, dy      [T, D] out (dy with y);  dw_post, dw_pre [D], dgate [gate_rows, D]
+ *               fp32 out, each with its input; NULL otherwise
+ *   ws          device workspace of moe_block_norm_backward_workspace_bytes
+ * With r = 1 / sqrt(mean v^2 + eps) of a row and w the weight with its offset:
+ *   a = w_pre dh,  dx = dz + r_z (a - z r_z^2 mean(a z)),  dw_pre = sum_t dh z r_z
+ *   dn = scale drop(dx) / (1 - dropout),  dgate = sum_t dn N(y) w_post,  b = dn gate w_post
+ *   dy = r_y (b - y r_y^2 mean(b y)),  dw_post = sum_t dn gate y r_y   (without w_post: dy = dn gate)
+ * The last three from dx before it is rounded.  Every sum runs in a fixed order.
+ * Two launches on `stream`.
+ */
+moe_status moe_block_norm_backward_workspace_bytes(const moe_norm* norm, size_t* bytes);
+moe_status moe_block_norm_backward(const moe_norm* norm, const void* z, const void* y, const void* dz, const void* dh,
+                                   const void* w_post, const void* gate, const void* w_pre, const uint64_t* rng,
+                                   void* dx, void* dy, float* dw_post, float* dgate, float* dw_pre, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 /* Read the sticky device error word (MOE_DEVERR_* bits).  SYNCHRONISES the
  * stream: diagnostics only, never on the hot path. */
 moe_status moe_get_device_error(const moe_shape* shape, const void* ws, size_t ws_bytes,

@@ -42,6 +42,12 @@ class MoeRouter(ctypes.Structure):
         ("scale", ctypes.c_float)]
 
 
+class MoeNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "D", "gate_rows")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "y_dtype", "w_dtype", "dh_dtype")] + [
+        (n, ctypes.c_double) for n in ("scale", "eps", "weight_offset", "dropout")]
+
+
 class MoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down", "ws_gate", "ws_up", "ws_down", "ss_gate", "ss_up",
@@ -99,6 +105,10 @@ _SIGS = {
                                                        ctypes.POINTER(ctypes.c_size_t)]),
     "moe_linear_int8": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_int64,
                                        _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "moe_block_norm": (ctypes.c_int, [ctypes.POINTER(MoeNorm)] + [_P] * 9),
+    "moe_block_norm_backward_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(MoeNorm),
+                                                               ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(MoeNorm)] + [_P] * 14 + [ctypes.c_size_t, _P]),
     "moe_get_device_error": (ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.c_size_t, _P,
                                             ctypes.POINTER(ctypes.c_int32)]),
     "moe_backward_prepare": (ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights), _P,

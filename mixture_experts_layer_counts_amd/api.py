@@ -3,7 +3,7 @@
 Torch supplies device memory and the current HIP stream; the C calls do all
 of the work.  Names follow include/moe.h: ``route``, ``schedule``,
 ``forward``, ``quantize_mxfp8``, ``pack_mxfp8_scales``, ``quantize_int8``,
-``matmul_int8`` and ``linear_int8``.
+``matmul_int8``, ``linear_int8``, ``few`` and ``block_norm``.
 """
 
 from __future__ import annotations
@@ -572,3 +572,108 @@ def tile_int8(q: torch.Tensor) -> torch.Tensor:
     if q.dtype != torch.int8:
         raise ValueError("q must be int8")
     return tile_mxfp8(q.view(torch.uint8)).view(torch.int8)
+
+
+def _norm_struct(x: torch.Tensor, y: Optional[torch.Tensor], post_weight, gate, pre_weight, scale: float, eps: float,
+                 weight_offset: float, dropout: float, rng, x_name: str) -> _lib.MoeNorm:
+    """The moe_norm of a call, its inputs checked."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{x_name} must be a tensor")
+    if x.dim() != 2 or x.dtype not in _INT8_DTYPES or x.device.type != "cuda":
+        raise ValueError(f"{x_name} must be a [T, D] bf16 or fp32 device tensor")
+    (T, D), dev = x.shape, x.device
+    _need(x, x_name, x.dtype, (T, D), dev)
+    if y is None and pre_weight is None:
+        raise ValueError("y or pre_weight must be given")
+    if y is None and (post_weight is not None or gate is not None or dropout):
+        raise ValueError("post_weight, gate and dropout need y")
+    if y is not None:
+        if not isinstance(y, torch.Tensor) or y.dtype not in _INT8_DTYPES:
+            raise ValueError("y must be a bf16 or fp32 tensor")
+        _need(y, "y", y.dtype, (T, D), dev)
+    wtype = None
+    for t, n in ((post_weight, "post_weight"), (gate, "gate"), (pre_weight, "pre_weight")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype not in _INT8_DTYPES:
+            raise ValueError(f"{n} must be a bf16 or fp32 tensor")
+        wtype = wtype or t.dtype
+        if n == "gate":
+            if t.dim() != 2 or t.shape[0] < 1 or T % t.shape[0]:
+                raise ValueError("gate must be [G, D], G a divisor of the rows")
+            _need(t, n, wtype, (t.shape[0], D), dev)
+        else:
+            _need(t, n, wtype, (D,), dev)
+    if not 0.0 <= dropout < 1.0:
+        raise ValueError("dropout must be in [0, 1)")
+    if dropout:
+        if rng is None:
+            raise ValueError("dropout needs rng")
+        _need(rng, "rng", torch.int64, (2,), dev)
+    n = _lib.MoeNorm()
+    n.T, n.D, n.gate_rows = T, D, 0 if gate is None else gate.shape[0]
+    n.x_dtype = _INT8_DTYPES[x.dtype]
+    n.y_dtype = _lib.DT_BF16 if y is None else _INT8_DTYPES[y.dtype]
+    n.w_dtype = _lib.DT_BF16 if wtype is None else _INT8_DTYPES[wtype]
+    n.scale, n.eps, n.weight_offset, n.dropout = scale, eps, weight_offset, dropout
+    return n
+
+
+def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, post_weight: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None, scale: float = 1.0,
+               eps: float = 1e-6, weight_offset: float = 0.0, dropout: float = 0.0,
+               rng: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(z, h) around a layer (moe_block_norm): the residual stream
+    z = x + scale * gate * drop(norm(y) * post_weight) behind it, and what the next
+    layer reads, h = norm(z) * pre_weight in bf16 (None without pre_weight).
+    Without ``y`` z is x itself: the norm before a first layer.  x, y [T, D] bf16 or
+    fp32; weights [D] and gate [G, D] (T / G consecutive rows share a row of it) of
+    one type; ``weight_offset`` is added to the weights.  ``dropout`` draws its mask
+    from ``rng``, int64 [2] on the device (seed and offset), and does not store it."""
+    lib, dev = _lib.load(), x.device
+    n = _norm_struct(x, y, post_weight, gate, pre_weight, scale, eps, weight_offset, dropout, rng, "x")
+    with _on(dev):
+        z = x if y is None else torch.empty_like(x)
+        h = None if pre_weight is None else torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        _lib.check("moe_block_norm", lib.moe_block_norm(
+            ctypes.byref(n), _ptr(x), _ptr(y), _ptr(post_weight), _ptr(gate), _ptr(pre_weight),
+            _ptr(rng) if dropout else None, None if y is None else _ptr(z), _ptr(h), _stream()))
+    return z, h
+
+
+def block_norm_backward(z: Optional[torch.Tensor], y: Optional[torch.Tensor], dz: Optional[torch.Tensor],
+                        dh: Optional[torch.Tensor], *, post_weight: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+                        scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0, dropout: float = 0.0,
+                        rng: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """The gradients of ``block_norm`` (moe_block_norm_backward) for gradients
+    ``dz`` (None: zero) and ``dh`` (with pre_weight) of its results: dx, dy,
+    dpost_weight, dgate, dpre_weight, the last three in fp32, each None without its
+    input.  ``z``: the stream as block_norm returned it (x, where it had no y); the
+    other arguments, ``rng``'s values among them, as in that call."""
+    lib = _lib.load()
+    n = _norm_struct(z, y, post_weight, gate, pre_weight, scale, eps, weight_offset, dropout, rng, "z")
+    (T, D), dev = z.shape, z.device
+    if dz is not None:
+        _need(dz, "dz", z.dtype, (T, D), dev)
+    if (dh is None) != (pre_weight is None):
+        raise ValueError("dh and pre_weight come together")
+    if dh is not None:
+        if not isinstance(dh, torch.Tensor) or dh.dtype not in _INT8_DTYPES:
+            raise ValueError("dh must be a bf16 or fp32 tensor")
+        _need(dh, "dh", dh.dtype, (T, D), dev)
+        n.dh_dtype = _INT8_DTYPES[dh.dtype]
+    nbytes = ctypes.c_size_t(0)
+    _lib.check("moe_block_norm_backward_workspace_bytes",
+               lib.moe_block_norm_backward_workspace_bytes(ctypes.byref(n), ctypes.byref(nbytes)))
+    with _on(dev):
+        def f32(like):
+            return None if like is None else torch.empty(like.shape, dtype=torch.float32, device=dev)
+        out = {"dx": torch.empty_like(z), "dy": None if y is None else torch.empty_like(y),
+               "dpost_weight": f32(post_weight), "dgate": f32(gate), "dpre_weight": f32(pre_weight)}
+        ws = torch.empty(max(nbytes.value, 1), dtype=torch.uint8, device=dev)
+        _lib.check("moe_block_norm_backward", lib.moe_block_norm_backward(
+            ctypes.byref(n), _ptr(z), _ptr(y), _ptr(dz), _ptr(dh), _ptr(post_weight), _ptr(gate), _ptr(pre_weight),
+            _ptr(rng) if dropout else None, _ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dpost_weight"]),
+            _ptr(out["dgate"]), _ptr(out["dpre_weight"]), _ptr(ws), nbytes.value, _stream()))
+    return out

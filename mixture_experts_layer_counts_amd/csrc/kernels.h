@@ -416,4 +416,33 @@ int few_ctl_ints(int E, int D);
 int few_list_ints(int E, int routes);
 hipError_t launch_few(const FewArgs& a, bool mx_routed, bool mx_shared, hipStream_t stream);
 
+// ---- norms, gate, dropout and residual sum around a layer (norm.hip) ----
+constexpr int kNormWidth = 16384;  // columns at most
+constexpr int kNormWaves = 8192;   // waves that the backward's runs of rows fill
+struct NormArgs {
+  const void *x, *y;  // [T][D]; y or NULL; the backward: z in x's place
+  const void *post, *gate, *pre;  // [D], [groups][D], [D], each or NULL
+  const uint64_t* rng;  // seed and offset
+  void *z, *h;        // z or NULL; h where there is pre
+  // backward
+  const void *dz, *dh;  // dz or NULL
+  void *dx, *dy;
+  float *dpost, *dgate, *dpre;
+  float* parts;  // 4 norm_runs().runs rows of D
+  int64_t T, groups, group;  // group: rows of one gate row
+  int D;
+  float factor, eps, offset;  // scale / (1 - p)
+  bool drop;
+  uint32_t threshold;  // p 2^32
+  // set by the launchers
+  int lanes;
+  int64_t run, runs;
+};
+struct NormRuns {
+  int64_t run, runs, blocks;  // rows of a run
+};
+NormRuns norm_runs(int64_t T, int D);
+hipError_t launch_norm(const NormArgs& a, bool x_f32, bool y_f32, bool w_f32, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, bool w_f32, bool dh_f32, hipStream_t stream);
+
 }  // namespace moe

@@ -1245,6 +1245,148 @@ moe_status moe_linear_int8(const void* x, int32_t x_dtype, int64_t M, int64_t K,
   return hip_status(moe::launch_gemm_i8(g, epi, s));
 }
 
+// ---- norms around a layer ----
+
+// Element sizes and shared checks of the two passes.
+static bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
+  if (!p || !q) return false;
+  const uint64_t a = reinterpret_cast<uint64_t>(p), b = reinterpret_cast<uint64_t>(q);
+  return a < b + m && b < a + n;
+}
+static bool aligned_to(const void* p, int64_t size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+
+static moe_status norm_sizes(const moe_norm* n) {
+  if (!n || n->T < 0 || n->T >= (int64_t(1) << 31) || n->D < 1 || n->gate_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (n->gate_rows > 0 && n->T % n->gate_rows) return MOE_ERR_INVALID_ARG;
+  for (const int32_t t : {n->x_dtype, n->y_dtype, n->w_dtype, n->dh_dtype})
+    if (t != MOE_DT_BF16 && t != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(n->scale) || !std::isfinite(n->eps) || n->eps < 0 || !std::isfinite(n->weight_offset))
+    return MOE_ERR_INVALID_ARG;
+  if (!(n->dropout >= 0 && n->dropout < 1)) return MOE_ERR_INVALID_ARG;
+  if (n->D < 8 || n->D > MOE_NORM_MAX_COLUMNS) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static int64_t dtype_size(int32_t t) { return t == MOE_DT_F32 ? 4 : 2; }
+
+// The arguments both passes have; x: the backward's z.
+static moe_status norm_args(const moe_norm* n, const void* x, const void* y, const void* w_post, const void* gate,
+                            const void* w_pre, const uint64_t* rng, moe::NormArgs* a) {
+  const moe_status st = norm_sizes(n);
+  if (st != MOE_OK) return st;
+  if (n->T > 0) {  // (no rows: their pointers may be NULL)
+    if (!y && !w_pre) return MOE_ERR_INVALID_ARG;
+    if (!y && (w_post || gate || n->dropout > 0)) return MOE_ERR_INVALID_ARG;
+  }
+  if ((n->gate_rows > 0) != (gate != nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((n->dropout > 0) != (rng != nullptr)) return MOE_ERR_INVALID_ARG;
+  const int64_t wsize = dtype_size(n->w_dtype);
+  if (!aligned_to(x, dtype_size(n->x_dtype)) || !aligned_to(y, dtype_size(n->y_dtype)) || !aligned_to(w_post, wsize) ||
+      !aligned_to(gate, wsize) || !aligned_to(w_pre, wsize) || !aligned_to(rng, 8))
+    return MOE_ERR_INVALID_ARG;
+  *a = moe::NormArgs{};
+  a->x = x;
+  a->y = y;
+  a->post = w_post;
+  a->gate = gate;
+  a->pre = w_pre;
+  a->rng = rng;
+  a->T = n->T;
+  a->D = static_cast<int>(n->D);
+  a->groups = n->gate_rows;
+  a->group = n->gate_rows > 0 ? n->T / n->gate_rows : 1;
+  a->factor = static_cast<float>(n->scale / (1.0 - n->dropout));
+  a->eps = static_cast<float>(n->eps);
+  a->offset = static_cast<float>(n->weight_offset);
+  a->drop = n->dropout > 0;
+  const double threshold = std::nearbyint(n->dropout * 4294967296.0);
+  a->threshold = threshold >= 4294967295.0 ? 0xffffffffu : static_cast<uint32_t>(threshold);
+  return MOE_OK;
+}
+
+moe_status moe_block_norm(const moe_norm* n, const void* x, const void* y, const void* w_post, const void* gate,
+                          const void* w_pre, const uint64_t* rng, void* z, void* h, void* stream) {
+  moe::NormArgs a;
+  const moe_status st = norm_args(n, x, y, w_post, gate, w_pre, rng, &a);
+  if (st != MOE_OK) return st;
+  if (n->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
+  if (!x || (y && !z) || (w_pre != nullptr) != (h != nullptr)) return MOE_ERR_INVALID_ARG;
+  const int64_t xs = dtype_size(n->x_dtype);
+  if (!aligned_to(z, xs) || !aligned_to(h, 2)) return MOE_ERR_INVALID_ARG;
+  const uint64_t rows = static_cast<uint64_t>(n->T) * n->D, w = dtype_size(n->w_dtype) * n->D;
+  const uint64_t zb = rows * xs, hb = rows * 2;
+  if (overlap(z, zb, h, hb)) return MOE_ERR_INVALID_ARG;
+  const struct {
+    const void* p;
+    uint64_t bytes;
+  } inputs[] = {{x, zb}, {y, rows * dtype_size(n->y_dtype)}, {w_post, w}, {w_pre, w}, {gate, w * n->gate_rows}, {rng, 16}};
+  for (const auto& in : inputs)
+    if (overlap(z, zb, in.p, in.bytes) || overlap(h, hb, in.p, in.bytes)) return MOE_ERR_INVALID_ARG;
+  a.z = z;
+  a.h = h;
+  return hip_status(moe::launch_norm(a, n->x_dtype == MOE_DT_F32, n->y_dtype == MOE_DT_F32, n->w_dtype == MOE_DT_F32,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_block_norm_backward_workspace_bytes(const moe_norm* n, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status st = norm_sizes(n);
+  if (st != MOE_OK) return st;
+  *bytes = sizeof(float) * 4 * moe::norm_runs(n->T, static_cast<int>(n->D)).runs * n->D;
+  return MOE_OK;
+}
+
+moe_status moe_block_norm_backward(const moe_norm* n, const void* z, const void* y, const void* dz, const void* dh,
+                                   const void* w_post, const void* gate, const void* w_pre, const uint64_t* rng,
+                                   void* dx, void* dy, float* dw_post, float* dgate, float* dw_pre, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  moe::NormArgs a;
+  moe_status st = norm_args(n, z, y, w_post, gate, w_pre, rng, &a);
+  if (st != MOE_OK) return st;
+  size_t need = 0;
+  st = moe_block_norm_backward_workspace_bytes(n, &need);
+  if (st != MOE_OK) return st;
+  if ((w_post != nullptr) != (dw_post != nullptr) || (w_pre != nullptr) != (dw_pre != nullptr) ||
+      (gate != nullptr) != (dgate != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && (!ws || !aligned_to(ws, 4))) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(dw_post, 4) || !aligned_to(dw_pre, 4) || !aligned_to(dgate, 4)) return MOE_ERR_INVALID_ARG;
+  if (n->T > 0) {
+    if (!dx || (y != nullptr) != (dy != nullptr) || (w_pre != nullptr) != (dh != nullptr) || (w_pre && !z))
+      return MOE_ERR_INVALID_ARG;
+    const int64_t xs = dtype_size(n->x_dtype), ys = dtype_size(n->y_dtype), hs = dtype_size(n->dh_dtype);
+    if (!aligned_to(dz, xs) || !aligned_to(dx, xs) || !aligned_to(dy, ys) || !aligned_to(dh, hs))
+      return MOE_ERR_INVALID_ARG;
+    const uint64_t rows = static_cast<uint64_t>(n->T) * n->D, w = static_cast<uint64_t>(n->D);
+    const struct {
+      const void* p;
+      uint64_t bytes;
+    } inputs[] = {{w_pre ? z : nullptr, rows * xs}, {y, rows * ys}, {dz, rows * xs}, {dh, rows * hs},
+                  {w_post, w * dtype_size(n->w_dtype)}, {w_pre, w * dtype_size(n->w_dtype)},
+                  {gate, w * n->gate_rows * dtype_size(n->w_dtype)}, {rng, 16}},
+      outputs[] = {{dx, rows * xs}, {dy, rows * ys}, {dw_post, 4 * w}, {dw_pre, 4 * w}, {dgate, 4 * w * n->gate_rows},
+                   {need ? ws : nullptr, need}};
+    for (const auto& out : outputs) {
+      for (const auto& in : inputs)
+        if (overlap(out.p, out.bytes, in.p, in.bytes)) return MOE_ERR_INVALID_ARG;
+      for (const auto& other : outputs)
+        if (&other != &out && overlap(out.p, out.bytes, other.p, other.bytes)) return MOE_ERR_INVALID_ARG;
+    }
+  }
+  a.dz = dz;
+  a.dh = dh;
+  a.dx = dx;
+  a.dy = dy;
+  a.dpost = dw_post;
+  a.dgate = dgate;
+  a.dpre = dw_pre;
+  a.parts = static_cast<float*>(ws);
+  return hip_status(moe::launch_norm_backward(a, n->x_dtype == MOE_DT_F32, n->y_dtype == MOE_DT_F32,
+                                              n->w_dtype == MOE_DT_F32, n->dh_dtype == MOE_DT_F32,
+                                              static_cast<hipStream_t>(stream)));
+}
+
 moe_status moe_probe_begin(int32_t kernel_id, int32_t max_launches) {
   if (kernel_id < 0 || kernel_id >= MOE_K_COUNT || max_launches < 1 || max_launches > (1 << 20))
     return MOE_ERR_INVALID_ARG;
