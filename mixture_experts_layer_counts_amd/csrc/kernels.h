@@ -418,7 +418,7 @@ hipError_t launch_few(const FewArgs& a, bool mx_routed, bool mx_shared, hipStrea
 
 // ---- norms, gate, dropout and residual sum around a layer (norm.hip) ----
 constexpr int kNormWidth = 16384;  // columns at most
-constexpr int kNormWaves = 8192;   // waves that the backward's runs of rows fill
+constexpr int kNormWaves = 4096;   // waves that the backward's runs of rows fill
 struct NormArgs {
   const void *x, *y;  // [T][D]; y or NULL; the backward: z in x's place
   const void *post, *gate, *pre;  // [D], [groups][D], [D], each or NULL
@@ -432,6 +432,7 @@ struct NormArgs {
   int64_t T, groups, group;  // group: rows of one gate row
   int D;
   float factor, eps, offset;  // scale / (1 - p)
+  bool w_f32;  // type of post, gate and pre
   bool drop;
   uint32_t threshold;  // p 2^32
   // set by the launchers
@@ -442,7 +443,7 @@ struct NormRuns {
   int64_t run, runs, blocks;  // rows of a run
 };
 NormRuns norm_runs(int64_t T, int D);
-hipError_t launch_norm(const NormArgs& a, bool x_f32, bool y_f32, bool w_f32, hipStream_t stream);
-hipError_t launch_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, bool w_f32, bool dh_f32, hipStream_t stream);
+hipError_t launch_norm(const NormArgs& a, bool x_f32, bool y_f32, hipStream_t stream);
+hipError_t launch_norm_backward(const NormArgs& a, bool x_f32, bool y_f32, bool dh_f32, hipStream_t stream);
 
 }  // namespace moe

@@ -1298,6 +1298,7 @@ static moe_status norm_args(const moe_norm* n, const void* x, const void* y, con
   a->factor = static_cast<float>(n->scale / (1.0 - n->dropout));
   a->eps = static_cast<float>(n->eps);
   a->offset = static_cast<float>(n->weight_offset);
+  a->w_f32 = n->w_dtype == MOE_DT_F32;
   a->drop = n->dropout > 0;
   const double threshold = std::nearbyint(n->dropout * 4294967296.0);
   a->threshold = threshold >= 4294967295.0 ? 0xffffffffu : static_cast<uint32_t>(threshold);
@@ -1324,7 +1325,7 @@ moe_status moe_block_norm(const moe_norm* n, const void* x, const void* y, const
     if (overlap(z, zb, in.p, in.bytes) || overlap(h, hb, in.p, in.bytes)) return MOE_ERR_INVALID_ARG;
   a.z = z;
   a.h = h;
-  return hip_status(moe::launch_norm(a, n->x_dtype == MOE_DT_F32, n->y_dtype == MOE_DT_F32, n->w_dtype == MOE_DT_F32,
+  return hip_status(moe::launch_norm(a, n->x_dtype == MOE_DT_F32, n->y_dtype == MOE_DT_F32,
                                      static_cast<hipStream_t>(stream)));
 }
 
@@ -1383,8 +1384,7 @@ moe_status moe_block_norm_backward(const moe_norm* n, const void* z, const void*
   a.dpre = dw_pre;
   a.parts = static_cast<float*>(ws);
   return hip_status(moe::launch_norm_backward(a, n->x_dtype == MOE_DT_F32, n->y_dtype == MOE_DT_F32,
-                                              n->w_dtype == MOE_DT_F32, n->dh_dtype == MOE_DT_F32,
-                                              static_cast<hipStream_t>(stream)));
+                                              n->dh_dtype == MOE_DT_F32, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_probe_begin(int32_t kernel_id, int32_t max_launches) {
