@@ -293,6 +293,28 @@ class MoELayer:
         out, out32 = self.forward(weights, x, x, gate, sched)
         return {"logits": lg, "idx": idx, "gate": gate, "out": out, "out32": out32, **sched}
 
+    def block(self, x: torch.Tensor, w_router: Optional[torch.Tensor], weights: Dict[str, torch.Tensor],
+              pre_weight: torch.Tensor, post_weight: Optional[torch.Tensor] = None,
+              gate: Optional[torch.Tensor] = None, next_weight: Optional[torch.Tensor] = None, scale: float = 1.0,
+              eps: float = 1e-6, weight_offset: float = 0.0, dropout: float = 0.0,
+              rng: Optional[torch.Tensor] = None, router: Optional[_lib.MoeRouter] = None,
+              bias: Optional[torch.Tensor] = None, train: bool = False) -> Dict[str, Optional[torch.Tensor]]:
+        """The layer as a block of a model, for R = 1: h = norm(x) * pre_weight, the
+        layer's out of h, and z = x + scale * gate * drop(norm(out) * post_weight) with
+        h_next = norm(z) * next_weight for what follows (``block_norm``).  Calls for
+        few tokens run the layer in one launch (``few``) unless ``train`` is set, which
+        keeps what ``MoEBackward.block`` needs.  The layer's results, h, z and h_next."""
+        s = self.shape
+        _, h = block_norm(x, pre_weight=pre_weight, eps=eps, weight_offset=weight_offset)
+        quantised = _lib.MOE_INT8 in (s.precision, s.shared_precision)
+        if train or s.T > _lib.FEW_TOKENS or s.num_src_ranks != 1 or quantised:
+            r = self(h, w_router, weights, router=router, bias=bias)
+        else:
+            r = self.few(h, w_router, weights, router=router, bias=bias, out32=False)
+        z, h_next = block_norm(x, r["out"], post_weight=post_weight, gate=gate, pre_weight=next_weight, scale=scale,
+                               eps=eps, weight_offset=weight_offset, dropout=dropout, rng=rng)
+        return {**r, "h": h, "z": z, "h_next": h_next}
+
     def routed_rows(self) -> torch.Tensor:
         """The routed output rows moe_forward left in the workspace (a view,
         bf16 [n, D]): by route t*k+s when R == 1, by schedule position when R > 1."""
@@ -417,6 +439,25 @@ class MoEBackward:
                 _lib.check("moe_backward_scored", self.lib.moe_backward_scored(
                     ctypes.byref(s), ctypes.byref(router), ctypes.byref(b), _ptr(x), _ptr(logits), *rest))
         return grads
+
+    def block(self, bw: Dict[str, torch.Tensor], x: torch.Tensor, r: Dict[str, torch.Tensor],
+              y_routes: torch.Tensor, dz: Optional[torch.Tensor], dh_next: Optional[torch.Tensor],
+              pre_weight: torch.Tensor, post_weight: Optional[torch.Tensor] = None,
+              gate: Optional[torch.Tensor] = None, next_weight: Optional[torch.Tensor] = None, scale: float = 1.0,
+              eps: float = 1e-6, weight_offset: float = 0.0, dropout: float = 0.0,
+              rng: Optional[torch.Tensor] = None, router: Optional[_lib.MoeRouter] = None
+              ) -> Dict[str, Optional[torch.Tensor]]:
+        """The gradients of ``MoELayer.block(..., train=True)``, which returned ``r``,
+        for gradients ``dz`` of its z and ``dh_next`` of its h_next: the layer's, with
+        dx that of the block's x, and dpre_weight, dpost_weight, dgate, dnext_weight."""
+        opts = dict(eps=eps, weight_offset=weight_offset)
+        out = block_norm_backward(r["z"], r["out"], dz, dh_next, post_weight=post_weight, gate=gate,
+                                  pre_weight=next_weight, scale=scale, dropout=dropout, rng=rng, **opts)
+        grads = self(bw, r["h"], r["idx"], r["gate"], r, y_routes, out["dy"], router=router,
+                     logits=None if router is None else r["logits"])
+        into = block_norm_backward(x, None, out["dx"], grads["dx"], pre_weight=pre_weight, **opts)
+        return {**grads, "dx": into["dx"], "dpre_weight": into["dpre_weight"], "dpost_weight": out["dpost_weight"],
+                "dgate": out["dgate"], "dnext_weight": out["dpre_weight"]}
 
     def device_error(self) -> int:
         torch.cuda.current_stream(self.device).synchronize()

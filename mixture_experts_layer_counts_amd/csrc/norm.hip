@@ -5,12 +5,13 @@
 //
 // One pass over the rows: a row stays in the registers of the threads that read
 // it (8 or 16 values each, one to sixteen waves a row) between its sums and its
-// results, and the next row's values are asked for before this row's sums.  The
-// parameters stay in registers over the rows of a thread.  The forward runs at
-// the rate of a copy; in the backward vector arithmetic (one operation for every
-// value of 8192 x 7168 takes 1.5 us) comes close to the memory's time, and
-// Philox's products alone are some 35 operations a value.  The backward needs no statistics from the forward: it reads z and y
-// whole anyway, and forms their sums beside its own.  With a = w_pre dh:
+// results.  In the forward the parameters stay there too, and the next row's
+// values are asked for before this row's sums: it runs at the rate of a copy
+// (8192 x 7168, x fp32: 147 to 162 us, 4.3 to 4.8 TB/s).  In the backward vector
+// arithmetic (one operation for every value of 8192 x 7168 takes 1.5 us) comes
+// close to the memory's time; Philox's products alone are some 35 operations a
+// value.  It needs no statistics from the forward: it reads z and y whole anyway,
+// and forms their sums beside its own.  With a = w_pre dh:
 //
 //   dz' = dz + r_z (a - z r_z^2 mean(a z)),   r = 1 / sqrt(mean v^2 + eps)
 //   dn = scale drop'(dz'),  dgate = sum_rows dn N(y) w_post,  b = dn gate w_post
