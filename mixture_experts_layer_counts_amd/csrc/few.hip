@@ -57,7 +57,7 @@ namespace {
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
 constexpr int kPerCu = 2;     // workgroups of a compute unit
 constexpr int kStageB = 128;  // bytes of a row per K stage
-constexpr int kDownCols = 32, kRouterRows = 32;  // of an item
+constexpr int kRouterRows = 32;  // of an item
 constexpr int kCombCols = 32;    // of a combine item, at least
 constexpr int kErrPipeline = 0x8;     // MOE_DEVERR_PIPELINE
 constexpr int kFewSpinCap = 1 << 20;  // polls of about 0.8 us each
@@ -393,7 +393,8 @@ __device__ __forceinline__ void choose(const FewArgs& a, int token, double* c_s,
         const float* part = a.parts + static_cast<int64_t>(token) * E + at;
         float p[kFewParts];
 #pragma unroll
-        for (int j = 0; j < kFewParts; ++j) p[j] = __uint_as_float(get32(part + static_cast<int64_t>(min(j, a.n_parts - 1)) * a.T * E));
+        for (int j = 0; j < kFewParts; ++j)
+          p[j] = j < a.n_parts ? __uint_as_float(get32(part + static_cast<int64_t>(j) * a.T * E)) : 0.f;
         v = p[0];
 #pragma unroll
         for (int j = 1; j < kFewParts; ++j) v += j < a.n_parts ? p[j] : 0.f;
@@ -440,22 +441,31 @@ __device__ __forceinline__ void choose(const FewArgs& a, int token, double* c_s,
     }
   }
   uint64_t kept = ~uint64_t(0);
+  int per = 1;
   if (r.kept_groups < r.groups) {
     settle();
+    // a group by `per` neighbouring lanes
+    while (2 * per * r.groups <= kWave) per *= 2;
+    const int group = lane / per;
     double best = -INFINITY, next = -INFINITY;
-    if (lane < r.groups)
-      for (int e = 0; e < r.group_size; ++e) {
-        const double v = c_s[lane * r.group_size + e];
+    if (group < r.groups)
+      for (int e = lane % per; e < r.group_size; e += per) {
+        const double v = c_s[group * r.group_size + e];
         next = max64(next, min64(best, v));
         best = max64(best, v);
       }
+    for (int d = 1; d < per; d *= 2) {
+      const double ob = __shfl_xor(best, d), on = __shfl_xor(next, d);
+      next = max64(min64(best, ob), max64(next, on));
+      best = max64(best, ob);
+    }
     const double v = r.top2 && r.group_size > 1 ? best + next : best;
     int better = 0;
     for (int o = 0; o < r.groups; ++o) {
-      const double u = __shfl(v, o);
-      better += u > v || (u == v && o < lane);
+      const double u = __shfl(v, o * per);
+      better += u > v || (u == v && o < group);
     }
-    kept = __ballot(lane < r.groups && better < r.kept_groups);
+    kept = __ballot(group < r.groups && better < r.kept_groups);
     settle();  // every lane has read
   }
   // candidates, and this lane's largest
@@ -466,7 +476,7 @@ __device__ __forceinline__ void choose(const FewArgs& a, int token, double* c_s,
     for (int i = 0; i < 4; ++i) {
       const int e = 4 * (kWave * q + lane) + i;
       const double v = c_s[e];
-      const bool in = (kept >> ((__umul24(static_cast<uint32_t>(e), r.group_magic) >> 20) & 63)) & 1;
+      const bool in = (kept >> (((__umul24(static_cast<uint32_t>(e), r.group_magic) >> 20) * per) & 63)) & 1;
       const double key = in && v > -INFINITY ? candidate(v, e) : -INFINITY;
       c_s[e] = key;
       best = max64(best, key);
@@ -779,11 +789,11 @@ __device__ __forceinline__ void finish_up(const FewArgs& a, const FewShared& sh,
   }
 }
 // y of a down item.
-template <int NB>
+template <int M, int NB>
 __device__ __forceinline__ void finish_down(const FewArgs& a, const FewShared& sh, const Part& p, int n0, int parity) {
   const int nb = (p.rows + 15) / 16;
-  for (int q = threadIdx.x; q < 2 * nb * kWave; q += kThreads) {
-    const int l = q & (kWave - 1), m = (q / kWave) & 1, n = q / kWave / 2;
+  for (int q = threadIdx.x; q < M * nb * kWave; q += kThreads) {
+    const int l = q & (kWave - 1), m = (q / kWave) % M, n = q / kWave / M;
     const int c = 16 * n + (l & 15), col = n0 + 16 * m + 4 * (l >> 4);
     if (c >= p.rows) continue;
     put_f4(a.y + static_cast<int64_t>(p.first + c) * a.D + col, wave_total<NB>(sh, parity, m * NB + n, l));
@@ -959,9 +969,9 @@ __device__ __forceinline__ bool products(FewShared& sh, Walk& walk, bool shared,
         finish_up<M, NBW, MX>(a, sh, done, done_n0, parity);
     } else {
       if (narrow)
-        finish_down<1>(a, sh, done, done_n0, parity);
+        finish_down<M, 1>(a, sh, done, done_n0, parity);
       else
-        finish_down<NBW>(a, sh, done, done_n0, parity);
+        finish_down<M, NBW>(a, sh, done, done_n0, parity);
     }
     if (!narrow) __syncthreads();  // its sums take both halves
     walk.pending = a.ctl + (UP ? up_count_at(done.place) : down_count_at(a.E, done_n0 / a.comb_cols));
@@ -970,17 +980,18 @@ __device__ __forceinline__ bool products(FewShared& sh, Walk& walk, bool shared,
 }
 
 // The workgroup's way; false if the launch was stopped.
-template <bool WIDE, bool MXR, bool MXS, int UM>
+template <bool WIDE, bool MXR, bool MXS, int UM, int DM>
 __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
   constexpr int NBW = WIDE ? 4 : 1;
   constexpr bool MXW = MXR || MXS;
-  constexpr int kUpCols = 8 * UM;
+  constexpr int kUpCols = 8 * UM, kDownCols = 16 * DM;
   constexpr int kDepth = UM == 1 ? 8 : 4;  // blocks of 16 rows by a stage that a wave has in flight
   const int tid = static_cast<int>(threadIdx.x);
   // where the items of a kind begin
   const int b_quant = a.w_router ? (a.E + kRouterRows - 1) / kRouterRows * a.n_parts : 0;
   const int b_choose = b_quant + (MXW ? (a.T * (a.D / 128) + kThreads - 1) / kThreads : 0);
-  const int b_build = b_choose + (a.T + kWaves - 1) / kWaves, b_up_s = b_build + 1;
+  const int n_choose = (a.T + kWaves - 1) / kWaves;  // (a single one builds the list itself)
+  const int b_build = b_choose + n_choose, b_up_s = b_build + (n_choose > 1 ? 1 : 0);
   const int b_up = b_up_s + a.Is / kUpCols;
 
   Walk walk{0, 1, 0, 0, nullptr, b_up, 0, 0};
@@ -1007,9 +1018,15 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
         if (wave / slots == turn && token < a.T) choose(a, token, c_s, l_s);
         __syncthreads();
       }
-      signal(a.ctl + kChosen);
-    } else {
-      if (!wait_for(sh, a.ctl, kChosen, b_build - b_choose, a.err)) return false;
+      if (n_choose > 1) {
+        signal(a.ctl + kChosen);
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+      }
+    }
+    if (walk.t == b_up_s - 1) {
+      if (n_choose > 1 && !wait_for(sh, a.ctl, kChosen, n_choose, a.err)) return false;
       build_list(a, sh);
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
@@ -1067,10 +1084,10 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
     const int begin = routed ? b_down : b_down_s, end = routed ? b_combine : b_down;
     if (walk.t >= end) continue;
     if (MXR == MXS || routed) {
-      if (!products<false, MXR, WIDE, 2, kDepth>(sh, walk, !routed, begin, end, (routed ? need_r : need_s) + (MXR ? 1 : 0), A))
+      if (!products<false, MXR, WIDE, DM, DM == 4 ? 8 : kDepth>(sh, walk, !routed, begin, end, (routed ? need_r : need_s) + (MXR ? 1 : 0), A))
         return false;
     } else {
-      if (!products<false, MXS, WIDE, 2, kDepth>(sh, walk, !routed, begin, end, need_s + (MXS ? 1 : 0), A)) return false;
+      if (!products<false, MXS, WIDE, DM, DM == 4 ? 8 : kDepth>(sh, walk, !routed, begin, end, need_s + (MXS ? 1 : 0), A)) return false;
     }
   }
   flush(walk);
@@ -1086,12 +1103,12 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
   return true;
 }
 
-// WIDE: more than 16 tokens.  MXR, MXS: routed and shared experts in MXFP8.  UM:
-// blocks of 16 rows of an up/gate item.
-template <bool WIDE, bool MXR, bool MXS, int UM>
+// WIDE: more than 16 tokens.  MXR, MXS: routed and shared experts in MXFP8.  UM, DM:
+// blocks of 16 rows of an up/gate and of a down item.
+template <bool WIDE, bool MXR, bool MXS, int UM, int DM>
 __global__ __launch_bounds__(kThreads, kPerCu) void few_kernel(const FewArgs a) {
   __shared__ FewShared sh;
-  walk_items<WIDE, MXR, MXS, UM>(a, sh);
+  walk_items<WIDE, MXR, MXS, UM, DM>(a, sh);
   // the last workgroup to leave clears the counters
   const int tid = static_cast<int>(threadIdx.x);
   __syncthreads();
@@ -1108,18 +1125,21 @@ hipError_t run_few(const FewArgs& a, int grid, hipStream_t stream) {
   FewArgs b = a;
   const int64_t experts = std::min<int64_t>(a.E, static_cast<int64_t>(a.T) * a.k) + 1;
   const int e_bytes = MXR ? 1 : 2;
-  const bool fine = experts * (a.I / 16 + a.D / 32) < 8 * grid;
+  const int64_t up = experts * (a.I / 16), down = experts * (a.D / 32);
+  const bool fine = up >= grid && up + down < 8 * grid, long_down = !fine && !WIDE && down > grid && down <= 2 * grid;
   // bytes enough for the draws not to be the limit, while every workgroup has several
   auto batch = [&](int64_t items, int64_t bytes) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(65536 / bytes, items / (4 * grid))));
   };
-  const int um = fine ? 1 : 2;
+  const int um = fine ? 1 : 2, dm = long_down ? 4 : 2;
   b.up_batch = batch(experts * (a.I / (8 * um)), static_cast<int64_t>(16) * um * a.D * e_bytes);
-  b.down_batch = batch(experts * (a.D / kDownCols), static_cast<int64_t>(kDownCols) * a.I * e_bytes);
+  b.down_batch = batch(experts * (a.D / (16 * dm)), static_cast<int64_t>(16) * dm * a.I * e_bytes);
   if (fine)
-    few_kernel<WIDE, MXR, MXS, 1><<<grid, kThreads, 0, stream>>>(b);
+    few_kernel<WIDE, MXR, MXS, 1, 2><<<grid, kThreads, 0, stream>>>(b);
+  else if (long_down)
+    few_kernel<WIDE, MXR, MXS, 2, WIDE ? 2 : 4><<<grid, kThreads, 0, stream>>>(b);
   else
-    few_kernel<WIDE, MXR, MXS, 2><<<grid, kThreads, 0, stream>>>(b);
+    few_kernel<WIDE, MXR, MXS, 2, 2><<<grid, kThreads, 0, stream>>>(b);
   return hipGetLastError();
 }
 
