@@ -615,9 +615,18 @@ def tile_int8(q: torch.Tensor) -> torch.Tensor:
     return tile_mxfp8(q.view(torch.uint8)).view(torch.int8)
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_sizes(T, D, gate_rows, x_dtype, y_dtype, w_dtype, dh_dtype, scale, eps, weight_offset, dropout):
+    n = _lib.MoeNorm()
+    n.T, n.D, n.gate_rows = T, D, gate_rows
+    n.x_dtype, n.y_dtype, n.w_dtype, n.dh_dtype = (_INT8_DTYPES[t] for t in (x_dtype, y_dtype, w_dtype, dh_dtype))
+    n.scale, n.eps, n.weight_offset, n.dropout = scale, eps, weight_offset, dropout
+    return n
+
+
 def _norm_struct(x: torch.Tensor, y: Optional[torch.Tensor], post_weight, gate, pre_weight, scale: float, eps: float,
-                 weight_offset: float, dropout: float, rng, x_name: str) -> _lib.MoeNorm:
-    """The moe_norm of a call, its inputs checked."""
+                 weight_offset: float, dropout: float, rng, x_name: str, dh=None) -> _lib.MoeNorm:
+    """The moe_norm of a call, its inputs checked (not to be changed: calls share it)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{x_name} must be a tensor")
     if x.dim() != 2 or x.dtype not in _INT8_DTYPES or x.device.type != "cuda":
@@ -651,13 +660,9 @@ def _norm_struct(x: torch.Tensor, y: Optional[torch.Tensor], post_weight, gate, 
         if rng is None:
             raise ValueError("dropout needs rng")
         _need(rng, "rng", torch.int64, (2,), dev)
-    n = _lib.MoeNorm()
-    n.T, n.D, n.gate_rows = T, D, 0 if gate is None else gate.shape[0]
-    n.x_dtype = _INT8_DTYPES[x.dtype]
-    n.y_dtype = _lib.DT_BF16 if y is None else _INT8_DTYPES[y.dtype]
-    n.w_dtype = _lib.DT_BF16 if wtype is None else _INT8_DTYPES[wtype]
-    n.scale, n.eps, n.weight_offset, n.dropout = scale, eps, weight_offset, dropout
-    return n
+    return _norm_sizes(T, D, 0 if gate is None else gate.shape[0], x.dtype, torch.bfloat16 if y is None else y.dtype,
+                       torch.bfloat16 if wtype is None else wtype, torch.bfloat16 if dh is None else dh.dtype, scale, eps,
+                       weight_offset, dropout)
 
 
 def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, post_weight: Optional[torch.Tensor] = None,
@@ -693,17 +698,16 @@ def block_norm_backward(z: Optional[torch.Tensor], y: Optional[torch.Tensor], dz
     input.  ``z``: the stream as block_norm returned it (x, where it had no y); the
     other arguments, ``rng``'s values among them, as in that call."""
     lib = _lib.load()
-    n = _norm_struct(z, y, post_weight, gate, pre_weight, scale, eps, weight_offset, dropout, rng, "z")
+    if (dh is None) != (pre_weight is None):
+        raise ValueError("dh and pre_weight come together")
+    if dh is not None and (not isinstance(dh, torch.Tensor) or dh.dtype not in _INT8_DTYPES):
+        raise ValueError("dh must be a bf16 or fp32 tensor")
+    n = _norm_struct(z, y, post_weight, gate, pre_weight, scale, eps, weight_offset, dropout, rng, "z", dh)
     (T, D), dev = z.shape, z.device
     if dz is not None:
         _need(dz, "dz", z.dtype, (T, D), dev)
-    if (dh is None) != (pre_weight is None):
-        raise ValueError("dh and pre_weight come together")
     if dh is not None:
-        if not isinstance(dh, torch.Tensor) or dh.dtype not in _INT8_DTYPES:
-            raise ValueError("dh must be a bf16 or fp32 tensor")
         _need(dh, "dh", dh.dtype, (T, D), dev)
-        n.dh_dtype = _INT8_DTYPES[dh.dtype]
     nbytes = ctypes.c_size_t(0)
     _lib.check("moe_block_norm_backward_workspace_bytes",
                lib.moe_block_norm_backward_workspace_bytes(ctypes.byref(n), ctypes.byref(nbytes)))

@@ -400,7 +400,12 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) b[c][i] = r.at(i);
       }
-      if (a.y) y[c] = load8<YF>(row_of(a.y, t, YF), d[c].d);
+      if (a.post || a.gate) {
+        y[c] = load8<YF>(row_of(a.y, t, YF), d[c].d);
+      } else {
+#pragma unroll
+        for (uint32_t& w : y[c].w) w = 0;  // dy does not depend on y
+      }
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
