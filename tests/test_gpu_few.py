@@ -183,6 +183,76 @@ def test_router_matches_the_standalone_one():
         assert torch.equal(idx, r["idx"]) and torch.equal(gate, r["gate"])
 
 
+def test_odd_logits():
+    """Given logits with ties, infinities, NaN and the type's lowest value: the choice and gates of moe_route_scored."""
+    dev = need_gpu()
+    low = torch.finfo(torch.float32).min
+    for E, k, kw in ((40, 6, dict(score="sigmoid", groups=4, kept_groups=2)), (300, 16, dict(score="softmax")),
+                     (700, 3, dict(score="softmax", renorm=False)), (64, 8, dict(groups=64, kept_groups=8, group_score="max"))):
+        c = Case(dev, 12, 64, 64, E, k, seed=E)
+        lg = torch.randn((12, E), generator=torch.Generator().manual_seed(E))
+        lg[1] = lg[1].round()
+        lg[2, ::3] = -float("inf")
+        lg[3, 1::2] = float("nan")
+        lg[4, 5:] = low
+        lg[5] = -float("inf")
+        lg[6] = 0.0
+        lg[7, 7] = float("inf")
+        lg = lg.to(dev)
+        bias = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(2)).to(dev)
+        for b in (None, bias):
+            r = c.layer.few(c.x, None, c.weights, logits=lg, router=router_for(**kw), bias=b)
+            assert c.layer.device_error() == 0x4  # MOE_DEVERR_NONFINITE
+            _, idx, gate = c.layer.route(None, None, lg, router=router_for(**kw), bias=b)
+            assert torch.equal(idx, r["idx"]) and torch.equal(gate, r["gate"])
+
+
+def test_two_at_once():
+    """Calls of two layers on two streams, and a captured one replayed beside eager calls of its own layer."""
+    dev = need_gpu()
+    a, b = Case(dev, 5, 1472, 320, 50, 6, 704, seed=1), Case(dev, 40, 512, 256, 30, 4, seed=2, tiled=True)
+    want = [c.layer.few(c.x, c.w_router, c.weights) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.layer.few(c.x, c.w_router, c.weights))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for r in got[i]:
+            assert all(torch.equal(r[n], want[i][n]) for n in r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = a.layer.few(a.x, a.w_router, a.weights)
+    for i in range(4):
+        a.x.mul_(-1.5)
+        graph.replay()
+        w = a.layer.few(a.x, a.w_router, a.weights)
+        torch.cuda.synchronize()
+        assert all(torch.equal(r[n], w[n]) for n in r)
+    assert a.layer.device_error() == 0 and b.layer.device_error() == 0
+
+
+def test_tokens_do_not_meet():
+    """A token's results are the same bits whatever the call's other tokens are, an infinity among them too."""
+    dev = need_gpu()
+    c = Case(dev, 20, 256, 128, 16, 4, seed=4)
+    r = c.layer.few(c.x, c.w_router, c.weights)
+    one = MoELayer(shape_for(1, 256, 128, 16, 4), device=dev)
+    for t in (0, 7, 19):
+        s = one.few(c.x[t:t + 1].contiguous(), c.w_router, c.weights)
+        assert all(torch.equal(r[n][t:t + 1], s[n]) for n in r)
+    c.x[3, 100] = float("inf")
+    q = c.layer.few(c.x, c.w_router, c.weights)
+    rest = [t for t in range(20) if t != 3]
+    assert all(torch.equal(r[n][rest], q[n][rest]) for n in r)
+    assert not torch.isfinite(q["out32"][3]).any()
+    z = MoELayer(shape_for(0, 256, 128, 16, 4), device=dev).few(c.x[:0], c.w_router, c.weights)
+    assert z["out"].shape == (0, 256)
+
+
 def test_refusals():
     dev = need_gpu()
     c = Case(dev, 4, 128, 64, 8, 2)
@@ -196,3 +266,6 @@ def test_refusals():
     x = torch.zeros((65, 128), dtype=torch.bfloat16, device=dev)
     with pytest.raises(RuntimeError, match="UNSUPPORTED"):
         big.few(x, c.w_router, c.weights)
+    shifted = torch.zeros(4 * 128 + 1, dtype=torch.bfloat16, device=dev)[1:].view(4, 128)  # not 16-byte aligned
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):
+        c.layer.few(shifted, c.w_router, c.weights)
