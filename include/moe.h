@@ -18,8 +18,11 @@
  *   moe_forward   shared expert, then per minibatch of b routed rows: gather
  *                 into the ring buffer, grouped up/gate GEMM with SwiGLU,
  *                 grouped down GEMM; then the fixed-order gate-weighted combine.
+ * or, for at most MOE_FEW_TOKENS tokens, in one (moe_few); with the norms, gate,
+ * dropout and residual sum around the layer as moe_block_norm,
  * and, for training on one GPU, the backward pass of such a forward
- * (moe_backward_prepare once per weight set, then moe_backward).
+ * (moe_backward_prepare once per weight set, then moe_backward; for the norms
+ * moe_block_norm_backward).
  *
  * Conventions for every entry point:
  *   - Tensor pointers are DEVICE pointers, allocated and owned by the caller;

@@ -661,8 +661,8 @@ def _norm_struct(x: torch.Tensor, y: Optional[torch.Tensor], post_weight, gate, 
             raise ValueError("dropout needs rng")
         _need(rng, "rng", torch.int64, (2,), dev)
     return _norm_sizes(T, D, 0 if gate is None else gate.shape[0], x.dtype, torch.bfloat16 if y is None else y.dtype,
-                       torch.bfloat16 if wtype is None else wtype, torch.bfloat16 if dh is None else dh.dtype, scale, eps,
-                       weight_offset, dropout)
+                       torch.bfloat16 if wtype is None else wtype, torch.bfloat16 if dh is None else dh.dtype,
+                       float(scale), float(eps), float(weight_offset), float(dropout))
 
 
 def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, post_weight: Optional[torch.Tensor] = None,

@@ -7,7 +7,8 @@
 // standing still between launches, and weights that are not yet asked for.  So
 // the work is cut into items in one order,
 //
-//   router rows | x in MXFP8 | choice of 4 tokens | list of experts |
+//   router rows | x in MXFP8 | choice of 4 tokens and, behind the last, the list
+//   of experts (by the choice's own item where there is one only) |
 //   shared up/gate | routed up/gate, expert by expert | (h in MXFP8) |
 //   shared down | routed down, expert by expert | combine
 //
@@ -20,9 +21,9 @@
 // while the tokens are routed, and an expert's down projection comes one pass
 // over the experts after its up/gate.
 //
-// An item of a product is 32 weight rows (of up/gate: 16 gate rows and the 16 up
-// rows of the same columns, so that SwiGLU needs no other item) by all tokens of
-// one expert: four waves share out K in stages of 128 bytes, weights and tokens
+// An item of a product is 16 M weight rows (of up/gate: 8 M gate rows and the
+// 8 M up rows of the same columns, so that SwiGLU needs no other item) by all
+// tokens of one expert, M = 1 to 4 by the rule at run_few: four waves share out K in stages of 128 bytes, weights and tokens
 // go straight from memory to the matrix core (v_mfma_f32_16x16x32_bf16, or
 // v_mfma_scale_f32_16x16x128_f8f6f4) with the weights as row operand, and the
 // waves' sums meet in LDS in a fixed order.  The first stages of the next item's
@@ -41,6 +42,15 @@
 // an XCD's whole cache back); an atomic on one address takes 11.5 ns, one after
 // the other, which is what bounds the number of items.  The last workgroup to
 // leave clears the counters for the next call.
+//
+// Measured (bf16, top 8, weights read once, from x to out): 7168 x 2048 and 256
+// experts, one token, 797 MB in 192 us (4.2 TB/s; MXFP8 404 MB in 157 us); eight
+// tokens 5.2 GB in 720 us (7.2 TB/s); 2048 x 768 and 128 experts, one token, 86 MB
+// in 66 us and 64 tokens, 1.2 GB in 293 us (4.1 TB/s).  With many tokens the bound
+// is memory.  With one it is the phases' chain: about 20 us until the list is
+// there, 30 us for a workgroup's first item of a kind (cold code, cold memory) and
+// 7 to 17 for a later one.  Two workgroups of a compute unit: three or four take
+// 248 to 284 us where two take 195, their counters' traffic growing with them.
 
 #include <algorithm>
 
@@ -985,7 +995,11 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
   constexpr int NBW = WIDE ? 4 : 1;
   constexpr bool MXW = MXR || MXS;
   constexpr int kUpCols = 8 * UM, kDownCols = 16 * DM;
-  constexpr int kDepth = UM == 1 ? 8 : 4;  // blocks of 16 rows by a stage that a wave has in flight
+  // Blocks of 16 rows by a stage that a wave has in flight.  Eight pay where a
+  // workgroup has few items (2048 x 768, one token: 71 us; four: 80), four where it
+  // has many and the code is short of registers (64 tokens: 303; eight: 331).
+  constexpr int kDepth = UM == 1 ? 8 : 4;
+  constexpr int kDownDepth = DM == 4 ? 8 : kDepth;
   const int tid = static_cast<int>(threadIdx.x);
   // where the items of a kind begin
   const int b_quant = a.w_router ? (a.E + kRouterRows - 1) / kRouterRows * a.n_parts : 0;
@@ -1084,10 +1098,10 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
     const int begin = routed ? b_down : b_down_s, end = routed ? b_combine : b_down;
     if (walk.t >= end) continue;
     if (MXR == MXS || routed) {
-      if (!products<false, MXR, WIDE, DM, DM == 4 ? 8 : kDepth>(sh, walk, !routed, begin, end, (routed ? need_r : need_s) + (MXR ? 1 : 0), A))
+      if (!products<false, MXR, WIDE, DM, kDownDepth>(sh, walk, !routed, begin, end, (routed ? need_r : need_s) + (MXR ? 1 : 0), A))
         return false;
     } else {
-      if (!products<false, MXS, WIDE, DM, DM == 4 ? 8 : kDepth>(sh, walk, !routed, begin, end, need_s + (MXS ? 1 : 0), A)) return false;
+      if (!products<false, MXS, WIDE, DM, kDownDepth>(sh, walk, !routed, begin, end, need_s + (MXS ? 1 : 0), A)) return false;
     }
   }
   flush(walk);
@@ -1127,7 +1141,14 @@ hipError_t run_few(const FewArgs& a, int grid, hipStream_t stream) {
   const int e_bytes = MXR ? 1 : 2;
   const int64_t up = experts * (a.I / 16), down = experts * (a.D / 32);
   const bool fine = up >= grid && up + down < 8 * grid, long_down = !fine && !WIDE && down > grid && down <= 2 * grid;
-  // bytes enough for the draws not to be the limit, while every workgroup has several
+  // Rows of an item.  `fine`, 16 of up/gate: short items where a workgroup has some
+  // but not many, so that the rounds end evenly (7168 x 2048, one token: 195 us; 32
+  // rows 212).  With many, or with less than a round of them, 32 (2048 x 768, 64
+  // tokens: 314; 16 rows 352.  One token: 66.5; 16 rows 69.5).  `long_down`, 64 of
+  // down: where 32 would make between one round and two, 64 makes one (2048 x 768,
+  // one token: 66.5; 32 rows 73.6).  Not with more than 16 tokens, whose sums take
+  // the registers.
+  // Items of a draw: bytes enough for the draws not to be the limit, while every workgroup has several
   auto batch = [&](int64_t items, int64_t bytes) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(65536 / bytes, items / (4 * grid))));
   };

@@ -347,3 +347,15 @@ def test_refusals():
     narrow = torch.zeros((6, 7), dtype=BF, device=dev)
     with pytest.raises(RuntimeError, match="UNSUPPORTED"):
         block_norm(narrow, None, pre_weight=torch.ones(7, dtype=BF, device=dev))
+
+
+def test_scale_of_a_tensor_is_read_at_each_call():
+    dev = need_gpu()
+    x = torch.randn((4, 64), generator=torch.Generator().manual_seed(1)).to(dev)
+    y = torch.randn((4, 64), generator=torch.Generator().manual_seed(2)).to(dev)
+    scale = torch.tensor(1.0)
+    one, _ = block_norm(x, y, scale=scale)
+    scale.fill_(2.0)
+    two, _ = block_norm(x, y, scale=scale)
+    assert torch.equal(one, x + y)
+    assert torch.equal(two, torch.addcmul(x.double(), y.double(), torch.tensor(2.0, dtype=torch.float64, device=dev)).float())
