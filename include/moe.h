@@ -574,9 +574,9 @@ typedef struct {
   int32_t y_dtype;   /* of y and dy */
   int32_t w_dtype;   /* of w_post, w_pre and gate */
   int32_t dh_dtype;  /* of dh (backward) */
-  double scale;      /* finite */
-  double eps;        /* finite, >= 0 */
-  double weight_offset; /* finite; 1 for weights stored as their difference to 1 */
+  double scale;      /* scale / (1 - dropout) finite in fp32 */
+  double eps;        /* >= 0, finite in fp32 */
+  double weight_offset; /* finite in fp32; 1 for weights stored as their difference to 1 */
   double dropout;    /* 0 <= dropout < 1 */
 } moe_norm;
 #define MOE_NORM_MAX_COLUMNS 16384

@@ -1260,9 +1260,10 @@ static moe_status norm_sizes(const moe_norm* n) {
   if (n->gate_rows > 0 && n->T % n->gate_rows) return MOE_ERR_INVALID_ARG;
   for (const int32_t t : {n->x_dtype, n->y_dtype, n->w_dtype, n->dh_dtype})
     if (t != MOE_DT_BF16 && t != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
-  if (!std::isfinite(n->scale) || !std::isfinite(n->eps) || n->eps < 0 || !std::isfinite(n->weight_offset))
-    return MOE_ERR_INVALID_ARG;
-  if (!(n->dropout >= 0 && n->dropout < 1)) return MOE_ERR_INVALID_ARG;
+  if (!(n->dropout >= 0 && n->dropout < 1) || !(n->eps >= 0)) return MOE_ERR_INVALID_ARG;
+  // (finite as the kernels take them, in fp32)
+  for (const double v : {n->scale / (1.0 - n->dropout), n->eps, n->weight_offset})
+    if (!std::isfinite(static_cast<float>(v))) return MOE_ERR_INVALID_ARG;
   if (n->D < 8 || n->D > MOE_NORM_MAX_COLUMNS) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -308,7 +308,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
 // A row is one chain of loads, two reductions and stores, and a compute unit's
 // registers hold one row of 7168 with sixteen waves: nothing is read ahead, and the
 // parameters are read again from the caches for every row, so that nothing spills
-// (8192 x 7168 in bf16, dh fp32, with dropout: 277 us in all; 405 with eight waves of
+// (8192 x 7168 in bf16, dh fp32, with dropout: 266 us in all; 405 with eight waves of
 // 16 values a thread that kept parameters and the next row in registers).
 template <bool XF, bool YF, bool HF, int CH, bool TAIL>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormArgs a) {

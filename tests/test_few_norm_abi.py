@@ -122,3 +122,8 @@ def test_norm_arguments(lib):
     assert forward(lib, norm(dropout=0.1)) == -1
     # no rows
     assert forward(lib, norm(T=0), x=None, y=None, z=None, h=None) == 0
+
+
+def test_norm_numbers_beyond_fp32(lib):
+    for kw in (dict(scale=1e39), dict(scale=3e38, dropout=0.5), dict(eps=1e39), dict(weight_offset=-1e39)):
+        assert forward(lib, norm(**kw), rng=P(7 * BIG) if "dropout" in kw else None) == -1, kw
