@@ -176,8 +176,12 @@ typedef struct {
  * Returns MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED for a bad shape. */
 moe_status moe_workspace_bytes(const moe_shape* shape, size_t* bytes);
 
-/* Clear the workspace's sticky error word and, for shapes moe_few serves, its
- * counters (small kernels on `stream`). */
+/* Clear the workspace's sticky error word and moe_few's counters (one small
+ * kernel on `stream`).  Both lie in the first MOE_WORKSPACE_HEAD_BYTES bytes of
+ * every shape's workspace, where no call puts anything else: calls of several
+ * shapes may share one workspace of the largest one's size, in stream order,
+ * and one initialisation, by any of the shapes, serves them all. */
+#define MOE_WORKSPACE_HEAD_BYTES 75520
 moe_status moe_workspace_init(const moe_shape* shape, void* ws, size_t ws_bytes, void* stream);
 
 /*
@@ -351,7 +355,8 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* weights, const
  *   out        [T, D] bf16 out: RNE of out32
  *   out32      [T, D] fp32 out, or NULL
  *   ws         the layer's workspace; moe_workspace_init must have run on it
- *              once (it clears the counters, which every call leaves cleared)
+ *              once, by any shape (it clears the counters, which every call
+ *              leaves cleared)
  * One GPU (num_src_ranks == 1); MOE_BF16 or MOE_MXFP8 experts, row-major or
  * K-tiled (MOE_INT8, T > MOE_FEW_TOKENS or num_src_ranks > 1:
  * MOE_ERR_UNSUPPORTED).  minibatch_rows, ring_rows and pipeline are not used.

@@ -68,21 +68,29 @@ constexpr int kWaves = 4, kThreads = kWaves * kWave;
 constexpr int kPerCu = 2;     // workgroups of a compute unit
 constexpr int kStageB = 128;  // bytes of a row per K stage
 constexpr int kRouterRows = 32;  // of an item
-constexpr int kCombCols = 32;    // of a combine item, at least
+constexpr int kCombCols = 64;    // of a combine item, at least
 constexpr int kErrPipeline = 0x8;     // MOE_DEVERR_PIPELINE
 constexpr int kFewSpinCap = 1 << 20;  // polls of about 0.8 us each
 
-// Words of the control block, apart by a cache line.
+// Words of the control block, apart by a cache line.  Its place in the workspace
+// and that of every word in it are the same for all shapes: calls of several
+// shapes may share a workspace, and what they leave cleared stays where the next
+// one looks.
 constexpr int kTicket = 0, kExit = 64, kRouted = 128, kChosen = 192, kAbort = 256, kCounts = 320;
-__host__ __device__ inline int up_count_at(int a) { return kCounts + a; }  // a: place among the active experts; E: shared
-__host__ __device__ inline int down_count_at(int E, int block) { return kCounts + E + 1 + block; }  // block: of combine
+constexpr int kMaxExperts = 1024, kMaxWidth = 65536;
+__host__ __device__ constexpr int up_count_at(int a) { return kCounts + a; }  // a: place among the active experts; E: shared
+__host__ __device__ constexpr int down_count_at(int block) { return kCounts + kMaxExperts + 1 + block; }  // block: of combine
 
 // "The list is there", a word for every workgroup: hundreds that poll one word
 // hold up the counters beside it.  Each clears its own.
 constexpr int kFewGrid = 256 * kPerCu, kFlagStride = 32;
-__host__ __device__ inline int flags_at(int E, int D) {
-  return (down_count_at(E, D / kCombCols) + kFlagStride - 1) / kFlagStride * kFlagStride;
-}
+constexpr int kFlags = (down_count_at(kMaxWidth / kCombCols) + kFlagStride - 1) / kFlagStride * kFlagStride;
+static_assert(kFlags + kFewGrid * kFlagStride == kFewCtlInts, "the block's size");
+
+// A draw, as it is used at most: no item of a call lies past it (1024 experts, 65536
+// columns by 8), and its batches of at most 64 items stay below 2^31.  So an item is
+// never in front of the first one, whatever the workspace holds.
+constexpr uint32_t kMaxDraw = 1u << 24;
 
 // The list of active experts in the workspace: their number, ids, first
 // positions and the routes by position (expert by expert, then by route).
@@ -884,6 +892,7 @@ __device__ __forceinline__ void ask(const FewArgs& a, Walk& w) {
 }
 // The item of a draw.
 __device__ __forceinline__ void resolve(const FewArgs& a, Walk& w, int v) {
+  v = static_cast<int>(min(static_cast<uint32_t>(v), kMaxDraw));
   w.t = v;
   w.left = 1;
   if (v < w.b_up || w.b_after == 0) return;
@@ -984,7 +993,7 @@ __device__ __forceinline__ bool products(FewShared& sh, Walk& walk, bool shared,
         finish_down<M, NBW>(a, sh, done, done_n0, parity);
     }
     if (!narrow) __syncthreads();  // its sums take both halves
-    walk.pending = a.ctl + (UP ? up_count_at(done.place) : down_count_at(a.E, done_n0 / a.comb_cols));
+    walk.pending = a.ctl + (UP ? up_count_at(done.place) : down_count_at(done_n0 / a.comb_cols));
     if (!more) return true;
   }
 }
@@ -1108,7 +1117,7 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
   while (walk.t < walk.b_end) {
     ask(a, walk);
     const int block = walk.t - b_combine;
-    if (!wait_for(sh, a.ctl, down_count_at(a.E, block), (A + 1) * (a.comb_cols / kDownCols), a.err)) return false;
+    if (!wait_for(sh, a.ctl, down_count_at(block), (A + 1) * (a.comb_cols / kDownCols), a.err)) return false;
     combine(a, sh, block * a.comb_cols, a.comb_cols);
     tell(sh, walk);
     __syncthreads();
@@ -1129,8 +1138,8 @@ __global__ __launch_bounds__(kThreads, kPerCu) void few_kernel(const FewArgs a) 
   if (tid == 0) sh.flag = __hip_atomic_fetch_add(a.ctl + kExit, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (sh.flag == static_cast<int>(gridDim.x) - 1) {
-    const int n = down_count_at(a.E, a.D / kCombCols);
-    for (int i = tid; i < n; i += kThreads) put32(a.ctl + i, 0);
+    const int counts = kCounts + a.E + 1, n = counts + a.D / a.comb_cols;
+    for (int i = tid; i < n; i += kThreads) put32(a.ctl + (i < counts ? i : down_count_at(i - counts)), 0);
   }
 }
 
@@ -1166,19 +1175,18 @@ hipError_t run_few(const FewArgs& a, int grid, hipStream_t stream) {
 
 }  // namespace
 
-int few_ctl_ints(int E, int D) { return flags_at(E, D) + kFewGrid * kFlagStride; }
 int few_list_ints(int E, int routes) { return list_order(E) + routes; }
 
 hipError_t launch_few(const FewArgs& args, bool mx_routed, bool mx_shared, hipStream_t stream) {
   FewArgs a = args;
-  if (a.T < 1 || a.T > kFewTokens || a.k < 1 || a.k > 16 || a.E < a.k || a.E > 1024 || a.D % 64 || a.I % 64 ||
-      a.Is % 64 || a.router.groups > kMaxGroups || a.E % a.router.groups)
+  if (a.T < 1 || a.T > kFewTokens || a.k < 1 || a.k > 16 || a.E < a.k || a.E > kMaxExperts || a.D % 64 || a.I % 64 ||
+      a.Is % 64 || a.D > kMaxWidth || a.router.groups > kMaxGroups || a.E % a.router.groups)
     return hipErrorInvalidValue;
   if ((mx_routed || mx_shared) && a.D % 128) return hipErrorInvalidValue;
   if ((mx_routed && a.I % 128) || (mx_shared && a.Is % 128)) return hipErrorInvalidValue;
   a.router.group_size = a.E / a.router.groups;
   a.router.group_magic = (1u << 20) / static_cast<uint32_t>(a.router.group_size) + 1;  // exact for e < 1024
-  a.flags = a.ctl + flags_at(a.E, a.D);
+  a.flags = a.ctl + kFlags;
   const int64_t cus = device_compute_units();
   const int grid = static_cast<int>(std::min<int64_t>(kFewGrid, kPerCu * (cus > 0 ? cus : 256)));
   // K parts of a router row: 16 stages of 64 values or so

@@ -380,6 +380,7 @@ hipError_t launch_pack_mx_scales(const uint8_t* scale, int64_t groups, int64_t r
 // ---- the layer for a few tokens in one launch (few.hip) ----
 constexpr int kFewTokens = 64;
 constexpr int kFewParts = 8;  // K parts of the router's rows, at most
+constexpr int kFewCtlInts = 18784;  // of the control block, for every shape
 struct FewWeights {
   const void *gate, *up, *down;  // bf16 or E4M3, row-major or K-tiled
   const uint8_t *s_gate, *s_up, *s_down;  // E4M3: stage-major scales
@@ -398,7 +399,7 @@ struct FewArgs {
   RouterArgs router;
   int T, D, I, Is, E, k;
   // workspace
-  int32_t* ctl;   // few_ctl_ints words, 0 before the first call
+  int32_t* ctl;   // kFewCtlInts words, 0 before the first call
   int32_t* list;  // few_list_ints words
   void* h;        // T k I + T Is values of 4 bytes
   float* y;       // [T k + T][D]
@@ -412,7 +413,6 @@ struct FewArgs {
   // set by the launcher, with flags: K parts, columns of a combine item, items of a draw
   int n_parts, comb_cols, up_batch, down_batch;
 };
-int few_ctl_ints(int E, int D);
 int few_list_ints(int E, int routes);
 hipError_t launch_few(const FewArgs& a, bool mx_routed, bool mx_shared, hipStream_t stream);
 

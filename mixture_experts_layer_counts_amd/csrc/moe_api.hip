@@ -34,7 +34,7 @@ struct Layout {
   int max_tiles;
   int routed_bm;      // tile height of the routed GEMMs' tile lists
   int bn_up, bn_down;  // output columns per work item of the routed bf16 GEMMs
-  // moe_few (shapes it serves)
+  // moe_few: its counters, and (shapes it serves) the rest
   size_t few_ctl, few_list, few_h, few_y, few_xq, few_xs, few_hq, few_hs, few_parts;
   size_t pipe_counters;  // pipeline == 1: (3 + max_tiles) * n_minibatches ints, then the work queues
   int64_t y_rows;
@@ -140,7 +140,9 @@ Layout layout_of(const moe_shape* s) {
     off = align_up(off + bytes);
     return at;
   };
+  // at the head of every shape's workspace, so that none of another shape's data lies there
   L.err = take(sizeof(int32_t));
+  L.few_ctl = take(sizeof(int32_t) * moe::kFewCtlInts);
   L.ord_local = take(sizeof(int32_t) * R * NK);
   L.chunk_cnt = take(sizeof(int32_t) * R * moe::sched_chunks(static_cast<int>(NK)) * Lx);
   L.M = take(sizeof(int32_t) * R * Lx);
@@ -195,7 +197,6 @@ Layout layout_of(const moe_shape* s) {
   if (few_shape(s)) {
     const bool mx = s->precision == MOE_MXFP8 || s->shared_precision == MOE_MXFP8;
     const int64_t h_elems = NK * s->I + s->T * s->I_shared;
-    L.few_ctl = take(sizeof(int32_t) * moe::few_ctl_ints(static_cast<int>(s->E_total), static_cast<int>(s->D)));
     L.few_list = take(sizeof(int32_t) * moe::few_list_ints(static_cast<int>(s->E_total), static_cast<int>(NK)));
     L.few_h = take(sizeof(float) * h_elems);
     L.few_y = take(sizeof(float) * (NK + s->T) * s->D);
@@ -740,11 +741,10 @@ moe_status moe_workspace_init(const moe_shape* shape, void* ws, size_t ws_bytes,
   Layout L;
   const moe_status st = check_ws(shape, ws, ws_bytes, &L);
   if (st != MOE_OK) return st;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  MOE_TRY_HIP(moe::launch_clear_int(at<int>(ws, L.err), 1, s));
-  if (!few_shape(shape)) return MOE_OK;
-  return hip_status(moe::launch_clear_int(
-      at<int>(ws, L.few_ctl), moe::few_ctl_ints(static_cast<int>(shape->E_total), static_cast<int>(shape->D)), s));
+  static_assert(MOE_WORKSPACE_HEAD_BYTES == kAlign + (sizeof(int32_t) * moe::kFewCtlInts + kAlign - 1) / kAlign * kAlign,
+                "the error word and moe_few's counters");
+  return hip_status(moe::launch_clear_int(at<int>(ws, L.err), MOE_WORKSPACE_HEAD_BYTES / sizeof(int32_t),
+                                          static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router, float* logits, int32_t* topk_idx,
