@@ -83,7 +83,8 @@ typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_INT8 = 2 } moe_precision;
 #define MOE_DEVERR_ROW_OVERFLOW 0x2 /* routed rows exceed max_rows; extra rows skipped */
 #define MOE_DEVERR_NONFINITE 0x4    /* a router logit is NaN or infinite */
 #define MOE_DEVERR_PIPELINE 0x8     /* a persistent-kernel wait gave up (about 1 s):
-                                       its workgroups were not all resident */
+                                       its workgroups were not all resident; or
+                                       moe_few's workspace needs moe_workspace_init */
 
 /*
  * Sizes and tunables.  On one GPU: num_src_ranks = 1, rank = 0,
@@ -371,8 +372,12 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* weights, const
  * The first call in a process asks the runtime for the current device's
  * compute-unit count; the call can be captured in a HIP graph.  Its workgroups
  * wait for each other in an order in which every wait ends, whatever else the
- * GPU runs (MOE_DEVERR_PIPELINE after about 1 s would mean a workspace that was
- * never initialised; initialise it before it is used again).
+ * GPU runs.  On a workspace that was never initialised a call sets
+ * MOE_DEVERR_PIPELINE (in an error word that nobody cleared) and writes nothing
+ * else outside the workspace.  If something else wrote to the counters, a call may
+ * wait for about 1 s before it gives up and sets that bit; it and later calls then
+ * leave their outputs incomplete or unwritten, each with the bit set, until
+ * moe_workspace_init has run again.
  */
 #define MOE_FEW_TOKENS 64
 moe_status moe_few(const moe_shape* shape, const moe_weights* weights, const moe_router* router, const void* x,

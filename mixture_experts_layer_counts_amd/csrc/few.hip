@@ -76,7 +76,11 @@ constexpr int kFewSpinCap = 1 << 20;  // polls of about 0.8 us each
 // and that of every word in it are the same for all shapes: calls of several
 // shapes may share a workspace, and what they leave cleared stays where the next
 // one looks.
-constexpr int kTicket = 0, kExit = 64, kRouted = 128, kChosen = 192, kAbort = 256, kCounts = 320;
+constexpr int kTicket = 0, kExit = 64, kRouted = 128, kChosen = 192, kState = 256, kCounts = 320;
+// The state word: kReady from the initialisation on, until a call gives up.  A call
+// that finds anything else (bytes never initialised, counters and flags that a call
+// which gave up left behind) reports it and does nothing.
+constexpr uint32_t kReady = 0x6d6f6531u;
 constexpr int kMaxExperts = 1024, kMaxWidth = 65536;
 __host__ __device__ constexpr int up_count_at(int a) { return kCounts + a; }  // a: place among the active experts; E: shared
 __host__ __device__ constexpr int down_count_at(int block) { return kCounts + kMaxExperts + 1 + block; }  // block: of combine
@@ -127,7 +131,7 @@ __device__ __forceinline__ int scalar_of(int v) { return __builtin_amdgcn_readfi
 
 struct FewShared {
   int next[2];  // by the item's parity
-  int flag, n_active;
+  int flag, n_active, ready;
   int wave_sum[kWaves];
   uint16_t id[1024];    // active expert -> expert
   uint16_t start[1025];  // its first position
@@ -146,13 +150,13 @@ __device__ __forceinline__ void signal(int* ctr) {
   if (threadIdx.x == 0) __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Wait for ctl[at] >= target.  It ends without a time limit (see above); the
-// limit is for a workspace that was never initialised, and stops the launch.
+// limit is for counters that something else wrote to, and stops the launch.
 __device__ __forceinline__ bool wait_for(FewShared& sh, int* ctl, int at, int target, int* err) {
   if (threadIdx.x == 0) {
     int ok = 1;
     for (int spins = 0; static_cast<int>(get32(ctl + at)) < target; ++spins) {
-      if ((spins & 63) == 63 && (spins > kFewSpinCap || get32(ctl + kAbort))) {
-        put32(ctl + kAbort, 1);
+      if ((spins & 63) == 63 && (spins > kFewSpinCap || get32(ctl + kState) != kReady)) {
+        put32(ctl + kState, 0);
         raise_error(err, kErrPipeline);
         ok = 0;
         break;
@@ -1018,9 +1022,16 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
   const int b_up = b_up_s + a.Is / kUpCols;
 
   Walk walk{0, 1, 0, 0, nullptr, b_up, 0, 0};
-  if (tid == 0) walk.drawn = draw(a);
+  if (tid == 0) {
+    walk.drawn = draw(a);
+    sh.ready = get32(a.ctl + kState) == kReady;  // (both in flight together)
+  }
   tell(sh, walk);
   __syncthreads();
+  if (!scalar_of(sh.ready)) {
+    if (tid == 0) raise_error(a.err, kErrPipeline);
+    return false;
+  }
   advance(a, sh, walk);
   while (walk.t < b_up_s) {
     ask(a, walk);
@@ -1132,14 +1143,15 @@ template <bool WIDE, bool MXR, bool MXS, int UM, int DM>
 __global__ __launch_bounds__(kThreads, kPerCu) void few_kernel(const FewArgs a) {
   __shared__ FewShared sh;
   walk_items<WIDE, MXR, MXS, UM, DM>(a, sh);
-  // the last workgroup to leave clears the counters
+  // the last workgroup to leave clears the counters (the state stays as it is)
   const int tid = static_cast<int>(threadIdx.x);
   __syncthreads();
   if (tid == 0) sh.flag = __hip_atomic_fetch_add(a.ctl + kExit, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (sh.flag == static_cast<int>(gridDim.x) - 1) {
     const int counts = kCounts + a.E + 1, n = counts + a.D / a.comb_cols;
-    for (int i = tid; i < n; i += kThreads) put32(a.ctl + (i < counts ? i : down_count_at(i - counts)), 0);
+    for (int i = tid; i < n; i += kThreads)
+      if (i != kState) put32(a.ctl + (i < counts ? i : down_count_at(i - counts)), 0);
   }
 }
 
@@ -1174,6 +1186,16 @@ hipError_t run_few(const FewArgs& a, int grid, hipStream_t stream) {
 }
 
 }  // namespace
+
+__global__ void few_init_kernel(int* err, int32_t* ctl) {
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < kFewCtlInts) ctl[i] = i == kState ? static_cast<int32_t>(kReady) : 0;
+  if (i == 0) *err = 0;
+}
+hipError_t launch_few_init(int* err, int32_t* ctl, hipStream_t stream) {
+  few_init_kernel<<<(kFewCtlInts + kThreads - 1) / kThreads, kThreads, 0, stream>>>(err, ctl);
+  return hipGetLastError();
+}
 
 int few_list_ints(int E, int routes) { return list_order(E) + routes; }
 

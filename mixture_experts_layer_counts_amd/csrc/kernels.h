@@ -399,7 +399,7 @@ struct FewArgs {
   RouterArgs router;
   int T, D, I, Is, E, k;
   // workspace
-  int32_t* ctl;   // kFewCtlInts words, 0 before the first call
+  int32_t* ctl;   // kFewCtlInts words, as launch_few_init leaves them before the first call
   int32_t* list;  // few_list_ints words
   void* h;        // T k I + T Is values of 4 bytes
   float* y;       // [T k + T][D]
@@ -413,6 +413,7 @@ struct FewArgs {
   // set by the launcher, with flags: K parts, columns of a combine item, items of a draw
   int n_parts, comb_cols, up_batch, down_batch;
 };
+hipError_t launch_few_init(int* err, int32_t* ctl, hipStream_t stream);
 int few_list_ints(int E, int routes);
 hipError_t launch_few(const FewArgs& a, bool mx_routed, bool mx_shared, hipStream_t stream);
 

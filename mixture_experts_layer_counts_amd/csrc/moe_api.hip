@@ -743,8 +743,8 @@ moe_status moe_workspace_init(const moe_shape* shape, void* ws, size_t ws_bytes,
   if (st != MOE_OK) return st;
   static_assert(MOE_WORKSPACE_HEAD_BYTES == kAlign + (sizeof(int32_t) * moe::kFewCtlInts + kAlign - 1) / kAlign * kAlign,
                 "the error word and moe_few's counters");
-  return hip_status(moe::launch_clear_int(at<int>(ws, L.err), MOE_WORKSPACE_HEAD_BYTES / sizeof(int32_t),
-                                          static_cast<hipStream_t>(stream)));
+  return hip_status(moe::launch_few_init(at<int>(ws, L.err), at<int32_t>(ws, L.few_ctl),
+                                         static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_route(const moe_shape* shape, const void* x, const void* w_router, float* logits, int32_t* topk_idx,
