@@ -361,8 +361,8 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* weights, const
  * One GPU (num_src_ranks == 1); MOE_BF16 or MOE_MXFP8 experts, row-major or
  * K-tiled (MOE_INT8, T > MOE_FEW_TOKENS or num_src_ranks > 1:
  * MOE_ERR_UNSUPPORTED).  minibatch_rows, ring_rows and pipeline are not used.
- * x, w_router, out32 and the weights are 16-byte aligned, out 8-byte, scales
- * and the other outputs 4-byte (MOE_ERR_INVALID_ARG).
+ * x, w_router, out32 and the weights are 16-byte aligned, out 8-byte, scales,
+ * bias and the other outputs 4-byte (MOE_ERR_INVALID_ARG).
  *
  * Values: sums are fp32, in a fixed order; routed outputs are not rounded to
  * bf16 before the combine, and bf16 experts keep 16 bits of h, so results

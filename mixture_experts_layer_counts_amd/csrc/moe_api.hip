@@ -1095,6 +1095,7 @@ moe_status moe_few(const moe_shape* shape, const moe_weights* w, const moe_route
   if (shape->T == 0) return MOE_OK;  // no rows: their pointers may be NULL
   if (!fits({x}, 16) || !fits({out}, 8) || !fits({logits, topk_idx, topk_gate}, 4)) return MOE_ERR_INVALID_ARG;
   if (w_router && reinterpret_cast<uintptr_t>(w_router) % 16) return MOE_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(bias) % 4) return MOE_ERR_INVALID_ARG;
   if (out32 && reinterpret_cast<uintptr_t>(out32) % 16) return MOE_ERR_INVALID_ARG;
   moe::FewArgs a{};
   a.x = static_cast<const uint16_t*>(x);
