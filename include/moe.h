@@ -587,7 +587,7 @@ typedef struct {
   double scale;      /* scale / (1 - dropout) finite in fp32 */
   double eps;        /* >= 0, finite in fp32 */
   double weight_offset; /* finite in fp32; 1 for weights stored as their difference to 1 */
-  double dropout;    /* 0 <= dropout < 1 */
+  double dropout;    /* 0 <= dropout, round(dropout * 2^32) < 2^32 */
 } moe_norm;
 #define MOE_NORM_MAX_COLUMNS 16384
 

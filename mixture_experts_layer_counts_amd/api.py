@@ -654,8 +654,8 @@ def _norm_struct(x: torch.Tensor, y: Optional[torch.Tensor], post_weight, gate, 
             _need(t, n, wtype, (t.shape[0], D), dev)
         else:
             _need(t, n, wtype, (D,), dev)
-    if not 0.0 <= dropout < 1.0:
-        raise ValueError("dropout must be in [0, 1)")
+    if not 0.0 <= dropout < 1.0 - 2.0 ** -33:  # (its threshold among 32-bit words is below 2^32)
+        raise ValueError("dropout must be in [0, 1 - 2^-33)")
     if dropout:
         if rng is None:
             raise ValueError("dropout needs rng")

@@ -1256,12 +1256,15 @@ static bool overlap(const void* p, uint64_t n, const void* q, uint64_t m) {
 }
 static bool aligned_to(const void* p, int64_t size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
 
+static double dropout_threshold(const moe_norm* n) { return std::nearbyint(n->dropout * 4294967296.0); }
+
 static moe_status norm_sizes(const moe_norm* n) {
   if (!n || n->T < 0 || n->T >= (int64_t(1) << 31) || n->D < 1 || n->gate_rows < 0) return MOE_ERR_INVALID_ARG;
   if (n->gate_rows > 0 && n->T % n->gate_rows) return MOE_ERR_INVALID_ARG;
   for (const int32_t t : {n->x_dtype, n->y_dtype, n->w_dtype, n->dh_dtype})
     if (t != MOE_DT_BF16 && t != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
-  if (!(n->dropout >= 0 && n->dropout < 1) || !(n->eps >= 0)) return MOE_ERR_INVALID_ARG;
+  // (a dropout that rounds to 2^32 has no threshold among the words)
+  if (!(n->dropout >= 0 && dropout_threshold(n) < 4294967296.0) || !(n->eps >= 0)) return MOE_ERR_INVALID_ARG;
   // (finite as the kernels take them, in fp32)
   for (const double v : {n->scale / (1.0 - n->dropout), n->eps, n->weight_offset})
     if (!std::isfinite(static_cast<float>(v))) return MOE_ERR_INVALID_ARG;
@@ -1302,8 +1305,7 @@ static moe_status norm_args(const moe_norm* n, const void* x, const void* y, con
   a->offset = static_cast<float>(n->weight_offset);
   a->w_f32 = n->w_dtype == MOE_DT_F32;
   a->drop = n->dropout > 0;
-  const double threshold = std::nearbyint(n->dropout * 4294967296.0);
-  a->threshold = threshold >= 4294967295.0 ? 0xffffffffu : static_cast<uint32_t>(threshold);
+  a->threshold = static_cast<uint32_t>(dropout_threshold(n));
   return MOE_OK;
 }
 

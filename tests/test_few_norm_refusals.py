@@ -1,10 +1,24 @@
 """Calls of moe_few, moe_block_norm and the block that are refused on the host, with what is wrong named (CPU)."""
 
+import ctypes
+
 from mixture_experts_layer_counts_amd import router_for, shape_for
-from tests.test_few_norm_abi import P, few, lib  # noqa: F401
+from tests.test_few_norm_abi import BIG, P, backward, few, forward, lib, norm  # noqa: F401
 
 
 def test_few_misaligned_bias(lib):  # noqa: F811
     s, r = shape_for(T=4, D=128, I=64, E=8, k=2), router_for()
     for at in (1, 2, 3):
         assert few(lib, s, router=r, bias=P(4096 + at)) == -1, at
+
+
+def test_dropout_of_everything(lib):  # noqa: F811
+    """A probability whose threshold is all of 2^32: no 32-bit word reaches it, and none is below it either way."""
+    for p in (1.0 - 2.0 ** -33, 1.0 - 2.0 ** -40, 1.0 - 2.0 ** -53):
+        n = norm(dropout=p)
+        assert forward(lib, n, rng=P(7 * BIG)) == -1, p
+        assert backward(lib, n, rng=P(13 * BIG)) == -1, p
+        assert lib.moe_block_norm_backward_workspace_bytes(ctypes.byref(n), ctypes.byref(ctypes.c_size_t())) == -1
+    # the largest one there is
+    ok = norm(dropout=1.0 - 2.0 ** -32)
+    assert lib.moe_block_norm_backward_workspace_bytes(ctypes.byref(ok), ctypes.byref(ctypes.c_size_t())) == 0
