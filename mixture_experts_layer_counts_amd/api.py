@@ -676,8 +676,9 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, post_weight
     fp32; weights [D] and gate [G, D] (T / G consecutive rows share a row of it) of
     one type; ``weight_offset`` is added to the weights.  ``dropout`` draws its mask
     from ``rng``, int64 [2] on the device (seed and offset), and does not store it."""
-    lib, dev = _lib.load(), x.device
+    lib = _lib.load()
     n = _norm_struct(x, y, post_weight, gate, pre_weight, scale, eps, weight_offset, dropout, rng, "x")
+    dev = x.device
     with _on(dev):
         z = x if y is None else torch.empty_like(x)
         h = None if pre_weight is None else torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
@@ -687,7 +688,7 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, post_weight
     return z, h
 
 
-def block_norm_backward(z: Optional[torch.Tensor], y: Optional[torch.Tensor], dz: Optional[torch.Tensor],
+def block_norm_backward(z: torch.Tensor, y: Optional[torch.Tensor], dz: Optional[torch.Tensor],
                         dh: Optional[torch.Tensor], *, post_weight: Optional[torch.Tensor] = None,
                         gate: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
                         scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0, dropout: float = 0.0,

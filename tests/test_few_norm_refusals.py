@@ -2,7 +2,9 @@
 
 import ctypes
 
-from mixture_experts_layer_counts_amd import router_for, shape_for
+import pytest
+
+from mixture_experts_layer_counts_amd import block_norm, block_norm_backward, router_for, shape_for
 from tests.test_few_norm_abi import BIG, P, backward, few, forward, lib, norm  # noqa: F401
 
 
@@ -22,3 +24,11 @@ def test_dropout_of_everything(lib):  # noqa: F811
     # the largest one there is
     ok = norm(dropout=1.0 - 2.0 ** -32)
     assert lib.moe_block_norm_backward_workspace_bytes(ctypes.byref(ok), ctypes.byref(ctypes.c_size_t())) == 0
+
+
+def test_streams_that_are_no_tensors(lib):  # noqa: F811
+    for v in (None, 1.0, [[0.0] * 8]):
+        with pytest.raises(TypeError, match="x must be a tensor"):
+            block_norm(v)
+        with pytest.raises(TypeError, match="z must be a tensor"):
+            block_norm_backward(v, None, None, None)
