@@ -450,6 +450,8 @@ class MoEBackward:
         """The gradients of ``MoELayer.block(..., train=True)``, which returned ``r``,
         for gradients ``dz`` of its z and ``dh_next`` of its h_next: the layer's, with
         dx that of the block's x, and dpre_weight, dpost_weight, dgate, dnext_weight."""
+        if any(n not in r for n in ("offsets", "sched", "route_dst")):
+            raise ValueError("r has no schedule: it must come from MoELayer.block(..., train=True)")
         opts = dict(eps=eps, weight_offset=weight_offset)
         out = block_norm_backward(r["z"], r["out"], dz, dh_next, post_weight=post_weight, gate=gate,
                                   pre_weight=next_weight, scale=scale, dropout=dropout, rng=rng, **opts)

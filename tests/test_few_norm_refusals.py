@@ -3,8 +3,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from mixture_experts_layer_counts_amd import block_norm, block_norm_backward, router_for, shape_for
+from mixture_experts_layer_counts_amd import MoEBackward, block_norm, block_norm_backward, router_for, shape_for
 from tests.test_few_norm_abi import BIG, P, backward, few, forward, lib, norm  # noqa: F401
 
 
@@ -32,3 +33,11 @@ def test_streams_that_are_no_tensors(lib):  # noqa: F811
             block_norm(v)
         with pytest.raises(TypeError, match="z must be a tensor"):
             block_norm_backward(v, None, None, None)
+
+
+def test_backward_of_a_block_that_kept_nothing(lib):  # noqa: F811
+    x = torch.zeros((4, 64))
+    back = MoEBackward(shape_for(T=4, D=64, I=64, E=8, k=2), device="cpu")
+    few_results = {n: x for n in ("logits", "idx", "gate", "out", "out32", "h", "z", "h_next")}
+    with pytest.raises(ValueError, match="train=True"):
+        back.block({}, x, few_results, x, x, None, pre_weight=x[0])
