@@ -39,8 +39,9 @@ namespace moe {
 
 namespace {
 
-// A 16-byte piece at any alignment of its elements.
-struct __attribute__((packed, aligned(2))) Piece {
+// A 16-byte piece at any alignment of its elements, of rows that are also written
+// by single elements.
+struct __attribute__((packed, aligned(2), may_alias)) Piece {
   uint32_t w[4];
 };
 
