@@ -568,8 +568,10 @@ moe_status moe_linear_int8(const void* x, int32_t x_dtype, int64_t M, int64_t K,
  * layer.  gate [gate_rows, D]: T / gate_rows consecutive rows share one of its rows
  * (1: a learned gate per channel; the batch size: one per sequence; T: one per token).
  * drop keeps an element if its 32 random bits are at least round(dropout * 2^32) and
- * divides what it keeps by 1 - dropout; what it drops adds nothing, an infinity or a
- * NaN neither.  The bits of element (t, d) are word d % 4 of Philox-4x32 of ten
+ * divides what it keeps by 1 - dropout; what it drops adds nothing, without w_post an
+ * infinity or a NaN neither.  (N(y) takes every value of a row, dropped or not: with
+ * w_post an infinity or a NaN anywhere in a row of y reaches that row's z, h and dy and
+ * the parameters' gradients.)  The bits of element (t, d) are word d % 4 of Philox-4x32 of ten
  * rounds at the counter (d / 4, t, offset mod 2^32, offset / 2^32) under the key
  * (seed mod 2^32, seed / 2^32).  The mask is never stored: the backward of a call
  * takes the same seed and offset.

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = n[c][i] * r * wq[c][i] * g[c][i];
-          // (a dropped value adds nothing, whatever it was)
+          // (a dropped value adds nothing, whatever it was; with w_post it is part of r)
           z[c][i] = keep[i] ? fmaf(v, a.factor, z[c][i]) : z[c][i];
         }
       }
@@ -448,7 +448,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float dn = dz[c][i] * a.factor, n = y[c].at(i) * ry;
-        // (a dropped value has no part in the sums, whatever it is)
+        // (a dropped value has no part in these sums, whatever it is; in its row's
+        // statistics, ry and m, it has, as the formulas say)
         S[c][i] = keep[i] ? fmaf(dn, n, S[c][i]) : S[c][i];
         b[c][i] = keep[i] ? dn * g[i] * w[i] : 0.f;
       }

@@ -19,3 +19,35 @@ def test_many_gate_rows_a_run(T, D, G, wt):
     c = Case(dev, T, D, F32, BF, wt, BF, True, G, True, 0.0, seed=T)
     check_forward(c)
     check_backward(c)
+
+
+def test_dropped_values_without_and_with_a_norm():
+    """What dropout drops adds nothing to the sum; but a row that is normalised first takes every value of it into its
+    statistics, dropped or not: an infinity there leaves the row's z at x, a NaN makes its kept values NaN, and the
+    row's dy is not finite.  No other row, and no dx, changes by a bit."""
+    dev = need_gpu()
+    inf, nan = float("inf"), float("nan")
+    for post in (False, True):
+        c = Case(dev, 12, 104, BF, BF, BF, BF, post, 3, True, 0.5, seed=4)
+        z0, h0 = block_norm(c.x, c.y, **c.kw)
+        g0 = block_norm_backward(z0, c.y, c.dz, c.dh, **c.kw)
+        y = c.y.clone()
+        for t, v in ((2, inf), (7, nan)):
+            d = int((~c.keep[t]).nonzero()[5])
+            y[t, d] = v
+        z, h = block_norm(c.x, y, **c.kw)
+        g = block_norm_backward(z0, y, c.dz, c.dh, **c.kw)
+        rest = [t for t in range(12) if t not in (2, 7)]
+        for a, b in ((z, z0), (h, h0), (g["dx"], g0["dx"]), (g["dy"], g0["dy"])):
+            assert torch.equal(a[rest], b[rest])
+        assert torch.equal(g["dx"], g0["dx"]) and torch.equal(g["dpre_weight"], g0["dpre_weight"])
+        if not post:
+            assert torch.equal(z, z0) and torch.equal(h, h0)
+            assert all(torch.equal(g[n], g0[n]) for n in ("dy", "dgate"))
+            continue
+        assert torch.equal(z[2], c.x[2])
+        keep = c.keep[7]
+        assert torch.equal(z[7][~keep], c.x[7][~keep]) and bool(torch.isnan(z[7][keep]).all())
+        assert not torch.isfinite(g["dy"][[2, 7]]).any()
+        # gate rows 0 (tokens 0 .. 3) and 1 (4 .. 7) have such a row, row 2 has none
+        assert torch.equal(g["dgate"][2], g0["dgate"][2])
