@@ -365,7 +365,7 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* weights, const
  * bias and the other outputs 4-byte (MOE_ERR_INVALID_ARG).
  *
  * Values: sums are fp32, in a fixed order; routed outputs are not rounded to
- * bf16 before the combine, and bf16 experts keep 16 bits of h, so results
+ * bf16 before the combine, and bf16 experts keep 17 bits of h, so results
  * differ from moe_forward's by that rounding.  MXFP8 quantises x and h as
  * moe_forward does.  Repeated calls give the same bits.  A token's results do
  * not depend on the other tokens of the call.

@@ -33,7 +33,9 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
 }
 
 // SiLU(g) * u, with the hardware reciprocal (about 1 ulp) in place of a
-// correctly rounded division: the result is rounded to bf16 or E4M3 next.
+// correctly rounded division, and an exponential whose error grows with |g|: some
+// (|g| + 6) 2^-24 in all.  The result is rounded to bf16 or E4M3 next, or kept in
+// two bf16 terms (17 bits; few.hip).
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }

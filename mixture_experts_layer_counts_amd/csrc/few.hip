@@ -29,10 +29,15 @@
 // waves' sums meet in LDS in a fixed order.  The first stages of the next item's
 // weights are asked for before an item's sums meet.
 //
-// Roundings: sums are fp32.  In bf16 h is kept as two bf16 terms (16 bits of
+// Roundings: sums are fp32.  In bf16 h is kept as two bf16 terms (17 bits of
 // it; the second product costs nothing beside the weights' stream), in MXFP8 it
-// is quantised as the layer defines.  Every expert's output stays fp32 until the
-// combine, acc = fma(g_s, y_s, acc) over the slots, then + shared.
+// is quantised as the layer defines.  (The matrix core sums products of 8-bit
+// values less exactly than others: 128 random products of E4M3 come out 1.5e-5 of
+// their sum's RMS off, 2.5e-4 of the largest product at most, by
+// v_mfma_scale_f32_16x16x128 and v_mfma_f32_16x16x32 alike.  So one value of h in
+// 600 falls on the other side of a border between two values of E4M3, here as in
+// moe_forward.)  Every expert's output stays fp32 until the combine,
+// acc = fma(g_s, y_s, acc) over the slots, then + shared.
 //
 // Between workgroups: results that others read are stored past the caches
 // (agent-scope stores), have arrived (vector memory completes in order, and a
@@ -795,14 +800,14 @@ __device__ __forceinline__ void finish_up(const FewArgs& a, const FewShared& sh,
     if constexpr (MX) {
       put_f4(reinterpret_cast<float*>(hr.base) + at, h);
     } else {
-      // h = hi + lo: the upper 8 bits cut off, the rest rounded
+      // h = hi + lo, each to nearest (hi cut off where it would round past the largest float)
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t cut = __float_as_uint(h[i]) & 0xffff0000u;
+        const uint32_t near = f32_to_bf16(h[i]);
         const bool finite = __builtin_isfinite(h[i]);
-        hi[i] = finite ? cut >> 16 : f32_to_bf16(h[i]);
-        lo[i] = finite ? f32_to_bf16(h[i] - __uint_as_float(cut)) : 0u;
+        hi[i] = finite && (near & 0x7fffu) == 0x7f80u ? __float_as_uint(h[i]) >> 16 : near;
+        lo[i] = finite ? f32_to_bf16(h[i] - bf16_to_f32(static_cast<uint16_t>(hi[i]))) : 0u;
       }
       uint16_t* const p16 = reinterpret_cast<uint16_t*>(hr.base) + at;
       put64(p16, hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
