@@ -970,6 +970,7 @@ __device__ __forceinline__ bool products(FewShared& sh, Walk& walk, bool shared,
     const int nb = scalar_of((p.rows + 15) / 16);
     const bool narrow = !WIDE || nb <= 1;
     if (narrow) {
+      // (0 only where something else wrote to the list: no index from it then)
       if (nb > 0) item_sums<1, SPLIT, kCoh>(sh, f, w, UP ? tokens_of<1, MX>(a, sh, p) : hidden_of<1, MX>(a, p), at, nb, walk.parity);
     } else {
       item_sums<NBW, SPLIT, kCoh>(sh, f, w, UP ? tokens_of<NBW, MX>(a, sh, p) : hidden_of<NBW, MX>(a, p), at, nb, walk.parity);
@@ -1166,14 +1167,18 @@ hipError_t run_few(const FewArgs& a, int grid, hipStream_t stream) {
   const int64_t experts = std::min<int64_t>(a.E, static_cast<int64_t>(a.T) * a.k) + 1;
   const int e_bytes = MXR ? 1 : 2;
   const int64_t up = experts * (a.I / 16), down = experts * (a.D / 32);
-  const bool fine = up >= grid && up + down < 8 * grid, long_down = !fine && !WIDE && down > grid && down <= 2 * grid;
+  const bool fine = !WIDE && up >= grid && up + down < 8 * grid;
+  const bool long_down = !fine && !WIDE && down > grid && down <= 2 * grid;
   // Rows of an item.  `fine`, 16 of up/gate: short items where a workgroup has some
   // but not many, so that the rounds end evenly (7168 x 2048, one token: 195 us; 32
-  // rows 212).  With many, or with less than a round of them, 32 (2048 x 768, 64
-  // tokens: 314; 16 rows 352.  One token: 66.5; 16 rows 69.5).  `long_down`, 64 of
-  // down: where 32 would make between one round and two, 64 makes one (2048 x 768,
-  // one token: 66.5; 32 rows 73.6).  Not with more than 16 tokens, whose sums take
-  // the registers.
+  // rows 212).  With many, or with less than a round of them, 32 (2048 x 768, one
+  // token: 66.5; 16 rows 69.5).  More than 16 tokens are read again for every item,
+  // so that twice the items cost more (4096 x 1024, 8 experts: 17 tokens 100 us, 16
+  // rows 115 to 123; 64 tokens 139, 16 rows 171; the same in MXFP8 97 and 121, 136
+  // and 171; 2048 x 1024, 16 experts, 17 tokens, the one that lost: 110, 16 rows 105).
+  // `long_down`, 64 of down: where 32 would make between one round and two, 64 makes
+  // one (2048 x 768, one token: 66.5; 32 rows 73.6).  Not with more than 16 tokens,
+  // whose sums take the registers.
   // Items of a draw: bytes enough for the draws not to be the limit, while every workgroup has several
   auto batch = [&](int64_t items, int64_t bytes) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(65536 / bytes, items / (4 * grid))));
@@ -1181,12 +1186,16 @@ hipError_t run_few(const FewArgs& a, int grid, hipStream_t stream) {
   const int um = fine ? 1 : 2, dm = long_down ? 4 : 2;
   b.up_batch = batch(experts * (a.I / (8 * um)), static_cast<int64_t>(16) * um * a.D * e_bytes);
   b.down_batch = batch(experts * (a.D / (16 * dm)), static_cast<int64_t>(16) * dm * a.I * e_bytes);
-  if (fine)
-    few_kernel<WIDE, MXR, MXS, 1, 2><<<grid, kThreads, 0, stream>>>(b);
-  else if (long_down)
-    few_kernel<WIDE, MXR, MXS, 2, WIDE ? 2 : 4><<<grid, kThreads, 0, stream>>>(b);
-  else
-    few_kernel<WIDE, MXR, MXS, 2, 2><<<grid, kThreads, 0, stream>>>(b);
+  if constexpr (!WIDE) {
+    if (fine || long_down) {
+      if (fine)
+        few_kernel<false, MXR, MXS, 1, 2><<<grid, kThreads, 0, stream>>>(b);
+      else
+        few_kernel<false, MXR, MXS, 2, 4><<<grid, kThreads, 0, stream>>>(b);
+      return hipGetLastError();
+    }
+  }
+  few_kernel<WIDE, MXR, MXS, 2, 2><<<grid, kThreads, 0, stream>>>(b);
   return hipGetLastError();
 }
 
