@@ -1014,11 +1014,12 @@ __device__ __forceinline__ bool walk_items(const FewArgs& a, FewShared& sh) {
   constexpr int NBW = WIDE ? 4 : 1;
   constexpr bool MXW = MXR || MXS;
   constexpr int kUpCols = 8 * UM, kDownCols = 16 * DM;
-  // Blocks of 16 rows by a stage that a wave has in flight.  Eight pay where a
-  // workgroup has few items (2048 x 768, one token: 71 us; four: 80), four where it
-  // has many and the code is short of registers (64 tokens: 303; eight: 331).
-  constexpr int kDepth = UM == 1 ? 8 : 4;
-  constexpr int kDownDepth = DM == 4 ? 8 : kDepth;
+  // Blocks of 16 rows by a stage that a wave has in flight: four, and of items of four
+  // blocks eight, two stages.  Eight for all items of up to 16 tokens gain nothing
+  // (2048 x 768, one token: 66.8 us either way; 1472 x 320, 13 tokens: 108, four 102),
+  // and for items of one block cost registers (7168 x 2048, one token: 190 us, four
+  // 189; in MXFP8 158, four 144).
+  constexpr int kDepth = 4, kDownDepth = DM == 4 ? 8 : kDepth;
   const int tid = static_cast<int>(threadIdx.x);
   // where the items of a kind begin
   const int b_quant = a.w_router ? (a.E + kRouterRows - 1) / kRouterRows * a.n_parts : 0;
