@@ -49,9 +49,10 @@
 // leave clears the counters for the next call.
 //
 // Measured (bf16, top 8, weights read once, from x to out): 7168 x 2048 and 256
-// experts, one token, 797 MB in 192 us (4.2 TB/s; 384 experts in MXFP8 457 MB in 157 us); eight
-// tokens 5.2 GB in 720 us (7.2 TB/s); 2048 x 768 and 128 experts, one token, 86 MB
-// in 66 us and 64 tokens, 1.2 GB in 293 us (4.1 TB/s).  With many tokens the bound
+// experts, one token, 797 MB in 192 us (4.2 TB/s; 384 experts in MXFP8 457 MB in 144
+// us); eight tokens 5.2 GB in 740 to 780 us (6.6 to 7.0 TB/s); 2048 x 768 and 128
+// experts, one token, 86 MB in 65 us and 64 tokens, 1.2 GB in 292 us (4.1 TB/s; in
+// MXFP8 0.62 GB in 223 us).  With many tokens the bound
 // is memory.  With one it is the phases' chain: about 20 us until the list is
 // there, 30 us for a workgroup's first item of a kind (cold code, cold memory) and
 // 7 to 17 for a later one.  Two workgroups of a compute unit: three or four take

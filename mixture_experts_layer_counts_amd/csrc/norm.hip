@@ -7,7 +7,8 @@
 // it (8 or 16 values each, one to sixteen waves a row) between its sums and its
 // results.  In the forward the parameters stay there too, and the next row's
 // values are asked for before this row's sums: it runs at the rate of a copy
-// (8192 x 7168, x fp32: 147 to 162 us, 4.3 to 4.8 TB/s).  In the backward vector
+// (8192 x 7168, x fp32: 162 us, 4.3 TB/s; above 8192 columns, where 19 to 53 registers
+// of a thread spill, 3.0: 4096 x 16384 in bf16 182 us).  In the backward vector
 // arithmetic (one operation for every value of 8192 x 7168 takes 1.5 us) comes
 // close to the memory's time; Philox's products alone are some 35 operations a
 // value.  It needs no statistics from the forward: it reads z and y whole anyway,
@@ -308,9 +309,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a) {
 //
 // A row is one chain of loads, two reductions and stores, and a compute unit's
 // registers hold one row of 7168 with sixteen waves: nothing is read ahead, and the
-// parameters are read again from the caches for every row, so that nothing spills
-// (8192 x 7168 in bf16, dh fp32, with dropout: 257 to 266 us in all; 405 with eight waves of
-// 16 values a thread that kept parameters and the next row in registers).
+// parameters are read again from the caches for every row, so that little spills: 2
+// to 12 registers a thread up to D = 8192, 8 in this case (8192 x 7168 in bf16, dh
+// fp32, with dropout: 257 to 266 us in all; 405 with eight waves of 16 values a thread
+// that kept parameters and the next row in registers).  Above 8192, with two chunks a
+// thread, 71 to 112 spill: 4096 x 16384 takes 456 us, 2.1 TB/s, where 8192 x 8192
+// reaches 3.5 (269 us).
 template <bool XF, bool YF, bool HF, int CH, bool TAIL>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormArgs a) {
   __shared__ float part[2][kMaxWaves][4];

@@ -89,7 +89,8 @@ def test_mxfp8_values(T, scale):
         zero = torch.zeros((64, N), dtype=torch.bfloat16, device=dev)
         w, val = {"ws_gate": zero, "ws_up": zero, "ws_down": zero.t().contiguous()}, {}
         for n, m in (("gate", torch.randn((1, N, N), generator=dg, device=dev) * scale),
-                     ("up", torch.randn((1, N, N), generator=dg, device=dev)), ("down", torch.eye(N, device=dev)[None])):
+                     ("up", torch.randn((1, N, N), generator=dg, device=dev)),
+                     ("down", torch.eye(N, device=dev)[None])):
             w["q_" + n], w["s_" + n], val[n] = mx(m)
         assert torch.equal(val["down"], torch.eye(N, device=dev).double())
         x = tokens(T, N, g, dev)

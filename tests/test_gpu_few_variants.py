@@ -1,19 +1,20 @@
-"""moe_few where test_gpu_few.py does not go, under its bounds: every kernel that the launcher chooses between, with K
-long enough that each wave refills its stages and runs its steady loop, draws of several items, and a router in several
-K parts.  The comments name what run_few's rule makes of a case (grid: 512 workgroups).
+"""moe_few where test_gpu_few.py does not go: every kernel that the launcher chooses between, with K long enough that
+each wave refills its stages and runs its steady loop, draws of several items, and a router in several K parts. The
+comments name what run_few's rule makes of a case (grid: 512 workgroups).
 
 bf16: the bounds of test_gpu_few.py.
 
-MXFP8, with long K: an error per token, of its RMS over the D outputs.  The matrix core's sums of 8-bit products are up to
-2^-12 of a large product off, so 2^-9 of the values of h fall on the other side of a border between two values of E4M3, each
-by a step, at most 2^-3 of itself: RMS(dh) <= 2^-3 sqrt(2^-9) = 2^-7.5 of h's, over many tokens.  In one token a single
-value far above the RMS may be among them, and a block of 32 whose largest value lies at a power of two may take the
-next one: values of one block B then move by at most 2^-3 of themselves (the largest where it is cut off at 448 or
-not), ||dh|| <= 2^-3 ||h_B||.  Such a block is one in 2^9 or so, and a token's expert has 2^6 or 2^7 of them: one is to be
-expected here and there, two at the block of the largest values are not.  w_down's entries are independent of dh and
-of h, of one size: an expert's output y moves by RMS(dy) / RMS(y) = ||dh|| / ||h||, to a few percent (D >= 2048 outputs).
-So a token's error is at most 1.25 sum_s g_s RMS(y_s) (2^-7 + 2^-3 max_B ||h_B|| / ||h||) over its experts, and the shared
-expert as one of gate 1.  A stage of K read from a wrong place, one of n, changes h by sqrt(2 / n), 0.18 of it or more.
+MXFP8, with long K: an error per token, of its RMS over the D outputs. The matrix core's sums of 8-bit products are
+up to 2^-12 of a large product off, so 2^-9 of the values of h fall on the other side of a border between two values
+of E4M3, each by a step, at most 2^-3 of itself: RMS(dh) <= 2^-3 sqrt(2^-9) = 2^-7.5 of h's, over many tokens. In
+one token a single value far above the RMS may be among them, and a block of 32 whose largest value lies at a power
+of two may take the next one: values of one block B then move by at most 2^-3 of themselves (the largest where it is
+cut off at 448 or not), ||dh|| <= 2^-3 ||h_B||. Such a block is one in 2^9 or so, and a token's expert has 2^6 or
+2^7 of them: one is to be expected here and there, two at the block of the largest values are not. w_down's entries
+are independent of dh and of h, of one size: an expert's output y moves by RMS(dy) / RMS(y) = ||dh|| / ||h||, to a
+few percent (D >= 2048 outputs). So a token's error is at most 1.25 sum_s g_s RMS(y_s) (2^-7 + 2^-3 max_B ||h_B|| /
+||h||) over its experts, and the shared expert as one of gate 1. A stage of K read from a wrong place, one of n,
+changes h by sqrt(2 / n), 0.18 of it or more.
 """
 
 import pytest
