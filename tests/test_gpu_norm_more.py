@@ -2,12 +2,13 @@
 rows whose last chunk overlaps, and dropped values in a row that is normalised.
 
 The bounds, counted from the kernels (u = 2^-24): a row's sums are chains of 8 or 17 additions in a thread (one or two
-chunks), 6 steps over a wave and up to 16 waves one after the other, 39 u at most of the sum of absolute values and half
-of it behind the root; with some twenty operations around them below 64 u.  Column sums are chains over a run's rows, then
-over a sixteenth of the runs, then over 16: with 4096 * 64 / lanes runs at most (4096 where a wave has a row, D up to
-512; 256 above 4096 columns) and two rows a run at least, T rows take ceil(T / runs) + ceil(runs / 16) + 15 additions.
-That is 273 at T = 8192 and D up to 512, the closest that it comes to T / 64 + 160 = 288 (142 against 222 at T = 4000, 281
-against 785 at 40000); groups that end inside a run add one addition each where the run's own are fewer.
+chunks), 6 steps over a wave and up to 16 waves one after the other, 39 u at most of the sum of absolute values and
+half of it behind the root; with some twenty operations around them below 64 u. Column sums are chains over a run's
+rows (a run of several groups adds their sums up, with no more additions than rows), then over a sixteenth of the
+runs, then over 16: with 4096 * 64 / lanes runs at most (4096 where a wave has a row, D up to 512; 256 above 4096
+columns) and two rows a run at least, T rows take ceil(T / runs) + ceil(runs / 16) + 15 additions. That comes closest
+to T / 64 + 160 with 273 against 287 at T = 8161 and D up to 512 (142 against 222 at T = 4000, 281 against 785 at
+40000).
 """
 
 import pytest
