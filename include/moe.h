@@ -375,7 +375,7 @@ moe_status moe_forward(const moe_shape* shape, const moe_weights* weights, const
  * GPU runs.  On a workspace that was never initialised a call sets
  * MOE_DEVERR_PIPELINE (in an error word that nobody cleared) and writes nothing
  * else outside the workspace.  If something else wrote to the counters, a call may
- * wait for about 1 s before it gives up and sets that bit; it and later calls then
+ * wait for about half a second before it gives up and sets that bit; it and later calls then
  * leave their outputs incomplete or unwritten, each with the bit set, until
  * moe_workspace_init has run again.
  */

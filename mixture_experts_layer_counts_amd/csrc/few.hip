@@ -76,7 +76,7 @@ constexpr int kStageB = 128;  // bytes of a row per K stage
 constexpr int kRouterRows = 32;  // of an item
 constexpr int kCombCols = 64;    // of a combine item, at least
 constexpr int kErrPipeline = 0x8;     // MOE_DEVERR_PIPELINE
-constexpr int kFewSpinCap = 1 << 20;  // polls of about 0.8 us each
+constexpr int kFewSpinCap = 1 << 20;  // polls of about 0.5 us each
 
 // Words of the control block, apart by a cache line.  Its place in the workspace
 // and that of every word in it are the same for all shapes: calls of several

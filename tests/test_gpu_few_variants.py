@@ -137,3 +137,22 @@ BATCHES = [  # draws of several items
 @pytest.mark.parametrize("T,D,I,E,k,Is,prec,sprec,tiled,router", BATCHES)
 def test_batches(T, D, I, E, k, Is, prec, sprec, tiled, router):
     check(T, D, I, E, k, Is, prec, sprec, tiled, router)
+
+
+ENDS = [  # the first and the last of the counters: 65536 columns, 1024 experts
+    (2, 65536, 64, 2, 1, 64, "bf16", "bf16", True),
+    (20, 65536, 128, 3, 2, 128, "mxfp8", "bf16", False),
+    (64, 64, 64, 1024, 16, 65536, "bf16", "bf16", False),
+]
+
+
+@pytest.mark.parametrize("T,D,I,E,k,Is,prec,sprec,tiled", ENDS)
+def test_ends_of_the_counters(T, D, I, E, k, Is, prec, sprec, tiled):
+    c, r = check(T, D, I, E, k, Is, prec, sprec, tiled)
+    # every counter is cleared again: the next call, of another shape, on the same workspace
+    other = Case(c.dev, 5, 192, 64, 30, 4, seed=1)
+    want = other.layer.few(other.x, other.w_router, other.weights)
+    other.layer.ws, other.layer.ws_bytes = c.layer.ws, c.layer.ws_bytes
+    got = other.layer.few(other.x, other.w_router, other.weights)
+    assert all(torch.equal(got[n], want[n]) for n in got)
+    assert other.layer.device_error() == 0

@@ -6,6 +6,7 @@ import ctypes
 import pytest
 import torch
 
+from mixture_experts_layer_counts_amd import MoELayer, shape_for
 from tests._gpu import need_gpu, say
 from tests.test_gpu_few import Case
 
@@ -42,3 +43,41 @@ def test_one_workspace_for_several_shapes():
         r = large.layer(large.x, large.w_router, large.weights)
         assert same(r, want_large)
     assert large.layer.device_error() == 0
+
+
+def test_graphs_of_two_shapes_on_one_workspace():
+    """Captured calls of two shapes, replayed in turn in stream order on one workspace, beside eager ones."""
+    dev = need_gpu()
+    a, b = Case(dev, 3, 512, 192, 40, 4, seed=8), Case(dev, 33, 384, 128, 24, 3, seed=9)
+    ws = torch.zeros(max(a.layer.ws_bytes, b.layer.ws_bytes), dtype=torch.uint8, device=dev)
+    for c in (a, b):
+        c.layer.ws, c.layer.ws_bytes = ws, ws.numel()
+    assert a.layer.lib.moe_workspace_init(ctypes.byref(a.layer.shape), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
+                                          None) == 0
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for c in (a, b):
+        c.layer.few(c.x, c.w_router, c.weights)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(c.layer.few(c.x, c.w_router, c.weights))
+        graphs.append(g)
+    for i in range(5):
+        a.x.mul_(-1.25)
+        b.x.add_(0.125)
+        for g in graphs if i % 2 else graphs[::-1]:
+            g.replay()
+        want = [c.layer.few(c.x, c.w_router, c.weights) for c in (a, b)]
+        torch.cuda.synchronize()
+        assert same(got[0], want[0]) and same(got[1], want[1])
+    assert a.layer.device_error() == 0
+
+
+def test_block_of_no_rows():
+    dev = need_gpu()
+    layer = MoELayer(shape_for(0, 128, 64, 8, 2), device=dev)
+    c = Case(dev, 2, 128, 64, 8, 2)
+    w = torch.ones(128, dtype=torch.bfloat16, device=dev)
+    r = layer.block(c.x[:0], c.w_router, c.weights, w, post_weight=w, next_weight=w)
+    assert r["z"].shape == (0, 128) and r["h_next"].shape == (0, 128) and r["out"].shape == (0, 128)
